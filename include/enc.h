@@ -428,6 +428,109 @@ ENC_API enc_status enc_op_ffn1(enc_t h, int layer, const void* h1, void* u, int 
 ENC_API enc_status enc_op_ffn2_ln(enc_t h, int layer, const void* u, const void* resid, void* out, int tokens,
                                   enc_stream_t stream);
 
+/* ------------------------------------------------------------------------------
+ * Attention with modified scores.  The source pages describe plain masked
+ * attention only; these calls serve encoders of the same layer structure whose
+ * attention has a tanh cap on its scores, a bias that depends on the distance
+ * (fixed slopes, or a learned table of relative position buckets), a document
+ * mask for rows that hold several texts, or a causal mask with a bidirectional
+ * prefix.  For sequence b with n = clamp(valid_len[b], 0, seq), head h, query
+ * position i and key position j:
+ *   u = scale q_i . k_j;  with cap > 0: u = cap tanh(u / cap)
+ *   t = u - slopes[h] |j - i| + bias_table[bucket(j - i)][h]
+ *   key j is visible to query i where i < n, j < n, (not causal, or j <= i, or
+ *   j < prefix_len[b]), and doc_ids[b][i] == doc_ids[b][j];
+ *   ctx_i = sum over the visible keys of softmax_j(t) v_j,
+ *   lse_i = log(sum over the visible keys of exp(t)).
+ * A row that sees no key, and every row i >= n, has ctx = 0 and lse = -infinity.
+ * (enc_op_attention without enc_set_scores computes rows i >= n like the others.)
+ * What q, k, v and dctx hold in rows i >= n is never used.
+ *
+ * bucket(r) of a relative position r = j - i, with num_buckets and max_distance:
+ *   bidirectional: m = num_buckets / 2, a = |r|, and m is added for r > 0;
+ *   else:          m = num_buckets, a = max(-r, 0);
+ *   e = floor(m / 2); a < e gives a, larger distances give
+ *   min(m - 1, e + floor(log(a / e) / log(max_distance / e) * (m - e) + 1e-9)).
+ * ---------------------------------------------------------------------------- */
+typedef struct {
+  float scale;                /* of q . k; 0 = 1/sqrt(size_per_head) */
+  float cap;                  /* 0 = none; else > 0 */
+  const float* slopes;        /* device [head_num], or NULL */
+  const float* bias_table;    /* device [num_buckets, head_num], FP32 in both modes, or NULL */
+  int num_buckets;            /* with a table: 2..128; bidirectional: even, >= 4 */
+  int max_distance;           /* with a table: above e, at most 2048 */
+  int bidirectional;
+  int causal;
+  const int32_t* prefix_len;  /* device [batch], or NULL = 0; needs causal */
+  const int32_t* doc_ids;     /* device [batch, seq], or NULL = one document */
+} enc_scores;
+
+/* enc_set_scores - run the attention of every later forward of this encoder
+ * handle (enc_forward, enc_forward_noalloc, enc_forward_host and _async,
+ * enc_graph_create) and of enc_op_attention with these scores; NULL restores
+ * plain attention.  The struct is copied; the device arrays that it names are
+ * read when the kernels run, so the caller keeps them alive and may rewrite
+ * their contents between forwards on the same stream.  prefix_len and doc_ids
+ * must fit the batch and seq of the forwards (device memory, for the host entry
+ * points too).  Host-side.  A recorded forward keeps the scores it recorded.
+ * Output rows i >= n of the stack are not meaningful, as without scores.
+ * Padding removal (enc_set_packing) has no such attention: a forward with both
+ * returns ENC_ERR_UNSUPPORTED.  The single-launch forward (ENC_OPT_PERSISTENT)
+ * is not taken, and enc_forward_host does not cut the batch into chunks. */
+ENC_API enc_status enc_set_scores(enc_t h, const enc_scores* scores);
+
+/* enc_reserve_scored - grow the scratch of the three calls below now
+ * (synchronous) to hold any of them at batch x seq (seq = capacity for the
+ * step).  Without it a call grows the scratch itself (cudaMalloc), except while
+ * `stream` is being captured: then ENC_ERR_INVALID_ARG.  Scratch that was ever
+ * handed to a call stays allocated until enc_destroy, so that a graph captured
+ * by the caller keeps valid addresses when the scratch grows later. */
+ENC_API enc_status enc_reserve_scored(enc_t h, int batch, int seq);
+
+/* enc_op_scored_attention - one attention step with these scores:
+ *   qkv [3, batch, head_num, seq, d] (what enc_op_qkv writes); valid_len device
+ *   int32 [batch]; ctx [batch * seq, H]; lse device FP32 [batch, head_num, seq]
+ *   (natural logarithm), or NULL.  seq <= 65536.  qkv and ctx 16-byte aligned.
+ * Accumulation, softmax and lse in FP32; FP16 mode rounds the unnormalised
+ * probabilities to FP16 before the product with V, as enc_op_attention does.
+ * Asynchronous. */
+ENC_API enc_status enc_op_scored_attention(enc_t h, const enc_scores* scores, const void* qkv,
+                                           const int32_t* valid_len, void* ctx, float* lse, int batch, int seq,
+                                           enc_stream_t stream);
+
+/* enc_op_scored_attention_backward - gradients of that step.  qkv, valid_len
+ * and scores as in the forward, ctx and lse its outputs, dctx [batch * seq, H]
+ * the gradient of ctx:
+ *   P = exp(t - lse), D_i = dctx_i . ctx_i, dT = P (dctx_i . v_j - D_i),
+ *   dU = dT (1 - (u / cap)^2) (dT without a cap),
+ *   dqkv [3, batch, head_num, seq, d]: dq_i = scale sum_j dU k_j,
+ *     dk_j = scale sum_i dU q_i, dv_j = sum_i P dctx_i; rows i >= n are zeros;
+ *   dtable FP32 [num_buckets, head_num], or NULL: the sum of dT over the batch
+ *     and every (i, j) of the bucket (overwritten, not added to).
+ * The same result on every run (no atomic additions).  FP16 mode accumulates in
+ * FP32 and rounds P and dU to FP16 for the products; dU is scaled by a power of
+ * two per (sequence, head) first, taken from the norms of dctx and v, so that
+ * neither small nor large gradients leave FP16's range.  dqkv may not overlap
+ * qkv, ctx or dctx.  Asynchronous. */
+ENC_API enc_status enc_op_scored_attention_backward(enc_t h, const enc_scores* scores, const void* qkv,
+                                                    const int32_t* valid_len, const void* ctx, const float* lse,
+                                                    const void* dctx, void* dqkv, float* dtable, int batch, int seq,
+                                                    enc_stream_t stream);
+
+/* enc_op_scored_attention_step - attention of one new token per sequence over a
+ * key/value cache, for incremental use of the single steps:
+ *   qkv [3, batch, head_num, 1, d] (enc_op_qkv at seq 1); cache
+ *   [2, batch, head_num, capacity, d] (keys, then values); len device int32
+ *   [batch], the tokens that the cache holds already; ctx [batch, H].
+ * The token's key and value are stored at position p = len[b], and its query
+ * attends to positions 0..p (whatever causal and prefix_len say); doc_ids is
+ * [batch, capacity] and holds p's document too.  len is not changed.  A sequence
+ * with len[b] outside [0, capacity) gets ctx = 0 and an unchanged cache.  Every
+ * other part of the cache stays as it is.  Asynchronous. */
+ENC_API enc_status enc_op_scored_attention_step(enc_t h, const enc_scores* scores, const void* qkv, void* cache,
+                                                const int32_t* len, void* ctx, int batch, int capacity,
+                                                enc_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -60,6 +60,11 @@ SIGNATURES = {
     "enc_op_out_proj_ln": (_i, [_vp, _i, _vp, _vp, _vp, _i, _vp]),
     "enc_op_ffn1": (_i, [_vp, _i, _vp, _vp, _i, _vp]),
     "enc_op_ffn2_ln": (_i, [_vp, _i, _vp, _vp, _vp, _i, _vp]),
+    "enc_set_scores": (_i, [_vp, _vp]),
+    "enc_reserve_scored": (_i, [_vp, _i, _i]),
+    "enc_op_scored_attention": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp]),
+    "enc_op_scored_attention_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp]),
+    "enc_op_scored_attention_step": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp]),
 }
 
 
@@ -74,6 +79,43 @@ DECODER_WEIGHT_FIELDS = ("w_qkv", "b_qkv", "w_o", "b_o", "ln1_g", "ln1_b", "w_q2
 
 class EncDecoderLayerWeights(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in DECODER_WEIGHT_FIELDS]
+
+
+class EncScores(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("cap", ctypes.c_float), ("slopes", _vp), ("bias_table", _vp),
+                ("num_buckets", _i), ("max_distance", _i), ("bidirectional", _i), ("causal", _i), ("prefix_len", _vp),
+                ("doc_ids", _vp)]
+
+
+class Scores:
+    """How attention modifies its scores (enc_scores in include/enc.h): a scale (None =
+    1/sqrt(size_per_head)), a tanh cap (0 = none), slopes [head_num] of a linear distance
+    bias, a table [num_buckets, head_num] of relative position biases, a causal mask with
+    prefix_len [batch], doc_ids [batch, seq].  slopes and table are CUDA float32 tensors,
+    prefix_len and doc_ids CUDA int32 tensors; they are kept alive by this object."""
+
+    def __init__(self, scale: Optional[float] = None, cap: float = 0.0, slopes=None, table=None,
+                 max_distance: int = 128, bidirectional: bool = True, causal: bool = False, prefix_len=None,
+                 doc_ids=None):
+        self.slopes, self.table, self.prefix_len, self.doc_ids = slopes, table, prefix_len, doc_ids
+        self.c = EncScores(scale=0.0 if scale is None else scale, cap=cap, slopes=_typed_ptr(slopes, "float32", 1),
+                           bias_table=_typed_ptr(table, "float32", 2),
+                           num_buckets=0 if table is None else table.shape[0],
+                           max_distance=0 if table is None else max_distance, bidirectional=int(bidirectional),
+                           causal=int(causal), prefix_len=_typed_ptr(prefix_len, "int32", 1),
+                           doc_ids=_typed_ptr(doc_ids, "int32", 2))
+
+    def check(self, head_num: int, batch: Optional[int] = None, seq: Optional[int] = None):
+        """Raise ValueError where a tensor does not fit head_num, batch or seq (the C ABI cannot see sizes)."""
+        for name, t, want in (("slopes", self.slopes, (head_num,)),
+                              ("table", self.table, (self.c.num_buckets, head_num)),
+                              ("prefix_len", self.prefix_len, (batch,)), ("doc_ids", self.doc_ids, (batch, seq))):
+            if t is not None and any(w is not None and w != n for w, n in zip(want, t.shape)):
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {want}")
+
+    @property
+    def pointer(self):
+        return ctypes.cast(ctypes.pointer(self.c), ctypes.c_void_p)
 
 
 class EncError(RuntimeError):
@@ -121,6 +163,24 @@ def _dptr(t, dtype_np=None) -> int:
     if not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
     return t.data_ptr()
+
+
+def _typed_ptr(t, dtype: str, dim: int) -> Optional[int]:
+    """Device pointer of a contiguous CUDA tensor of that dtype and rank (None for None)."""
+    if t is None:
+        return None
+    p = _dptr(t)
+    if str(t.dtype) != f"torch.{dtype}" or t.dim() != dim:
+        raise ValueError(f"expected a {dim}-dimensional {dtype} tensor, got {tuple(t.shape)} {t.dtype}")
+    return p
+
+
+def _shaped_ptr(t, dtype: str, numel: int) -> int:
+    """Device pointer of a contiguous CUDA tensor of that dtype and element count."""
+    p = _dptr(t)
+    if str(t.dtype) != f"torch.{dtype}" or t.numel() != numel:
+        raise ValueError(f"expected {numel} elements of {dtype}, got {tuple(t.shape)} {t.dtype}")
+    return p
 
 
 class Encoder:
@@ -306,6 +366,54 @@ class Encoder:
         """out = LN2(u W2 + b2 + resid)."""
         _check(self.lib.enc_op_ffn2_ln(self.handle, layer, _dptr(u), _dptr(resid), _dptr(out), tokens,
                                        _current_stream(stream)))
+
+    # -------------------------------------------------------------- attention with modified scores
+    def _act(self) -> str:
+        return "float16" if self.dtype == "fp16" else "float32"
+
+    def set_scores(self, scores: Optional["Scores"]):
+        """Run the attention of every later forward (and of op_attention) with these scores; None = plain."""
+        if scores is not None:
+            scores.check(self.head_num)
+        _check(self.lib.enc_set_scores(self.handle, None if scores is None else scores.pointer))
+        self._scores_keep = scores
+
+    def reserve_scored(self, batch: int, seq: int):
+        """Grow the scratch of the op_scored_* calls now (see enc_reserve_scored)."""
+        _check(self.lib.enc_reserve_scored(self.handle, batch, seq))
+
+    def op_scored_attention(self, scores: "Scores", qkv, valid_len, ctx, batch: int, seq: int, lse=None, stream=None):
+        """ctx (and lse [batch, head_num, seq], float32) of qkv [3, batch, head_num, seq, d]."""
+        scores.check(self.head_num, batch, seq)
+        m = batch * seq * self.hidden
+        _check(self.lib.enc_op_scored_attention(
+            self.handle, scores.pointer, _shaped_ptr(qkv, self._act(), 3 * m), _shaped_ptr(valid_len, "int32", batch),
+            _shaped_ptr(ctx, self._act(), m),
+            None if lse is None else _shaped_ptr(lse, "float32", batch * seq * self.head_num), batch, seq,
+            _current_stream(stream)))
+
+    def op_scored_attention_backward(self, scores: "Scores", qkv, valid_len, ctx, lse, dctx, dqkv, batch: int, seq: int,
+                                     dtable=None, stream=None):
+        """dqkv (and dtable [num_buckets, head_num], float32) from the forward's ctx and lse and from dctx."""
+        scores.check(self.head_num, batch, seq)
+        m = batch * seq * self.hidden
+        _check(self.lib.enc_op_scored_attention_backward(
+            self.handle, scores.pointer, _shaped_ptr(qkv, self._act(), 3 * m), _shaped_ptr(valid_len, "int32", batch),
+            _shaped_ptr(ctx, self._act(), m), _shaped_ptr(lse, "float32", batch * seq * self.head_num),
+            _shaped_ptr(dctx, self._act(), m), _shaped_ptr(dqkv, self._act(), 3 * m),
+            None if dtable is None else _shaped_ptr(dtable, "float32", scores.c.num_buckets * self.head_num), batch, seq,
+            _current_stream(stream)))
+
+    def op_scored_attention_step(self, scores: "Scores", qkv, cache, length, ctx, batch: int, capacity: int,
+                                 stream=None):
+        """ctx [batch, hidden] of one new token per sequence; its key and value go into cache
+        [2, batch, head_num, capacity, d] at position length[b]."""
+        scores.check(self.head_num, batch, capacity)
+        m = batch * self.hidden
+        _check(self.lib.enc_op_scored_attention_step(
+            self.handle, scores.pointer, _shaped_ptr(qkv, self._act(), 3 * m),
+            _shaped_ptr(cache, self._act(), 2 * m * capacity), _shaped_ptr(length, "int32", batch),
+            _shaped_ptr(ctx, self._act(), m), batch, capacity, _current_stream(stream)))
 
 
 class Decoder:

@@ -16,6 +16,7 @@
 #include <cstdio>
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -144,6 +145,11 @@ struct enc_handle {
   CUtensorMap* d_wmaps = nullptr;           // device [L][4] weight maps of the single-launch forward
   void* persist_partial = nullptr;          // its FFN2 partial tiles and tile counters
   std::vector<cudaEvent_t> trace;   // optional per-kernel events for enc_forward
+  bool scored = false;              // enc_set_scores: the forwards' attention has modified scores
+  enc::ScoreArgs scores;
+  void* scored_ws = nullptr;        // scratch of the enc_op_scored_* calls
+  size_t scored_ws_bytes = 0;
+  std::vector<void*> scored_retired;   // smaller scratch that captured graphs may still name
   bool decoder = false;             // created by enc_decoder_create (its layers in dlayers)
   std::vector<struct DecLayerDev> dlayers;
 };
@@ -302,8 +308,19 @@ bool use_tc_attention(const enc_handle* h, int seq) {
   return enc::attention_tc_supported(h->d, seq) && h->tc_attn;
 }
 
+// Attention with modified scores (scored.cuh).
+enc_status step_scored(enc_handle* h, const enc::ScoreArgs& s, const void* qkv, const int32_t* vl, void* ctx,
+                       float* lse, int batch, int seq, cudaStream_t st) {
+  const enc::ScoredShape sh{batch, seq, h->nh, h->d};
+  cudaError_t e = enc::launch_scored_simt(s, qkv, vl, ctx, lse, sh, h->dtype == ENC_FP16, st);
+  if (e != cudaSuccess) return cuda_fail(e, "scored attention launch");
+  ++h->launches;
+  return ENC_OK;
+}
+
 enc_status step_attention(enc_handle* h, const void* qkv, const int32_t* vl, void* ctx, int batch, int seq,
                           cudaStream_t st) {
+  if (h->scored) return step_scored(h, h->scores, qkv, vl, ctx, nullptr, batch, seq, st);
   cudaError_t e;
   if (h->dtype == ENC_FP16 && use_tc_attention(h, seq))
     e = enc::launch_attention_tc(static_cast<const __half*>(qkv), vl, nullptr, static_cast<__half*>(ctx), batch, seq,
@@ -358,7 +375,7 @@ bool ln_fused(const enc_handle* h, int tokens, int which) {
 // The single-launch forward (persistent.cu): FP16, padding kept, few enough
 // tokens that every GEMM is a weight stream.
 bool use_persistent(const enc_handle* h, int batch, int seq) {
-  return h->dtype == ENC_FP16 && !h->packed && h->persistent && h->persist_partial && h->d_wmaps &&
+  return h->dtype == ENC_FP16 && !h->packed && !h->scored && h->persistent && h->persist_partial && h->d_wmaps &&
          enc::persistent_supported(batch, seq, h->nh, h->d, h->F, h->num_sms);
 }
 
@@ -470,8 +487,99 @@ enc_status check_ptrs(std::initializer_list<const void*> ps) {
   return ENC_OK;
 }
 
+// A forward whose attention has modified scores.
+enc_status check_scored_forward(const enc_handle* h, int seq) {
+  if (!h->scored) return ENC_OK;
+  if (h->packed) return fail(ENC_ERR_UNSUPPORTED, "padding removal has no attention with modified scores");
+  if (seq > enc::kMaxScoreSeq)
+    return fail(ENC_ERR_UNSUPPORTED, "seq %d exceeds %d with modified scores", seq, enc::kMaxScoreSeq);
+  return ENC_OK;
+}
+
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
+// Checks an enc_scores and lays it out for the kernels.
+enc_status make_scores(const enc_handle* h, const enc_scores* p, enc::ScoreArgs& s) {
+  if (!p) return fail(ENC_ERR_INVALID_ARG, "scores is null");
+  if (!std::isfinite(p->scale)) return fail(ENC_ERR_INVALID_ARG, "scale is not finite");
+  if (!std::isfinite(p->cap) || p->cap < 0.f) return fail(ENC_ERR_INVALID_ARG, "cap must be finite and >= 0");
+  s.scale = p->scale == 0.f ? 1.f / sqrtf((float)h->d) : p->scale;
+  s.cap = p->cap;
+  s.slopes = p->slopes;
+  s.table = p->bias_table;
+  s.causal = p->causal != 0;
+  s.prefix = p->prefix_len;
+  s.docs = p->doc_ids;
+  if (p->prefix_len && !p->causal) return fail(ENC_ERR_INVALID_ARG, "prefix_len needs causal");
+  if (!p->bias_table) return ENC_OK;
+  const bool both = p->bidirectional != 0;
+  if (p->num_buckets < (both ? 4 : 2) || p->num_buckets > enc::kMaxScoreBuckets || (both && p->num_buckets % 2))
+    return fail(ENC_ERR_INVALID_ARG, "num_buckets %d: 2..%d, and even and >= 4 when bidirectional", p->num_buckets,
+                enc::kMaxScoreBuckets);
+  const int m = both ? p->num_buckets / 2 : p->num_buckets, e = m / 2;
+  if (p->max_distance <= e || p->max_distance > enc::kMaxScoreDistance)
+    return fail(ENC_ERR_INVALID_ARG, "max_distance %d: above %d and at most %d", p->max_distance, e,
+                enc::kMaxScoreDistance);
+  s.buckets = p->num_buckets;
+  s.distance = p->max_distance;
+  s.both = both;
+  // bounds[k - 1]: the first distance whose logarithmic bucket is at least k
+  // (k = 1 .. m - e - 1), found next to e (max_distance / e)^(k / (m - e)).
+  const double ratio = log((double)p->max_distance / e);
+  auto bucket = [&](int a) { return (int)floor(log((double)a / e) / ratio * (m - e) + 1e-9); };
+  s.num_bounds = 0;
+  for (int k = 1; k < m - e; ++k) {
+    int a = std::max(e, (int)(e * exp(ratio * k / (m - e))) - 1);
+    while (bucket(a) < k) ++a;
+    while (a > e && bucket(a - 1) >= k) --a;
+    s.bounds[s.num_bounds++] = a;
+  }
+  return ENC_OK;
+}
+
+// Scratch of the backward pass: the row sums D, then each query block's sums
+// of the table's gradient (for the smallest block and the largest table).
+size_t scored_rowsum_bytes(const enc_handle* h, int batch, int seq) {
+  return align_up((size_t)batch * seq * h->nh * 4, 256);
+}
+size_t scored_ws_bytes(const enc_handle* h, int batch, int seq) {
+  const size_t blocks = ((size_t)seq + enc::kScoredSimtRows - 1) / enc::kScoredSimtRows;
+  return scored_rowsum_bytes(h, batch, seq) + (size_t)batch * h->nh * blocks * enc::kMaxScoreBuckets * 4;
+}
+
+enc_status ensure_scored_ws(enc_handle* h, int batch, int seq, bool have_stream, cudaStream_t st) {
+  const size_t need = scored_ws_bytes(h, batch, seq);
+  if (need <= h->scored_ws_bytes) return ENC_OK;
+  if (have_stream) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(st, &cap);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return cuda_fail(e, "cudaStreamIsCapturing");
+    }
+    if (cap != cudaStreamCaptureStatusNone)
+      return fail(ENC_ERR_INVALID_ARG, "%zu bytes of scratch needed while the stream is captured: call "
+                  "enc_reserve_scored first", need);
+  }
+  void* p = nullptr;
+  const size_t bytes = std::max(need, 2 * h->scored_ws_bytes);   // doubling bounds what the retired ones hold
+  if (cudaMalloc(&p, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(ENC_ERR_OOM, "scratch allocation of %zu bytes failed", bytes);
+  }
+  if (h->scored_ws) h->scored_retired.push_back(h->scored_ws);
+  h->scored_ws = p;
+  h->scored_ws_bytes = bytes;
+  return ENC_OK;
+}
+
 void free_handle(enc_handle* h) {
   if (!h) return;
+  if (h->scored_ws) cudaFree(h->scored_ws);
+  for (void* p : h->scored_retired) cudaFree(p);
   for (int i = 0; i < enc_handle::kMaxChunks; ++i) {
     if (h->ev_in[i]) cudaEventDestroy(h->ev_in[i]);
     if (h->ev_done[i]) cudaEventDestroy(h->ev_done[i]);
@@ -874,6 +982,7 @@ enc_status forward_impl(enc_handle* h, const void* x, const int32_t* valid_len, 
   if ((s = check_tokens(batch, seq)) != ENC_OK) return s;
   if ((s = check_ptrs({x, out})) != ENC_OK) return s;
   if (!valid_len) return fail(ENC_ERR_INVALID_ARG, "valid_len is null");
+  if ((s = check_scored_forward(h, seq)) != ENC_OK) return s;
   const size_t M = (size_t)batch * seq;
   const size_t bytes = M * h->H * h->esize;
   const char* xb = static_cast<const char*>(x);
@@ -1051,6 +1160,7 @@ enc_status enc_forward_noalloc(enc_t h, const void* x, const int32_t* valid_len,
   if ((s = check_tokens(batch, seq)) != ENC_OK) return s;
   if ((s = check_ptrs({x, out})) != ENC_OK) return s;
   if (!valid_len) return fail(ENC_ERR_INVALID_ARG, "valid_len is null");
+  if ((s = check_scored_forward(h, seq)) != ENC_OK) return s;
   const size_t M = (size_t)batch * seq;
   const size_t bytes = M * h->H * h->esize;
   const char* xb = static_cast<const char*>(x);
@@ -1086,6 +1196,7 @@ enc_status enc_forward_host(enc_t h, const void* x, const int32_t* valid_len, vo
   PdlScope pdl(h);
   if ((s = check_tokens(batch, seq)) != ENC_OK) return s;
   if (!x || !valid_len || !out) return fail(ENC_ERR_INVALID_ARG, "null host buffer");
+  if ((s = check_scored_forward(h, seq)) != ENC_OK) return s;
   const size_t seq_bytes = (size_t)seq * h->H * h->esize;
   const size_t act_al = align_up((size_t)batch * seq_bytes, 256);
   if ((s = host_setup(h, batch, seq)) != ENC_OK) return s;
@@ -1098,7 +1209,7 @@ enc_status enc_forward_host(enc_t h, const void* x, const int32_t* valid_len, vo
   const long tokens = (long)batch * seq;
   int chunks = (int)std::min<long>(h->host_chunks, std::max<long>(1, tokens / 2048));
   chunks = std::min(chunks, batch);
-  if (h->packed || h->L < 2) chunks = 1;
+  if (h->packed || h->scored || h->L < 2) chunks = 1;
   char* base = static_cast<char*>(h->stage);
   char* dx = base;
   char* dout = base + act_al;
@@ -1177,6 +1288,7 @@ enc_status enc_forward_host_async(enc_t h, const void* x, const int32_t* valid_l
   PdlScope pdl(h);
   if ((s = check_tokens(batch, seq)) != ENC_OK) return s;
   if (!x || !valid_len || !out) return fail(ENC_ERR_INVALID_ARG, "null host buffer");
+  if ((s = check_scored_forward(h, seq)) != ENC_OK) return s;
   if ((s = host_setup(h, batch, seq)) != ENC_OK) return s;
   const int k = h->host_slot;
   const size_t act = (size_t)batch * seq * h->H * h->esize;
@@ -1353,6 +1465,8 @@ enc_status enc_op_attention(enc_t h, const void* qkv, const int32_t* valid_len, 
   if ((s = check_tokens(batch, seq)) != ENC_OK) return s;
   if ((s = check_ptrs({qkv, ctx})) != ENC_OK) return s;
   if (!valid_len) return fail(ENC_ERR_INVALID_ARG, "valid_len is null");
+  if (h->scored && seq > enc::kMaxScoreSeq)
+    return fail(ENC_ERR_UNSUPPORTED, "seq %d exceeds %d with modified scores", seq, enc::kMaxScoreSeq);
   if ((s = step_attention(h, qkv, valid_len, ctx, batch, seq, reinterpret_cast<cudaStream_t>(stream))) != ENC_OK)
     return s;
   return ok();
@@ -1400,6 +1514,113 @@ enc_status enc_op_ffn2_ln(enc_t h, int layer, const void* u, const void* resid, 
   const Workspace w = carve(h, (size_t)tokens);
   if ((s = step_ffn2(h, layer, u, resid, w.a, tokens, st)) != ENC_OK) return s;
   if ((s = step_ln(h, layer, 2, w.a, out, tokens, st)) != ENC_OK) return s;
+  return ok();
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ attention with modified scores
+
+static enc_status scored_prologue(enc_t h, const enc_scores* scores, int batch, int seq, enc::ScoreArgs& s) {
+  enc_status st = op_prologue(h, 0, false, 1);
+  if (st != ENC_OK) return st;
+  if ((st = check_tokens(batch, seq)) != ENC_OK) return st;
+  if (seq > enc::kMaxScoreSeq) return fail(ENC_ERR_UNSUPPORTED, "seq %d exceeds %d", seq, enc::kMaxScoreSeq);
+  return make_scores(h, scores, s);
+}
+
+extern "C" {
+
+enc_status enc_set_scores(enc_t h, const enc_scores* scores) {
+  if (!h) return fail(ENC_ERR_INVALID_ARG, "null handle");
+  if (h->decoder) return fail(ENC_ERR_INVALID_ARG, "modified scores need an encoder handle");
+  enc::ScoreArgs s;
+  if (scores) {
+    enc_status st = make_scores(h, scores, s);
+    if (st != ENC_OK) return st;
+  }
+  h->scored = scores != nullptr;
+  h->scores = s;
+  return ok();
+}
+
+enc_status enc_reserve_scored(enc_t h, int batch, int seq) {
+  enc_status s = op_prologue(h, 0, false, 1);
+  if (s != ENC_OK) return s;
+  if ((s = check_tokens(batch, seq)) != ENC_OK) return s;
+  if (seq > enc::kMaxScoreSeq) return fail(ENC_ERR_UNSUPPORTED, "seq %d exceeds %d", seq, enc::kMaxScoreSeq);
+  if ((s = ensure_scored_ws(h, batch, seq, false, nullptr)) != ENC_OK) return s;
+  return ok();
+}
+
+enc_status enc_op_scored_attention(enc_t h, const enc_scores* scores, const void* qkv, const int32_t* valid_len,
+                                   void* ctx, float* lse, int batch, int seq, enc_stream_t stream) {
+  enc::ScoreArgs a;
+  enc_status s = scored_prologue(h, scores, batch, seq, a);
+  if (s != ENC_OK) return s;
+  PdlScope pdl(h);
+  if ((s = check_ptrs({qkv, ctx})) != ENC_OK) return s;
+  if (!valid_len) return fail(ENC_ERR_INVALID_ARG, "valid_len is null");
+  const size_t act = (size_t)batch * seq * h->H * h->esize;
+  if (overlap(ctx, act, qkv, 3 * act)) return fail(ENC_ERR_INVALID_ARG, "ctx overlaps qkv");
+  if ((s = step_scored(h, a, qkv, valid_len, ctx, lse, batch, seq, reinterpret_cast<cudaStream_t>(stream))) != ENC_OK)
+    return s;
+  return ok();
+}
+
+enc_status enc_op_scored_attention_backward(enc_t h, const enc_scores* scores, const void* qkv,
+                                            const int32_t* valid_len, const void* ctx, const float* lse,
+                                            const void* dctx, void* dqkv, float* dtable, int batch, int seq,
+                                            enc_stream_t stream) {
+  enc::ScoreArgs a;
+  enc_status s = scored_prologue(h, scores, batch, seq, a);
+  if (s != ENC_OK) return s;
+  PdlScope pdl(h);
+  if ((s = check_ptrs({qkv, ctx, dctx, dqkv})) != ENC_OK) return s;
+  if (!valid_len || !lse) return fail(ENC_ERR_INVALID_ARG, "valid_len or lse is null");
+  if (dtable && !a.table) return fail(ENC_ERR_INVALID_ARG, "dtable without a bias_table");
+  const size_t act = (size_t)batch * seq * h->H * h->esize;
+  if (overlap(dqkv, 3 * act, qkv, 3 * act) || overlap(dqkv, 3 * act, ctx, act) || overlap(dqkv, 3 * act, dctx, act))
+    return fail(ENC_ERR_INVALID_ARG, "dqkv overlaps an input");
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if ((s = ensure_scored_ws(h, batch, seq, true, st)) != ENC_OK) return s;
+  float* rowsum = static_cast<float*>(h->scored_ws);
+  float* partial =
+      dtable ? reinterpret_cast<float*>(static_cast<char*>(h->scored_ws) + scored_rowsum_bytes(h, batch, seq)) : nullptr;
+  const enc::ScoredShape sh{batch, seq, h->nh, h->d};
+  const bool half = h->dtype == ENC_FP16;
+  cudaError_t e = enc::launch_scored_rowsum(ctx, dctx, valid_len, rowsum, sh, half, st);
+  if (e != cudaSuccess) return cuda_fail(e, "scored attention row sums launch");
+  ++h->launches;
+  e = enc::launch_scored_backward_simt(a, qkv, valid_len, dctx, lse, rowsum, dqkv, partial, sh, half, st);
+  if (e != cudaSuccess) return cuda_fail(e, "scored attention backward launch");
+  h->launches += 2;
+  const int blocks = (seq + enc::kScoredSimtRows - 1) / enc::kScoredSimtRows;
+  if (dtable) {
+    e = enc::launch_scored_table_grad(partial, dtable, batch, blocks, a.buckets, h->nh, st);
+    if (e != cudaSuccess) return cuda_fail(e, "table gradient launch");
+    ++h->launches;
+  }
+  return ok();
+}
+
+enc_status enc_op_scored_attention_step(enc_t h, const enc_scores* scores, const void* qkv, void* cache,
+                                        const int32_t* len, void* ctx, int batch, int capacity, enc_stream_t stream) {
+  enc::ScoreArgs a;
+  enc_status s = scored_prologue(h, scores, batch, capacity, a);
+  if (s != ENC_OK) return s;
+  PdlScope pdl(h);
+  if ((s = check_ptrs({qkv, cache, ctx})) != ENC_OK) return s;
+  if (!len) return fail(ENC_ERR_INVALID_ARG, "len is null");
+  const size_t act = (size_t)batch * h->H * h->esize;
+  if (overlap(ctx, act, qkv, 3 * act) || overlap(cache, 2 * act * capacity, qkv, 3 * act) ||
+      overlap(cache, 2 * act * capacity, ctx, act))
+    return fail(ENC_ERR_INVALID_ARG, "qkv, cache and ctx overlap");
+  const enc::ScoredShape sh{batch, capacity, h->nh, h->d};
+  cudaError_t e = enc::launch_scored_step(a, qkv, cache, len, ctx, sh, h->dtype == ENC_FP16, h->num_sms,
+                                          reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "scored attention step launch");
+  ++h->launches;
   return ok();
 }
 

@@ -209,6 +209,47 @@ bool persistent_supported(int B, int S, int NH, int D, int F, int num_sms);
 size_t persistent_partial_bytes(int H, int F);
 cudaError_t launch_persistent(const PersistArgs& args, cudaStream_t stream);
 
+// ---- attention with modified scores (scored.cuh has the formulas) ----
+constexpr int kMaxScoreBuckets = 128;
+constexpr int kMaxScoreDistance = 2048;
+constexpr int kMaxScoreSeq = 65536;
+struct ScoreArgs {
+  float scale = 0.f;                // of q . k
+  float cap = 0.f;                  // 0: no cap
+  const float* slopes = nullptr;    // [nh] or nullptr
+  const float* table = nullptr;     // [buckets, nh] or nullptr
+  int buckets = 0, distance = 0, both = 0;
+  int causal = 0;
+  const int32_t* prefix = nullptr;  // [B] or nullptr
+  const int32_t* docs = nullptr;    // [B, S] or nullptr
+  // Distances from which the logarithmic buckets 1, 2, ... past the exact ones start.
+  int num_bounds = 0;
+  int bounds[kMaxScoreBuckets / 2] = {};
+};
+struct ScoredShape {
+  int batch, seq, head_num, size_per_head;
+};
+// Forward: qkv [3, B, nh, S, d] -> ctx [B*S, nh*d], and lse [B, nh, S] unless nullptr.
+// Rows that see no key (rows i >= n among them): ctx = 0, lse = -inf.
+cudaError_t launch_scored_simt(const ScoreArgs& s, const void* qkv, const int32_t* valid_len, void* ctx, float* lse,
+                               const ScoredShape& sh, bool half, cudaStream_t stream);
+// Row sums D_i = dctx_i . ctx_i (0 for i >= n) -> rowsum [B, nh, S].
+cudaError_t launch_scored_rowsum(const void* ctx, const void* dctx, const int32_t* valid_len, float* rowsum,
+                                 const ScoredShape& sh, bool half, cudaStream_t stream);
+// Backward: dqkv [3, B, nh, S, d]; partial [B, nh, ceil(S / rows of a block), buckets] gets each query
+// block's sums of the table's gradient (nullptr: no table gradient).
+constexpr int kScoredSimtRows = 64;
+cudaError_t launch_scored_backward_simt(const ScoreArgs& s, const void* qkv, const int32_t* valid_len,
+                                        const void* dctx, const float* lse, const float* rowsum, void* dqkv,
+                                        float* partial, const ScoredShape& sh, bool half, cudaStream_t stream);
+// One new token per sequence: qkv [3, B, nh, 1, d], cache [2, B, nh, capacity, d] (sh.seq = capacity),
+// position len[b]; ctx [B, nh*d].  docs is [B, capacity].
+cudaError_t launch_scored_step(const ScoreArgs& s, const void* qkv, void* cache, const int32_t* len, void* ctx,
+                               const ScoredShape& sh, bool half, int num_sms, cudaStream_t stream);
+// dtable [buckets, nh] = the partial sums added over the batch and the query blocks, in a fixed order.
+cudaError_t launch_scored_table_grad(const float* partial, float* dtable, int batch, int blocks, int buckets,
+                                     int head_num, cudaStream_t stream);
+
 // ---- weight repack, encoder.cu ----
 int device_sm_count();
 

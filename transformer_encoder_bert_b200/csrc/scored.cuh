@@ -1,0 +1,68 @@
+// Attention with modified scores: what its kernels share.
+//
+// For query position i and key position j of one sequence (n valid positions)
+// and head h, with s = q_i . k_j:
+//   u = scale * s;  with a cap: u = cap * tanh(u / cap)
+//   t = u - slopes[h] * |j - i| + table[bucket(j - i)][h]
+//   j is visible to i where i, j < n, where a causal mask has j <= i or
+//   j < prefix, and where doc[i] == doc[j].
+// The causal, prefix and length masks leave each query the keys [0, jlim_i):
+// jlim_i = min(n, max(i + 1, prefix)) (n without the causal mask); and each key
+// the queries [ilow_j, n): ilow_j = j where the causal mask holds and
+// j >= prefix, else 0.  The kernels work on t in units of log2 (t2 = t log2 e),
+// so that exp is one ex2.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "internal.h"
+
+namespace enc {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Bucket of the relative position rel = key - query.
+__host__ __device__ __forceinline__ int score_bucket(const ScoreArgs& s, int rel) {
+  const int nb = s.both ? s.buckets >> 1 : s.buckets;
+  const int a = s.both ? (rel < 0 ? -rel : rel) : (rel < 0 ? -rel : 0);
+  const int exact = nb >> 1;
+  int c = a;
+  if (a >= exact) {
+    int lo = 0, hi = s.num_bounds;          // how many bounds are <= a
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s.bounds[mid] <= a) lo = mid + 1; else hi = mid;
+    }
+    c = exact + lo;
+  }
+  return c + (s.both && rel > 0 ? nb : 0);
+}
+
+// The part of t2 that depends on the distance alone.
+__device__ __forceinline__ float score_bias2(const ScoreArgs& s, int nh, int h, float slope, int rel) {
+  float b = -slope * fabsf(static_cast<float>(rel));
+  if (s.table) b += s.table[static_cast<size_t>(score_bucket(s, rel)) * nh + h];
+  return b * kLog2e;
+}
+
+__device__ __forceinline__ int score_len(const int32_t* valid_len, int b, int S) {
+  const int n = valid_len[b];
+  return n < 0 ? 0 : (n > S ? S : n);
+}
+
+__device__ __forceinline__ int score_prefix(const ScoreArgs& s, int b) { return s.prefix ? s.prefix[b] : 0; }
+
+// First key that query i does not see for its position, and first query that
+// sees key j.
+__device__ __forceinline__ int score_jlim(const ScoreArgs& s, int i, int n, int prefix) {
+  return s.causal ? min(n, max(i + 1, prefix)) : n;
+}
+__device__ __forceinline__ int score_ilow(const ScoreArgs& s, int j, int prefix) {
+  return s.causal && j >= prefix ? j : 0;
+}
+
+}  // namespace enc
