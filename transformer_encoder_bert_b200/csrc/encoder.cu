@@ -312,7 +312,11 @@ bool use_tc_attention(const enc_handle* h, int seq) {
 enc_status step_scored(enc_handle* h, const enc::ScoreArgs& s, const void* qkv, const int32_t* vl, void* ctx,
                        float* lse, int batch, int seq, cudaStream_t st) {
   const enc::ScoredShape sh{batch, seq, h->nh, h->d};
-  cudaError_t e = enc::launch_scored_simt(s, qkv, vl, ctx, lse, sh, h->dtype == ENC_FP16, st);
+  cudaError_t e;
+  if (h->dtype == ENC_FP16 && h->tc_attn)
+    e = enc::launch_scored_tc(s, static_cast<const __half*>(qkv), vl, static_cast<__half*>(ctx), lse, sh, h->status, st);
+  else
+    e = enc::launch_scored_simt(s, qkv, vl, ctx, lse, sh, h->dtype == ENC_FP16, st);
   if (e != cudaSuccess) return cuda_fail(e, "scored attention launch");
   ++h->launches;
   return ENC_OK;

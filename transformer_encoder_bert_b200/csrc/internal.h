@@ -233,6 +233,9 @@ struct ScoredShape {
 // Rows that see no key (rows i >= n among them): ctx = 0, lse = -inf.
 cudaError_t launch_scored_simt(const ScoreArgs& s, const void* qkv, const int32_t* valid_len, void* ctx, float* lse,
                                const ScoredShape& sh, bool half, cudaStream_t stream);
+// The same on the tensor cores, FP16 (scored_tc.cu).
+cudaError_t launch_scored_tc(const ScoreArgs& s, const __half* qkv, const int32_t* valid_len, __half* ctx, float* lse,
+                             const ScoredShape& sh, int* status, cudaStream_t stream);
 // Row sums D_i = dctx_i . ctx_i (0 for i >= n) -> rowsum [B, nh, S].
 cudaError_t launch_scored_rowsum(const void* ctx, const void* dctx, const int32_t* valid_len, float* rowsum,
                                  const ScoredShape& sh, bool half, cudaStream_t stream);

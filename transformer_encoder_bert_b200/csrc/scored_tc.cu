@@ -1,0 +1,515 @@
+// Forward of attention with modified scores on the 5th-generation tensor cores
+// (tcgen05 + TMEM + TMA), FP16.
+//
+// A CTA takes TILES tiles of 128 query rows of one (sequence, head) and walks
+// the blocks of BN keys that some row sees.  Warps:
+//   TILES x 4   softmax: thread r of a tile owns query row r = TMEM lane r
+//   1           one thread issues the MMAs
+//                 S = Q K^T    M = 128, N = BN, both operands in shared memory
+//                 O += P V     M = 128, N = D, K = 16 per step, P read from TMEM
+//   1           one thread issues the TMA loads (Q once; K and V through rings)
+// A softmax thread reads its whole row of S into registers and releases S, so
+// that the next block's S is computed during this block's exponentials; it
+// turns the row into t (scale, cap, bias, masks), takes the maximum, writes
+// P = 2^(t2 - m) as FP16 to its own columns of TMEM and adds up l in FP32.
+// m is a reference maximum: it moves only when a block exceeds it by 2^8, and
+// then the thread scales its row of O first.  O / l does not depend on m.
+//
+// TMEM columns: S [TILES][BN], P [TILES][BN / 2], O [TILES][D].
+//
+// Keys hidden by length, causal or prefix masks are a suffix of the row, so a
+// block past every row's limit is not visited and only blocks that a row's limit
+// cuts are masked per element.  With documents the CTA first takes the least and
+// largest id of every block: blocks whose range does not meet the rows' range
+// are not visited, and blocks that hold only the rows' one document are not
+// masked.
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
+#include "scored_tc.cuh"
+
+namespace enc {
+namespace scored_tc {
+
+namespace {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+}  // namespace
+
+bool encode_operand_map(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t planes,
+                        uint32_t box_cols, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {cols, rows, planes};
+  const cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1}, estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+constexpr float kRescaleLog2 = 8.f;                // P < 2^8 between moves of the reference maximum
+
+template <int D, int TILES, int BN>
+struct Cfg {
+  static constexpr int kSoftmaxThreads = TILES * 128;
+  // Two tiles: the other two warps are filled up to a warpgroup, whose registers the softmax warps take
+  // (a row of 128 scores lives in registers): 2 x 128 x 216 + 128 x 72 = 384 x 168.
+  static constexpr bool kSplitRegs = TILES == 2;
+  static constexpr int kThreads = kSoftmaxThreads + (kSplitRegs ? 128 : 64);
+  static constexpr int kSub = D > 64 ? D / 64 : 1;         // 64-column sub-tiles of an operand
+  static constexpr int kQBytes = kSub * 128 * 128;
+  static constexpr int kKVSub = BN * 128;
+  static constexpr int kKVBytes = kSub * kKVSub;
+  static constexpr int kStages = 3;
+  static constexpr int kK = TILES * kQBytes;
+  static constexpr int kV = kK + kStages * kKVBytes;
+  static constexpr int kBars = kV + kStages * kKVBytes;
+  // q_full, k_full, k_empty, v_full, v_empty (kStages each), s_full, s_free, p_full, o_done (TILES each), drain
+  static constexpr int kNumBars = 2 + 4 * kStages + 4 * TILES;
+  static constexpr int kSlot = kBars + kNumBars * 8;
+  static constexpr int kDocs = (kSlot + 16 + 15) / 16 * 16;            // per softmax warp: the block's documents
+  static constexpr int kLut = kDocs + TILES * 4 * BN * 4;
+  static constexpr int kS = 0, kP = TILES * BN, kO = kP + TILES * BN / 2;
+  static constexpr int kTmemUsed = kO + TILES * D;
+  static constexpr int kTmemCols = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+  static_assert(kTmemUsed <= 512, "TMEM");
+  static size_t smem(const ScoreArgs& s, int seq) {
+    return 1024 + kLut + (size_t)lut_floats(s, BN) * 4 + (s.docs ? (size_t)(seq + BN - 1) / BN : 0);
+  }
+};
+
+template <int D, int TILES, int BN>
+__global__ void __launch_bounds__(Cfg<D, TILES, BN>::kThreads, TILES == 1 ? 2 : 1)
+    scored_tc_kernel(const __grid_constant__ ScoreArgs s, const __grid_constant__ CUtensorMap tm_q,
+                     const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_ctx,
+                     const int32_t* __restrict__ valid_len, __half* __restrict__ ctx, float* __restrict__ lse, int B,
+                     int S, int NH, int* __restrict__ status) {
+  using C = Cfg<D, TILES, BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::kBars;
+  const uint32_t q_full = bar0, drain = bar0 + 8;
+  auto k_full = [&](int st) { return bar0 + 16 + 8 * st; };
+  auto k_empty = [&](int st) { return bar0 + 16 + 8 * (C::kStages + st); };
+  auto v_full = [&](int st) { return bar0 + 16 + 8 * (2 * C::kStages + st); };
+  auto v_empty = [&](int st) { return bar0 + 16 + 8 * (3 * C::kStages + st); };
+  const uint32_t tile_bars = bar0 + 16 + 32 * C::kStages;
+  auto s_full = [&](int t) { return tile_bars + 8 * t; };
+  auto s_free = [&](int t) { return tile_bars + 8 * (TILES + t); };
+  auto p_full = [&](int t) { return tile_bars + 8 * (2 * TILES + t); };
+  auto o_done = [&](int t) { return tile_bars + 8 * (3 * TILES + t); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kSlot);
+  float* lut = reinterpret_cast<float*>(smem + C::kLut);
+  uint8_t* cls = reinterpret_cast<uint8_t*>(lut + lut_floats(s, BN));   // documents: 0 skip, 1 whole, 2 mask per element
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int q0 = (gridDim.x - 1 - blockIdx.x) * (128 * TILES);          // long causal rows first
+  const int H = NH * D;
+  pdl_wait();
+  const int n = score_len(valid_len, b, S), prefix = score_prefix(s, b);
+  if (q0 >= n) {                                           // no query here: ctx = 0, lse = -inf
+    const int rows = min(128 * TILES, S - q0);
+    for (int k = tid; k < rows * (D / 8); k += C::kThreads)
+      *reinterpret_cast<uint4*>(ctx + ((size_t)b * S + q0 + k / (D / 8)) * H + h * D + (k % (D / 8)) * 8) =
+          make_uint4(0, 0, 0, 0);
+    if (lse)
+      for (int k = tid; k < rows; k += C::kThreads) lse[((size_t)b * NH + h) * S + q0 + k] = -INFINITY;
+    return;
+  }
+  // Keys that the last row of tile t sees (its blocks: [0, nb[t])).
+  int klim[TILES], nb[TILES], nbmax = 0;
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) {
+    const int first = q0 + 128 * t, last = min(first + 127, n - 1);
+    klim[t] = first < n ? score_jlim(s, last, n, prefix) : 0;
+    nb[t] = (klim[t] + BN - 1) / BN;
+    nbmax = max(nbmax, nb[t]);
+  }
+
+  if (tid == 0) {
+    for (int k = 0; k < C::kNumBars; ++k) mbar_init(bar0 + 8 * k, 1);
+    for (int t = 0; t < TILES; ++t) {
+      mbar_init(s_free(t), 4);
+      mbar_init(p_full(t), 4);
+    }
+    fence_barrier_init();
+  }
+  if (warp == TILES * 4) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  const int32_t* docs = s.docs ? s.docs + (size_t)b * S : nullptr;
+  if (docs) {                                              // one warp per block of keys
+    const int rows_end = min(q0 + 128 * TILES, n);
+    int rlo = INT32_MAX, rhi = INT32_MIN;
+    for (int k = q0 + lane; k < rows_end; k += 32) {
+      const int v = docs[k];
+      rlo = min(rlo, v);
+      rhi = max(rhi, v);
+    }
+    rlo = __reduce_min_sync(0xffffffffu, rlo);
+    rhi = __reduce_max_sync(0xffffffffu, rhi);
+    for (int jb = warp; jb < nbmax; jb += C::kThreads / 32) {
+      int lo = INT32_MAX, hi = INT32_MIN;
+#pragma unroll
+      for (int c = 0; c < BN; c += 32) {
+        const int j = jb * BN + c + lane;
+        if (j < n) {
+          const int v = docs[j];
+          lo = min(lo, v);
+          hi = max(hi, v);
+        }
+      }
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      if (lane == 0) cls[jb] = hi < rlo || lo > rhi ? 0 : (lo == hi && rlo == rhi ? 1 : 2);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();                                           // after taking TMEM
+  auto next_block = [&](int jb) {                          // first block at or after jb that is visited
+    if (docs)
+      while (jb < nbmax && cls[jb] == 0) ++jb;
+    return jb;
+  };
+
+  bool ok = true;
+  if (warp >= TILES * 4) {
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == TILES * 4 + 1 && lane == 0) {              // TMA
+      prefetch_tmap(&tm_q);
+      prefetch_tmap(&tm_kv);
+      const int bh = b * NH + h, plane = B * NH;
+      mbar_arrive_expect_tx(q_full, TILES * C::kQBytes);
+      for (int t = 0; t < TILES; ++t)
+        for (int u = 0; u < C::kSub; ++u)
+          tma_load_3d(&tm_q, sbase + t * C::kQBytes + u * 16384, q_full, 64 * u, q0 + 128 * t, bh);
+      int it = 0;
+      for (int jb = next_block(0); jb < nbmax; jb = next_block(jb + 1), ++it) {
+        const int st = it % C::kStages;
+        const uint32_t ph = ((it / C::kStages) & 1) ^ 1;
+        if (it >= C::kStages && !(ok = mbar_wait(k_empty(st), ph, kWaitLimitNs))) break;
+        mbar_arrive_expect_tx(k_full(st), C::kKVBytes);
+        for (int u = 0; u < C::kSub; ++u)
+          tma_load_3d(&tm_kv, sbase + C::kK + st * C::kKVBytes + u * C::kKVSub, k_full(st), 64 * u, jb * BN, plane + bh);
+        if (it >= C::kStages && !(ok = mbar_wait(v_empty(st), ph, kWaitLimitNs))) {
+          mbar_wait(k_full(st), ph ^ 1, kWaitLimitNs);
+          break;
+        }
+        mbar_arrive_expect_tx(v_full(st), C::kKVBytes);
+        for (int u = 0; u < C::kSub; ++u)
+          tma_load_3d(&tm_kv, sbase + C::kV + st * C::kKVBytes + u * C::kKVSub, v_full(st), 64 * u, jb * BN,
+                      2 * plane + bh);
+      }
+      // Every load has landed before the CTA exits.
+      mbar_wait(q_full, 0, kWaitLimitNs);
+      for (int k = it > C::kStages ? it - C::kStages : 0; k < it; ++k) {
+        mbar_wait(k_full(k % C::kStages), (k / C::kStages) & 1, kWaitLimitNs);
+        mbar_wait(v_full(k % C::kStages), (k / C::kStages) & 1, kWaitLimitNs);
+      }
+    } else if (warp == TILES * 4 && lane == 0) {           // MMA
+      constexpr uint32_t idesc_s = idesc_f16_f32(128, BN);
+      constexpr uint32_t idesc_o = idesc_bmn(128, D);
+      auto issue_s = [&](int t, int st) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t u = kk / 4, o = (kk % 4) * 32;
+          mma_f16_ss(tmem + C::kS + t * BN, smem_desc_sw128(sbase + t * C::kQBytes + u * 16384 + o),
+                     smem_desc_sw128(sbase + C::kK + st * C::kKVBytes + u * C::kKVSub + o), idesc_s, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(s_full(t));
+      };
+      int jb = next_block(0);
+      ok = mbar_wait(q_full, 0, kWaitLimitNs) && mbar_wait(k_full(0), 0, kWaitLimitNs);
+      if (ok) {
+        tc_fence_after();
+        for (int t = 0; t < TILES; ++t)
+          if (jb < nb[t]) issue_s(t, 0);
+        mma_commit(k_empty(0));
+      }
+      for (int it = 0; ok && jb < nbmax; ++it) {
+        const int nxt = next_block(jb + 1), st = it % C::kStages;
+        if (nxt < nbmax) {
+          const int sn = (it + 1) % C::kStages;
+          if (!(ok = mbar_wait(k_full(sn), ((it + 1) / C::kStages) & 1, kWaitLimitNs))) break;
+          for (int t = 0; t < TILES && ok; ++t)
+            if (nxt < nb[t]) {
+              if (!(ok = mbar_wait(s_free(t), it & 1, kWaitLimitNs))) break;
+              tc_fence_after();
+              issue_s(t, sn);
+            }
+          if (!ok) break;
+          mma_commit(k_empty(sn));
+        }
+        if (!(ok = mbar_wait(v_full(st), (it / C::kStages) & 1, kWaitLimitNs))) break;
+        for (int t = 0; t < TILES && ok; ++t)
+          if (jb < nb[t]) {
+            if (!(ok = mbar_wait(p_full(t), it & 1, kWaitLimitNs))) break;
+            tc_fence_after();
+            const int ksteps = (min(BN, klim[t] - jb * BN) + 15) >> 4;
+            for (int kk = 0; kk < ksteps; ++kk)
+              mma_f16_ts(tmem + C::kO + t * D, tmem + C::kP + t * (BN / 2) + 8 * kk,
+                         desc_mn_sw128(sbase + C::kV + st * C::kKVBytes + kk * 2048, C::kKVSub), idesc_o,
+                         (it > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(o_done(t));
+          }
+        if (!ok) break;
+        mma_commit(v_empty(st));
+        jb = nxt;
+      }
+      mma_commit(drain);                                   // every MMA issued here has completed
+      mbar_wait(drain, 0, kWaitLimitNs);
+    }
+  } else {
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane;   // tile, row of the tile = TMEM lane
+    const int i = q0 + 128 * t + r;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t t_s = t_lane + C::kS + t * BN, t_p = t_lane + C::kP + t * (BN / 2), t_o = t_lane + C::kO + t * D;
+    const Bias bias = make_bias(s, lut, NH, h, BN, tid, C::kSoftmaxThreads);
+    asm volatile("bar.sync 1, %0;" ::"n"(C::kSoftmaxThreads) : "memory");
+    const Cap cap = make_cap(s);
+    const float scale2 = s.scale * kLog2e;
+    const int jlim = i < n ? score_jlim(s, i, n, prefix) : 0;
+    const int i_first = q0 + 128 * t, i_last = i_first + 127;
+    // Keys that every valid row of the tile sees (as far as length and causality go).
+    const int jall = i_first < n ? score_jlim(s, i_first, n, prefix) : 0;
+    const int doc = docs && i < n ? docs[i] : 0;
+    int* wdocs = reinterpret_cast<int*>(smem + C::kDocs) + warp * BN;
+    float m_ref = -INFINITY;
+    uint64_t sum2 = 0;                                     // two partial row sums (0.0f, 0.0f)
+    int it = 0;
+    for (int jb = next_block(0); jb < nb[t]; jb = next_block(jb + 1), ++it) {
+      const int j0 = jb * BN;
+      if (!(ok = warp_wait(s_full(t), it & 1))) break;
+      tc_fence_after();
+      uint32_t sv[BN / 32][32];
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) tmem_ld_32x32b_x32_async(t_s + 32 * c, sv[c]);
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) tmem_wait_ld(sv[c]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_free(t));
+
+      auto x = [&](int k) -> uint32_t& { return sv[k / 32][k % 32]; };
+      // t2 of the row.
+      const bool near = (s.table || s.slopes) && j0 - i_last < bias.reach && j0 + BN - 1 - i_first > -bias.reach;
+      const bool ahead = j0 - i_last >= bias.reach;
+      const float step = ahead ? -bias.slope2 : bias.slope2;
+      const float base = (ahead ? bias.right : bias.left) + step * (float)(j0 - i);
+      const float* row = bias.lut + bias.off + (j0 - i);   // read only where the block is near
+      if (cap.on) {
+#pragma unroll
+        for (int k = 0; k < BN; ++k)
+          x(k) = __float_as_uint(
+              fmaf(-2.f * cap.cap2, rcp(1.f + ex2(__uint_as_float(x(k)) * cap.in)), cap.cap2));
+        if (near) {
+#pragma unroll
+          for (int k = 0; k < BN; ++k) x(k) = __float_as_uint(__uint_as_float(x(k)) + row[k]);
+        } else if (s.table || s.slopes) {
+#pragma unroll
+          for (int k = 0; k < BN; ++k)
+            x(k) = __float_as_uint(__uint_as_float(x(k)) + fmaf((float)k, step, base));
+        }
+      } else if (near) {
+#pragma unroll
+        for (int k = 0; k < BN; ++k) x(k) = __float_as_uint(fmaf(__uint_as_float(x(k)), scale2, row[k]));
+      } else if (s.slopes) {
+#pragma unroll
+        for (int k = 0; k < BN; ++k)
+          x(k) = __float_as_uint(fmaf(__uint_as_float(x(k)), scale2, fmaf((float)k, step, base)));
+      } else {
+        const float add = s.table ? base : 0.f;
+#pragma unroll
+        for (int k = 0; k < BN; ++k) x(k) = __float_as_uint(fmaf(__uint_as_float(x(k)), scale2, add));
+      }
+      if (j0 + BN > jall) {
+        const int lim = jlim - j0;
+#pragma unroll
+        for (int k = 0; k < BN; ++k)
+          if (k >= lim) x(k) = __float_as_uint(-INFINITY);
+      }
+      if (docs && cls[jb] == 2) {
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < BN; c += 32) wdocs[c + lane] = j0 + c + lane < n ? docs[j0 + c + lane] : 0;
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < BN; k += 4) {
+          const int4 dj = *reinterpret_cast<const int4*>(wdocs + k);
+          if (dj.x != doc) x(k) = __float_as_uint(-INFINITY);
+          if (dj.y != doc) x(k + 1) = __float_as_uint(-INFINITY);
+          if (dj.z != doc) x(k + 2) = __float_as_uint(-INFINITY);
+          if (dj.w != doc) x(k + 3) = __float_as_uint(-INFINITY);
+        }
+      }
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < BN; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(x(k)));
+      const float bmax = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+
+      // P's columns are free, and O is whole, once the previous P V has completed.
+      if (it > 0 && !(ok = warp_wait(o_done(t), (it - 1) & 1))) break;
+      // Until a key has been seen m_ref is -inf, and O and l are zeros.
+      const bool moved = bmax > m_ref + kRescaleLog2;
+      if (any_warp(moved)) {
+        const float alpha = moved ? ex2(m_ref - bmax) : 1.f;
+        if (moved) m_ref = bmax;
+        if (it > 0) {
+          tc_fence_after();
+          uint32_t oa[32];
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            tmem_ld_32x32b_x32(t_o + c, oa);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) oa[k] = __float_as_uint(__uint_as_float(oa[k]) * alpha);
+            tmem_st_32x32b_x32(t_o + c, oa);
+          }
+        }
+        sum2 = f2_mul(sum2, f2_pack(alpha, alpha));
+      }
+      const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+      const uint64_t neg_m2 = f2_pack(-mu, -mu);
+#pragma unroll
+      for (int c = 0; c < BN; c += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          float t0, t1;
+          f2_unpack(f2_add(f2_pack(__uint_as_float(x(c + k)), __uint_as_float(x(c + k + 1))), neg_m2), t0, t1);
+          const float p0 = ex2(t0), p1 = ex2(t1);
+          sum2 = f2_add(sum2, f2_pack(p0, p1));
+          pk[k / 2] = half2_of(p0, p1);
+        }
+        tmem_st_32x32b_x16_async(t_p + c / 2, pk);
+      }
+      // V rows of keys in [n, n rounded up to 16) are read by P V: zeros, whatever memory holds there.
+      const int lim = n - j0, lim16 = (min(BN, klim[t] - j0) + 15) & ~15;
+      if (lim < lim16 && (warp & 3) == 0) {
+        const int st = it % C::kStages;
+        if (!(ok = warp_wait(v_full(st), (it / C::kStages) & 1))) break;
+        for (int k = lane; k < (lim16 - lim) * 8 * C::kSub; k += 32) {
+          const int u = k / ((lim16 - lim) * 8), rr = lim + k % ((lim16 - lim) * 8) / 8;
+          *reinterpret_cast<uint4*>(smem + C::kV + st * C::kKVBytes + u * C::kKVSub + rr * 128 + (k % 8) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();                          // visible to the tensor core
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(t));
+    }
+    if (ok && it > 0) ok = warp_wait(o_done(t), (it - 1) & 1);
+    if (ok && i_first < S) {
+      tc_fence_after();
+      float s0, s1;
+      f2_unpack(sum2, s0, s1);
+      const float l = s0 + s1;
+      const bool seen = it > 0 && i < n && l > 0.f;        // (rows i >= n may have been computed from anything)
+      const float inv = seen ? 1.f / l : 0.f;
+      // The row as FP16 into the Q tile (its readers, the MMAs of S, have completed), swizzled as the
+      // store's box is; then one TMA store per 64 columns of the warp's 32 rows.
+      constexpr int kCols = D < 64 ? D : 64, kRowBytes = 2 * kCols;
+      if (it == 0) mbar_wait(q_full, 0, kWaitLimitNs);     // no MMA read Q: its load must have landed
+      uint8_t* out = smem + t * C::kQBytes;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t oa[32];
+        if (it > 0) tmem_ld_32x32b_x32(t_o + c, oa);
+        uint8_t* orow = out + (c / 64) * 16384 + (warp & 3) * 32 * kRowBytes + lane * kRowBytes;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = seen ? half2_of(__uint_as_float(oa[8 * u + 2 * k]) * inv, __uint_as_float(oa[8 * u + 2 * k + 1]) * inv)
+                        : 0u;
+          const int unit = (c % 64) / 8 + u;
+          const int sw = D < 64 ? unit ^ ((lane >> 1) & 3) : unit ^ (lane & 7);
+          *reinterpret_cast<uint4*>(orow + 16 * sw) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      const int row0 = i_first + (warp & 3) * 32;
+      if (lane == 0 && row0 < S) {                         // rows at or past S are outside the map
+        for (int u = 0; u < C::kSub; ++u)
+          tma_store_3d(&tm_ctx, smem_u32(out) + u * 16384 + (warp & 3) * 32 * kRowBytes, h * D + 64 * u, row0, b);
+        bulk_commit_group();
+      }
+      if (lse && i < S) lse[((size_t)b * NH + h) * S + i] = seen ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+      if (lane == 0) bulk_wait_group_all();
+    }
+  }
+
+  if (!ok) atomicCAS(status, 0, kStatusWaitTimeout);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == TILES * 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int D, int TILES, int BN>
+cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, __half* ctx, float* lse,
+                     const ScoredShape& sh, int* status, cudaStream_t stream) {
+  using C = Cfg<D, TILES, BN>;
+  static const cudaError_t attr = cudaFuncSetAttribute(scored_tc_kernel<D, TILES, BN>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (attr != cudaSuccess) return attr;
+  const uint64_t planes = 3ull * sh.batch * sh.head_num;
+  CUtensorMap tq, tkv, tc;
+  if (!encode_operand_map(&tq, qkv, D, sh.seq, planes, 64, 128) ||
+      !encode_operand_map(&tkv, qkv, D, sh.seq, planes, 64, BN) ||
+      !encode_operand_map(&tc, ctx, (uint64_t)sh.head_num * D, sh.seq, sh.batch, D < 64 ? D : 64, 32))
+    return cudaErrorInvalidValue;
+  const dim3 grid((sh.seq + 128 * TILES - 1) / (128 * TILES), sh.head_num, sh.batch);
+  return launch_kernel(scored_tc_kernel<D, TILES, BN>, grid, dim3(C::kThreads), C::smem(s, sh.seq), stream, nullptr, 0,
+                       s, tq, tkv, tc, vl, ctx, lse, sh.batch, sh.seq, sh.head_num, status);
+}
+
+}  // namespace
+}  // namespace scored_tc
+
+cudaError_t launch_scored_tc(const ScoreArgs& s, const __half* qkv, const int32_t* valid_len, __half* ctx, float* lse,
+                             const ScoredShape& sh, int* status, cudaStream_t stream) {
+  using namespace scored_tc;
+  const bool wide = sh.seq > 128;
+  switch (sh.size_per_head) {
+    case 32:
+      return wide ? launch_d<32, 2, 128>(s, qkv, valid_len, ctx, lse, sh, status, stream)
+                  : launch_d<32, 1, 64>(s, qkv, valid_len, ctx, lse, sh, status, stream);
+    case 64:
+      return wide ? launch_d<64, 2, 128>(s, qkv, valid_len, ctx, lse, sh, status, stream)
+                  : launch_d<64, 1, 64>(s, qkv, valid_len, ctx, lse, sh, status, stream);
+    case 128:
+      return wide ? launch_d<128, 2, 64>(s, qkv, valid_len, ctx, lse, sh, status, stream)
+                  : launch_d<128, 1, 64>(s, qkv, valid_len, ctx, lse, sh, status, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace enc

@@ -1,0 +1,133 @@
+// What the tensor-core kernels of attention with modified scores share: tensor
+// maps, descriptors, and the arithmetic of a row of scores.
+#pragma once
+
+#include "scored.cuh"
+#include "sm100.cuh"
+
+namespace enc {
+namespace scored_tc {
+
+using namespace sm100;
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+// Head-split operands [*, S, d] as {d, S, planes} and merged ones [B, S, H] as
+// {H, S, B}; boxes of 64 columns (128 bytes, 128-byte swizzle).  A box over
+// heads of 32 is wider than the tensor (head-split: zeros) or reaches into the
+// next head (merged): only its first 32 columns are used.
+bool encode_operand_map(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t planes,
+                        uint32_t box_cols, uint32_t box_rows);
+
+__device__ __forceinline__ void tma_load_3d(const CUtensorMap* m, uint32_t dst, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
+// Contiguous bytes (a multiple of 16, both addresses 16-byte aligned), counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// MN-major operand, 128-byte swizzle: rows of 64 MN elements, K rows in groups
+// of 8 that are 1 KB apart; the second group of 64 MN elements `mn_bytes` on.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t mn_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(mn_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+__host__ __device__ constexpr uint32_t idesc_bmn(int m, int n) { return idesc_f16_f32(m, n) | (1u << 16); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Waits on one lane, result broadcast to the warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  int got = 0;
+  if ((threadIdx.x & 31) == 0) got = mbar_wait(bar, parity, kWaitLimitNs) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, got, 0) != 0;
+}
+__device__ __forceinline__ bool any_warp(bool p) { return __any_sync(0xffffffffu, p); }
+
+// Distance bias of a 128-row tile of positions against a block of positions.
+// The bias is a function of the distance alone, and past +-reach it is a
+// constant plus the slope's linear part.  A block that lies past the reach on
+// one side adds `base + step * column`; the others read a table in shared
+// memory that holds the bias of every distance within reach of such a block
+// (score_bias2 at index distance + off), neighbouring lanes at neighbouring
+// addresses.
+struct Bias {
+  const float* lut;     // shared memory
+  int off;              // index of distance 0
+  int reach;            // max_distance with a table, else 0
+  float slope2;         // slopes[h] log2 e
+  float right, left;    // table bias of far keys on either side, in log2 units
+};
+
+// The LUT spans distances that blocks within reach can hold: 128 rows against `block` columns.
+__host__ __device__ constexpr int lut_half(int reach, int block) { return reach + 128 + block; }
+__host__ __device__ inline int lut_floats(const ScoreArgs& s, int block) {
+  return s.table || s.slopes ? (2 * lut_half(s.table ? s.distance : 0, block) + 1 + 3) / 4 * 4 : 0;
+}
+
+// Filled by `threads` threads (t = 0 ..); a barrier must follow.
+__device__ __forceinline__ Bias make_bias(const ScoreArgs& s, float* lut, int nh, int h, int block, int t,
+                                          int threads) {
+  Bias b;
+  b.lut = lut;
+  b.reach = s.table ? s.distance : 0;
+  b.off = lut_half(b.reach, block);
+  const float slope = s.slopes ? s.slopes[h] : 0.f;
+  b.slope2 = slope * kLog2e;
+  b.right = s.table ? s.table[(size_t)score_bucket(s, s.distance) * nh + h] * kLog2e : 0.f;
+  b.left = s.table ? s.table[(size_t)score_bucket(s, -s.distance) * nh + h] * kLog2e : 0.f;
+  if (s.table || s.slopes)
+    for (int k = t; k <= 2 * b.off; k += threads) lut[k] = score_bias2(s, nh, h, slope, k - b.off);
+  return b;
+}
+
+// Constants of the cap: tanh(u / cap) = 1 - 2 r, r = 1 / (1 + 2^(s * in)),
+// t2 = cap2 - 2 cap2 r, and the derivative 1 - tanh^2 = 4 r (1 - r).  r comes
+// from ex2 and rcp approximations (relative error about 2^-22), so t is off by
+// about cap * 2^-21.
+struct Cap {
+  float in, cap2;
+  bool on;
+};
+__device__ __forceinline__ Cap make_cap(const ScoreArgs& s) {
+  Cap c;
+  c.on = s.cap > 0.f;
+  c.in = c.on ? 2.f * kLog2e * s.scale / s.cap : 0.f;
+  c.cap2 = s.cap * kLog2e;
+  return c;
+}
+
+}  // namespace scored_tc
+}  // namespace enc
