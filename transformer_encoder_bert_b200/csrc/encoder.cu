@@ -528,7 +528,6 @@ enc_status make_scores(const enc_handle* h, const enc_scores* p, enc::ScoreArgs&
     return fail(ENC_ERR_INVALID_ARG, "max_distance %d: above %d and at most %d", p->max_distance, e,
                 enc::kMaxScoreDistance);
   s.buckets = p->num_buckets;
-  s.distance = p->max_distance;
   s.both = both;
   // bounds[k - 1]: the first distance whose logarithmic bucket is at least k
   // (k = 1 .. m - e - 1), found next to e (max_distance / e)^(k / (m - e)).
@@ -541,17 +540,20 @@ enc_status make_scores(const enc_handle* h, const enc_scores* p, enc::ScoreArgs&
     while (a > e && bucket(a - 1) >= k) --a;
     s.bounds[s.num_bounds++] = a;
   }
+  s.reach = s.num_bounds ? s.bounds[s.num_bounds - 1] : e;
   return ENC_OK;
 }
 
-// Scratch of the backward pass: the row sums D, then each query block's sums
-// of the table's gradient (for the smallest block and the largest table).
-size_t scored_rowsum_bytes(const enc_handle* h, int batch, int seq) {
-  return align_up((size_t)batch * seq * h->nh * 4, 256);
+// Scratch of the backward pass: the row statistics (of either kernels), then
+// each query block's sums of the table's gradient (for the smallest block and
+// the largest table).
+size_t scored_rows_bytes(const enc_handle* h, int batch, int seq) {
+  return align_up(std::max((size_t)batch * seq * h->nh * 4,
+                           enc::scored_backward_tc_scratch(enc::ScoredShape{batch, seq, h->nh, h->d})), 256);
 }
 size_t scored_ws_bytes(const enc_handle* h, int batch, int seq) {
   const size_t blocks = ((size_t)seq + enc::kScoredSimtRows - 1) / enc::kScoredSimtRows;
-  return scored_rowsum_bytes(h, batch, seq) + (size_t)batch * h->nh * blocks * enc::kMaxScoreBuckets * 4;
+  return scored_rows_bytes(h, batch, seq) + (size_t)batch * h->nh * blocks * enc::kMaxScoreBuckets * 4;
 }
 
 enc_status ensure_scored_ws(enc_handle* h, int batch, int seq, bool have_stream, cudaStream_t st) {
@@ -1588,18 +1590,27 @@ enc_status enc_op_scored_attention_backward(enc_t h, const enc_scores* scores, c
     return fail(ENC_ERR_INVALID_ARG, "dqkv overlaps an input");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if ((s = ensure_scored_ws(h, batch, seq, true, st)) != ENC_OK) return s;
-  float* rowsum = static_cast<float*>(h->scored_ws);
   float* partial =
-      dtable ? reinterpret_cast<float*>(static_cast<char*>(h->scored_ws) + scored_rowsum_bytes(h, batch, seq)) : nullptr;
+      dtable ? reinterpret_cast<float*>(static_cast<char*>(h->scored_ws) + scored_rows_bytes(h, batch, seq)) : nullptr;
   const enc::ScoredShape sh{batch, seq, h->nh, h->d};
-  const bool half = h->dtype == ENC_FP16;
-  cudaError_t e = enc::launch_scored_rowsum(ctx, dctx, valid_len, rowsum, sh, half, st);
-  if (e != cudaSuccess) return cuda_fail(e, "scored attention row sums launch");
-  ++h->launches;
-  e = enc::launch_scored_backward_simt(a, qkv, valid_len, dctx, lse, rowsum, dqkv, partial, sh, half, st);
+  cudaError_t e;
+  int rows;                                                // of a query block of `partial`
+  if (h->dtype == ENC_FP16 && h->tc_attn) {
+    rows = enc::kScoredTcRows;
+    e = enc::launch_scored_backward_tc(a, static_cast<const __half*>(qkv), valid_len, static_cast<const __half*>(ctx),
+                                       lse, static_cast<const __half*>(dctx), static_cast<__half*>(dqkv), partial,
+                                       h->scored_ws, sh, h->status, st);
+  } else {
+    const bool half = h->dtype == ENC_FP16;
+    float* rowsum = static_cast<float*>(h->scored_ws);
+    rows = enc::kScoredSimtRows;
+    e = enc::launch_scored_rowsum(ctx, dctx, valid_len, rowsum, sh, half, st);
+    if (e == cudaSuccess)
+      e = enc::launch_scored_backward_simt(a, qkv, valid_len, dctx, lse, rowsum, dqkv, partial, sh, half, st);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "scored attention backward launch");
-  h->launches += 2;
-  const int blocks = (seq + enc::kScoredSimtRows - 1) / enc::kScoredSimtRows;
+  h->launches += 3;
+  const int blocks = (seq + rows - 1) / rows;
   if (dtable) {
     e = enc::launch_scored_table_grad(partial, dtable, batch, blocks, a.buckets, h->nh, st);
     if (e != cudaSuccess) return cuda_fail(e, "table gradient launch");

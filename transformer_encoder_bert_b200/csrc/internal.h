@@ -218,7 +218,8 @@ struct ScoreArgs {
   float cap = 0.f;                  // 0: no cap
   const float* slopes = nullptr;    // [nh] or nullptr
   const float* table = nullptr;     // [buckets, nh] or nullptr
-  int buckets = 0, distance = 0, both = 0;
+  int buckets = 0, both = 0;
+  int reach = 0;                    // first distance of the last bucket: the table's bias is constant from there on
   int causal = 0;
   const int32_t* prefix = nullptr;  // [B] or nullptr
   const int32_t* docs = nullptr;    // [B, S] or nullptr
@@ -249,6 +250,14 @@ cudaError_t launch_scored_backward_simt(const ScoreArgs& s, const void* qkv, con
 // position len[b]; ctx [B, nh*d].  docs is [B, capacity].
 cudaError_t launch_scored_step(const ScoreArgs& s, const void* qkv, void* cache, const int32_t* len, void* ctx,
                                const ScoredShape& sh, bool half, int num_sms, cudaStream_t stream);
+// The same on the tensor cores, FP16 (scored_tc_bwd.cu), the row sums included; partial has query blocks of
+// kScoredTcRows; scratch: scored_backward_tc_scratch bytes.
+constexpr int kScoredTcRows = 128;
+size_t scored_backward_tc_scratch(const ScoredShape& sh);
+cudaError_t launch_scored_backward_tc(const ScoreArgs& s, const __half* qkv, const int32_t* valid_len,
+                                      const __half* ctx, const float* lse, const __half* dctx, __half* dqkv,
+                                      float* partial, void* scratch, const ScoredShape& sh, int* status,
+                                      cudaStream_t stream);
 // dtable [buckets, nh] = the partial sums added over the batch and the query blocks, in a fixed order.
 cudaError_t launch_scored_table_grad(const float* partial, float* dtable, int batch, int blocks, int buckets,
                                      int head_num, cudaStream_t stream);

@@ -86,7 +86,7 @@ __device__ __forceinline__ bool any_warp(bool p) { return __any_sync(0xffffffffu
 struct Bias {
   const float* lut;     // shared memory
   int off;              // index of distance 0
-  int reach;            // max_distance with a table, else 0
+  int reach;            // s.reach with a table, else 0
   float slope2;         // slopes[h] log2 e
   float right, left;    // table bias of far keys on either side, in log2 units
 };
@@ -94,7 +94,7 @@ struct Bias {
 // The LUT spans distances that blocks within reach can hold: 128 rows against `block` columns.
 __host__ __device__ constexpr int lut_half(int reach, int block) { return reach + 128 + block; }
 __host__ __device__ inline int lut_floats(const ScoreArgs& s, int block) {
-  return s.table || s.slopes ? (2 * lut_half(s.table ? s.distance : 0, block) + 1 + 3) / 4 * 4 : 0;
+  return s.table || s.slopes ? (2 * lut_half(s.table ? s.reach : 0, block) + 1 + 3) / 4 * 4 : 0;
 }
 
 // Filled by `threads` threads (t = 0 ..); a barrier must follow.
@@ -102,12 +102,12 @@ __device__ __forceinline__ Bias make_bias(const ScoreArgs& s, float* lut, int nh
                                           int threads) {
   Bias b;
   b.lut = lut;
-  b.reach = s.table ? s.distance : 0;
+  b.reach = s.table ? s.reach : 0;
   b.off = lut_half(b.reach, block);
   const float slope = s.slopes ? s.slopes[h] : 0.f;
   b.slope2 = slope * kLog2e;
-  b.right = s.table ? s.table[(size_t)score_bucket(s, s.distance) * nh + h] * kLog2e : 0.f;
-  b.left = s.table ? s.table[(size_t)score_bucket(s, -s.distance) * nh + h] * kLog2e : 0.f;
+  b.right = s.table ? s.table[(size_t)score_bucket(s, s.reach) * nh + h] * kLog2e : 0.f;
+  b.left = s.table ? s.table[(size_t)score_bucket(s, -s.reach) * nh + h] * kLog2e : 0.f;
   if (s.table || s.slopes)
     for (int k = t; k <= 2 * b.off; k += threads) lut[k] = score_bias2(s, nh, h, slope, k - b.off);
   return b;

@@ -1,0 +1,707 @@
+// Backward of attention with modified scores on the 5th-generation tensor
+// cores, FP16: one kernel in two modes.
+//
+// With dT = P (dP - D), dP = dO V^T, D_i = dO_i . O_i, dU = dT (1 - tanh^2):
+//   dQ mode   rows = 128 queries, blocks of 64 keys:  dQ += dU K
+//   dKV mode  rows = 128 keys, blocks of 64 queries:  dV += P^T dO, dK += dU^T Q
+// Either mode keeps two operands of its rows in shared memory (Q and dO, or K
+// and V) and streams the two of the columns, and both form the same two score
+// tiles with the rows in TMEM lanes, so one thread owns one row:
+//   S  = A0 B0^T, dP = A1 B1^T        M = 128, N = 64, K = D, shared memory
+//   acc0 += dU B0, (dKV) acc1 += P B1   M = 128, N = D, K = 64, dU and P in TMEM
+// S and dP are computed twice (once a mode) instead of adding dQ up with
+// atomics from the dKV mode: 7 products instead of 5, but no FP32 traffic of dQ
+// through memory and the same result on every run.
+//
+// Warps: NB warpgroups of threads that own rows, taking the blocks in turn
+// (each with its own S and dP columns in TMEM), one MMA warp, one TMA warp.
+// Heads up to 64 run one warpgroup and two CTAs per SM (256 TMEM columns), so
+// that one CTA's exponentials run under the other's products; heads of 128
+// fill the TMEM with one CTA, which has two warpgroups instead.
+//
+// P and dU are rounded to FP16 for the products.  P is at most 1.  dU is scaled
+// by a power of two e per (sequence, head): |dT| <= 2 max|dO_i| max|v_j|, and e
+// puts that product of norms between 2^13 and 2^14, so that no dU leaves FP16's
+// range and small gradients keep their bits.  e is exact and is taken out of
+// the FP32 results.
+//
+// The table's gradient (dQ mode) is the sum of dT over every diagonal of equal
+// distance, then over a bucket's distances.  A warp owns 32 rows: the partial
+// sum of a diagonal moves one lane up with each column, so a shuffle and an add
+// per column sum all diagonals of the block in a fixed order; a block whose
+// distances all share a bucket only adds its values up.
+#include "scored_tc.cuh"
+
+namespace enc {
+namespace scored_tc {
+namespace {
+
+constexpr int kBN = 64;                        // columns of a block
+constexpr int kDQ = 0, kDKV = 1;
+
+template <int D, int MODE>
+struct BCfg {
+  static constexpr int NB = D > 64 ? 2 : 1;
+  static constexpr int kRowThreads = NB * 128;
+  static constexpr int kThreads = kRowThreads + 64;
+  static constexpr int kSub = D > 64 ? D / 64 : 1;
+  static constexpr int kABytes = kSub * 128 * 128;         // one operand of the rows
+  static constexpr int kBSub = kBN * 128;
+  static constexpr int kBBytes = kSub * kBSub;             // one operand of a block's columns
+  static constexpr int kStages = 3;
+  static constexpr int kStage = 2 * kBBytes;
+  static constexpr int kB = 2 * kABytes;
+  static constexpr int kCol = kB + kStages * kStage;       // dKV: lse2 and D of a block's queries, per stage
+  static constexpr int kColBytes = 2 * kBN * 4;
+  static constexpr int kBars = kCol + (MODE == kDKV ? kStages * kColBytes : 0);
+  // a_full, drain, b_full, b_empty (kStages each), s_full, p_full, done (NB each)
+  static constexpr int kNumBars = 2 + 2 * kStages + 3 * NB;
+  static constexpr int kSlot = kBars + kNumBars * 8;
+  static constexpr int kDocs = (kSlot + 16 + 15) / 16 * 16;   // per row warp: the block's documents
+  static constexpr int kDiag = kDocs + NB * 4 * kBN * 4;      // dQ: per row warp, finished diagonals
+  static constexpr int kSums = kDiag + (MODE == kDQ ? NB * 4 * kBN * 4 : 0);   // dQ: per row warp, bucket sums
+  static constexpr int kLut = kSums + (MODE == kDQ ? NB * 4 * kMaxScoreBuckets * 4 : 0);
+  static constexpr int kS = 0, kDP = NB * kBN, kAcc = 2 * NB * kBN;
+  static constexpr int kTmemUsed = kAcc + (MODE == kDKV ? 2 : 1) * D;
+  static constexpr int kTmemCols = kTmemUsed <= 256 ? 256 : 512;
+  static size_t smem(const ScoreArgs& s, int seq, bool table) {
+    return 1024 + kLut + (size_t)lut_floats(s, kBN) * 4 + (table ? (size_t)(2 * s.reach + 1) : 0) +
+           (s.docs ? (size_t)(seq + kBN - 1) / kBN : 0);
+  }
+};
+
+// One row's block of 64 columns, 32 at a time: from S and dP to P and dU.
+struct RowBlock {
+  uint32_t t_s, t_dp;       // TMEM addresses of the row warp's S and dP columns
+  float base, step;         // bias (less lse2 in dQ mode): base + step * column, or base + lut
+  const float* lut;         // at column 0
+  int lo, hi;               // visible columns, as far as length and causality go
+  const int* docs;          // documents of the columns (shared memory), or nullptr
+  int doc;
+  float e, de;              // dU's scale, and D e (dQ mode)
+  const float* col;         // dKV mode: lse2 [64], D [64] of the columns (shared memory)
+  float* diag;              // dQ mode: where lane 31 leaves finished diagonals
+};
+
+// NEAR 0: linear bias; 1: bias from the table in shared memory; 2: that, and the diagonals' sums.
+// sum: NEAR 2: the diagonal that this lane holds at the end; else += dT.
+template <int MODE, bool CAP, int NEAR, bool MASK>
+__device__ __forceinline__ void row_block(const RowBlock& rb, const Cap& cap, float scale2, int lane, float& sum) {
+  float run = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < kBN; c += 32) {
+    uint32_t sv[32], dp[32];
+    tmem_ld_32x32b_x32_async(rb.t_s + c, sv);
+    tmem_ld_32x32b_x32_async(rb.t_dp + c, dp);
+    tmem_wait_ld(sv);
+    tmem_wait_ld(dp);
+    uint32_t pp[MODE == kDKV ? 16 : 1], pu[16];
+    const float* lut = MODE == kDQ ? rb.lut + c : rb.lut - c;
+    const float base = NEAR ? rb.base : fmaf((float)c, rb.step, rb.base);
+    const int lo = rb.lo - c, hi = rb.hi - c;
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      float nl[4] = {}, dcol[4];
+      int4 dj = make_int4(0, 0, 0, 0);
+      if (MODE == kDKV) {
+        const float4 a = *reinterpret_cast<const float4*>(rb.col + c + k);
+        const float4 d = *reinterpret_cast<const float4*>(rb.col + kBN + c + k);
+        nl[0] = a.x; nl[1] = a.y; nl[2] = a.z; nl[3] = a.w;
+        dcol[0] = d.x * rb.e; dcol[1] = d.y * rb.e; dcol[2] = d.z * rb.e; dcol[3] = d.w * rb.e;
+      }
+      if (MASK && rb.docs) dj = *reinterpret_cast<const int4*>(rb.docs + c + k);
+      const int djs[4] = {dj.x, dj.y, dj.z, dj.w};
+      float p[4], u[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float s = __uint_as_float(sv[k + q]);
+        const float add = NEAR ? base + (MODE == kDQ ? lut[k + q] : lut[-(k + q)]) : fmaf((float)(k + q), rb.step, base);
+        float t, r = 0.f;
+        if (CAP) {
+          r = rcp(1.f + ex2(s * cap.in));
+          t = fmaf(-2.f * cap.cap2, r, cap.cap2) + add;
+        } else {
+          t = fmaf(s, scale2, add);
+        }
+        if (MODE == kDKV) t -= nl[q];
+        p[q] = ex2(t);
+        float dt = p[q] * fmaf(__uint_as_float(dp[k + q]), rb.e, MODE == kDKV ? -dcol[q] : -rb.de);
+        u[q] = CAP ? dt * (4.f * r * (1.f - r)) : dt;
+        if (MASK) {                                        // (hidden scores may be NaN)
+          const bool see = k + q >= lo && k + q < hi && (!rb.docs || djs[q] == rb.doc);
+          p[q] = see ? p[q] : 0.f;
+          dt = see ? dt : 0.f;
+          u[q] = see ? u[q] : 0.f;
+        }
+        if (MODE == kDQ) {
+          if (NEAR == 2) {
+            const float up = __shfl_up_sync(0xffffffffu, run, 1);
+            run = lane == 0 ? dt : up + dt;
+            if (lane == 31) rb.diag[c + k + q] = run;
+          } else {
+            sum += dt;
+          }
+        }
+      }
+      if (MODE == kDKV) {
+        pp[k / 2] = half2_of(p[0], p[1]);
+        pp[k / 2 + 1] = half2_of(p[2], p[3]);
+      }
+      pu[k / 2] = half2_of(u[0], u[1]);
+      pu[k / 2 + 1] = half2_of(u[2], u[3]);
+    }
+    // Over columns that this lane has read.
+    if constexpr (MODE == kDKV) tmem_st_32x32b_x16_async(rb.t_s + c / 2, pp);
+    tmem_st_32x32b_x16_async(rb.t_dp + c / 2, pu);
+  }
+  if (NEAR == 2) sum = run;
+}
+
+template <int MODE, bool CAP, int NEAR>
+__device__ __forceinline__ void row_block_m(bool mask, const RowBlock& rb, const Cap& cap, float scale2, int lane,
+                                            float& sum) {
+  if (mask)
+    row_block<MODE, CAP, NEAR, true>(rb, cap, scale2, lane, sum);
+  else
+    row_block<MODE, CAP, NEAR, false>(rb, cap, scale2, lane, sum);
+}
+
+// Adds 32 lanes' values to the warp's bucket sums.  The lanes' distances are consecutive (up or down), so a
+// bucket's lanes are neighbours: a segmented scan, then the last lane of each run adds.
+__device__ __forceinline__ void add_by_bucket(float v, int bucket, float* sums, int lane) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const float w = __shfl_up_sync(0xffffffffu, v, off);
+    const int bk = __shfl_up_sync(0xffffffffu, bucket, off);
+    if (lane >= off && bk == bucket) v += w;
+  }
+  const int after = __shfl_down_sync(0xffffffffu, bucket, 1);
+  if (lane == 31 || after != bucket) sums[bucket] += v;
+  __syncwarp();
+}
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
+    scored_tc_bwd_kernel(const __grid_constant__ ScoreArgs s, const __grid_constant__ CUtensorMap tm_a0,
+                         const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b0,
+                         const __grid_constant__ CUtensorMap tm_b1, const __grid_constant__ CUtensorMap tm_out,
+                         const int32_t* __restrict__ valid_len, const float* __restrict__ rows2, int Sp,
+                         const float* __restrict__ norms, float* __restrict__ partial, __half* __restrict__ dqkv, int B,
+                         int S, int NH, int* __restrict__ status) {
+  using C = BCfg<D, MODE>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::kBars;
+  const uint32_t a_full = bar0, drain = bar0 + 8;
+  auto b_full = [&](int st) { return bar0 + 16 + 8 * st; };
+  auto b_empty = [&](int st) { return bar0 + 16 + 8 * (C::kStages + st); };
+  const uint32_t buf_bars = bar0 + 16 + 16 * C::kStages;
+  auto s_full = [&](int w) { return buf_bars + 8 * w; };
+  auto p_full = [&](int w) { return buf_bars + 8 * (C::NB + w); };
+  auto done = [&](int w) { return buf_bars + 8 * (2 * C::NB + w); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kSlot);
+  float* lut = reinterpret_cast<float*>(smem + C::kLut);
+  uint8_t* bucket_of = reinterpret_cast<uint8_t*>(lut + lut_floats(s, kBN));   // by distance + reach
+  uint8_t* cls = bucket_of + (partial ? 2 * s.reach + 1 : 0);   // documents: 0 skip, 1 whole, 2 mask per element
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int blk = MODE == kDQ ? gridDim.x - 1 - blockIdx.x : blockIdx.x;    // long causal rows first
+  const int r0 = blk * 128;
+  const size_t bh = (size_t)b * NH + h;
+  const int planes = B * NH;
+  pdl_wait();
+  const int n = score_len(valid_len, b, S), prefix = score_prefix(s, b);
+  if (r0 >= n) {                                           // padding: zero gradients
+    const int rows = min(128, S - r0);
+    for (int part = MODE == kDQ ? 0 : 1; part < (MODE == kDQ ? 1 : 3); ++part)
+      for (int k = tid; k < rows * (D / 8); k += C::kThreads)
+        *reinterpret_cast<uint4*>(dqkv + (((size_t)part * planes + bh) * S + r0) * D + (size_t)k * 8) =
+            make_uint4(0, 0, 0, 0);
+    if (MODE == kDQ && partial)
+      for (int k = tid; k < s.buckets; k += C::kThreads) partial[(bh * gridDim.x + blk) * s.buckets + k] = 0.f;
+    return;
+  }
+  // Blocks of columns that some row sees, as far as length and causality go.
+  const int r_last = min(r0 + 127, n - 1);
+  const int jb0 = MODE == kDQ ? 0 : score_ilow(s, r0, prefix) / kBN;
+  const int jb1 = ((MODE == kDQ ? score_jlim(s, r_last, n, prefix) : n) + kBN - 1) / kBN;
+
+  if (tid == 0) {
+    for (int k = 0; k < C::kNumBars; ++k) mbar_init(bar0 + 8 * k, 1);
+    for (int w = 0; w < C::NB; ++w) mbar_init(p_full(w), 4);
+    fence_barrier_init();
+  }
+  if (warp == C::NB * 4) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  const int32_t* docs = s.docs ? s.docs + (size_t)b * S : nullptr;
+  if (docs) {
+    int rlo = INT32_MAX, rhi = INT32_MIN;
+    for (int k = r0 + lane; k <= r_last; k += 32) {
+      const int v = docs[k];
+      rlo = min(rlo, v);
+      rhi = max(rhi, v);
+    }
+    rlo = __reduce_min_sync(0xffffffffu, rlo);
+    rhi = __reduce_max_sync(0xffffffffu, rhi);
+    for (int jb = jb0 + warp; jb < jb1; jb += C::kThreads / 32) {
+      int lo = INT32_MAX, hi = INT32_MIN;
+#pragma unroll
+      for (int c = 0; c < kBN; c += 32) {
+        const int j = jb * kBN + c + lane;
+        if (j < n) {
+          const int v = docs[j];
+          lo = min(lo, v);
+          hi = max(hi, v);
+        }
+      }
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      if (lane == 0) cls[jb] = hi < rlo || lo > rhi ? 0 : (lo == hi && rlo == rhi ? 1 : 2);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();                                           // after taking TMEM
+  auto next_block = [&](int jb) {
+    if (docs)
+      while (jb < jb1 && cls[jb] == 0) ++jb;
+    return jb;
+  };
+
+  bool ok = true;
+  if (warp == C::NB * 4 + 1) {
+    if (lane == 0) {                                       // TMA
+      const int a0 = MODE == kDQ ? (int)bh : planes + (int)bh;               // plane of Q or K
+      const int b0 = MODE == kDQ ? planes + (int)bh : (int)bh;               // plane of K or Q
+      mbar_arrive_expect_tx(a_full, 2 * C::kABytes);
+      for (int u = 0; u < C::kSub; ++u) {
+        tma_load_3d(&tm_a0, sbase + u * 16384, a_full, 64 * u, r0, a0);
+        if (MODE == kDQ)
+          tma_load_3d(&tm_a1, sbase + C::kABytes + u * 16384, a_full, h * D + 64 * u, r0, b);       // dO
+        else
+          tma_load_3d(&tm_a1, sbase + C::kABytes + u * 16384, a_full, 64 * u, r0, 2 * planes + (int)bh);   // V
+      }
+      int it = 0;
+      for (int jb = next_block(jb0); jb < jb1; jb = next_block(jb + 1), ++it) {
+        const int st = it % C::kStages, c0 = jb * kBN;
+        if (it >= C::kStages && !(ok = mbar_wait(b_empty(st), ((it / C::kStages) & 1) ^ 1, kWaitLimitNs))) break;
+        const uint32_t dst = sbase + C::kB + st * C::kStage;
+        mbar_arrive_expect_tx(b_full(st), C::kStage + (MODE == kDKV ? C::kColBytes : 0));
+        for (int u = 0; u < C::kSub; ++u) {
+          tma_load_3d(&tm_b0, dst + u * C::kBSub, b_full(st), 64 * u, c0, b0);
+          if (MODE == kDQ)
+            tma_load_3d(&tm_b1, dst + C::kBBytes + u * C::kBSub, b_full(st), 64 * u, c0, 2 * planes + (int)bh);   // V
+          else
+            tma_load_3d(&tm_b1, dst + C::kBBytes + u * C::kBSub, b_full(st), h * D + 64 * u, c0, b);   // dO
+        }
+        if (MODE == kDKV)                                  // rows of rows2 are padded to whole blocks
+          for (int k = 0; k < 2; ++k)
+            bulk_load(sbase + C::kCol + st * C::kColBytes + k * kBN * 4, rows2 + ((size_t)k * planes + bh) * Sp + c0,
+                      kBN * 4, b_full(st));
+      }
+      mbar_wait(a_full, 0, kWaitLimitNs);                  // every load has landed before the CTA exits
+      for (int k = it > C::kStages ? it - C::kStages : 0; k < it; ++k)
+        mbar_wait(b_full(k % C::kStages), (k / C::kStages) & 1, kWaitLimitNs);
+    }
+  } else if (warp == C::NB * 4) {
+    if (lane == 0) {                                       // MMA
+      constexpr uint32_t idesc_s = idesc_f16_f32(128, kBN);
+      constexpr uint32_t idesc_o = idesc_bmn(128, D);
+      auto issue_scores = [&](int it) {                    // S and dP of block number `it`
+        const int w = it % C::NB;
+        const uint32_t st = sbase + C::kB + (it % C::kStages) * C::kStage;
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t u = kk / 4, o = (kk % 4) * 32;
+            mma_f16_ss(tmem + (a ? C::kDP : C::kS) + w * kBN, smem_desc_sw128(sbase + a * C::kABytes + u * 16384 + o),
+                       smem_desc_sw128(st + a * C::kBBytes + u * C::kBSub + o), idesc_s, kk > 0 ? 1u : 0u);
+          }
+        mma_commit(s_full(w));
+      };
+      ok = mbar_wait(a_full, 0, kWaitLimitNs);
+      int jb = next_block(jb0), ahead = jb;                // block of `it`, and the next whose scores are not issued
+      int issued = 0;
+      for (; issued < C::NB && ok && ahead < jb1; ++issued) {
+        if (!(ok = mbar_wait(b_full(issued % C::kStages), 0, kWaitLimitNs))) break;
+        tc_fence_after();
+        issue_scores(issued);
+        ahead = next_block(ahead + 1);
+      }
+      for (int it = 0; ok && jb < jb1; ++it, jb = next_block(jb + 1)) {
+        const int w = it % C::NB;
+        const uint32_t st = sbase + C::kB + (it % C::kStages) * C::kStage;
+        if (!(ok = mbar_wait(p_full(w), (it / C::NB) & 1, kWaitLimitNs))) break;
+        tc_fence_after();
+        const int ksteps = (min(kBN, n - jb * kBN) + 15) >> 4;
+        for (int kk = 0; kk < ksteps; ++kk)
+          mma_f16_ts(tmem + C::kAcc, tmem + C::kDP + w * kBN + 8 * kk, desc_mn_sw128(st + kk * 2048, C::kBSub), idesc_o,
+                     (it > 0 || kk > 0) ? 1u : 0u);
+        if (MODE == kDKV)
+          for (int kk = 0; kk < ksteps; ++kk)
+            mma_f16_ts(tmem + C::kAcc + D, tmem + C::kS + w * kBN + 8 * kk,
+                       desc_mn_sw128(st + C::kBBytes + kk * 2048, C::kBSub), idesc_o, (it > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(done(w));
+        mma_commit(b_empty(it % C::kStages));
+        if (ahead < jb1) {                                 // S and dP may be overwritten once P and dU have been read
+          if (!(ok = mbar_wait(b_full(issued % C::kStages), (issued / C::kStages) & 1, kWaitLimitNs))) break;
+          if (!(ok = mbar_wait(done(w), (it / C::NB) & 1, kWaitLimitNs))) break;
+          tc_fence_after();
+          issue_scores(issued);
+          ++issued;
+          ahead = next_block(ahead + 1);
+        }
+      }
+      mma_commit(drain);                                   // every MMA issued here has completed
+      mbar_wait(drain, 0, kWaitLimitNs);
+    }
+  } else {
+    const int w = warp >> 2, quad = warp & 3, r = quad * 32 + lane;   // warpgroup; row of the tile = TMEM lane
+    const int pos = r0 + r;                                // the row's position
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const Bias bias = make_bias(s, lut, NH, h, kBN, tid, C::kRowThreads);
+    float* sums = reinterpret_cast<float*>(smem + C::kSums) + warp * kMaxScoreBuckets;
+    if (MODE == kDQ && partial) {
+      for (int k = tid; k <= 2 * s.reach; k += C::kRowThreads)
+        bucket_of[k] = static_cast<uint8_t>(score_bucket(s, k - s.reach));
+      for (int k = lane; k < s.buckets; k += 32) sums[k] = 0.f;
+    }
+    // dU's scale: norms holds the largest |dO_i|^2 and |v_j|^2 of every 128 rows.
+    float mo = 0.f, mv = 0.f;
+    for (int k = lane; k < (n + 127) / 128; k += 32) {
+      mo = fmaxf(mo, norms[bh * (Sp / 128) + k]);
+      mv = fmaxf(mv, norms[((size_t)planes + bh) * (Sp / 128) + k]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, off));
+      mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, off));
+    }
+    const float prod = sqrtf(mo) * sqrtf(mv);
+    int ex = 0;
+    if (prod > 0.f && prod < INFINITY) frexpf(prod, &ex);  // prod in [2^(ex-1), 2^ex)
+    ex = max(-100, min(100, 14 - ex));
+    const float e = exp2f((float)ex), inv_e = exp2f((float)-ex);
+    asm volatile("bar.sync 1, %0;" ::"n"(C::kRowThreads) : "memory");
+
+    const Cap cap = make_cap(s);
+    const float scale2 = s.scale * kLog2e;
+    const bool mine = pos < n;
+    float lse2 = 0.f, dsum = 0.f;
+    if (MODE == kDQ) {                                     // (+inf where the row sees nothing)
+      lse2 = rows2[bh * Sp + pos];
+      dsum = rows2[((size_t)planes + bh) * Sp + pos];
+    }
+    const int r_end = r0 + 127;
+    // The columns that the row sees, and those that every row of the tile sees.
+    const int lo = MODE == kDQ ? 0 : score_ilow(s, pos, prefix);
+    const int hi = !mine ? 0 : MODE == kDQ ? score_jlim(s, pos, n, prefix) : n;
+    const int lo_all = MODE == kDQ ? 0 : score_ilow(s, r_end, prefix);
+    const int hi_all = MODE == kDQ ? score_jlim(s, r0, n, prefix) : n;
+    RowBlock rb;
+    rb.doc = docs && mine ? docs[pos] : 0;
+    rb.e = e;
+    rb.de = dsum * e;
+    rb.t_s = t_lane + C::kS + w * kBN;
+    rb.t_dp = t_lane + C::kDP + w * kBN;
+    rb.diag = reinterpret_cast<float*>(smem + C::kDiag) + warp * kBN;
+    int* wdocs = reinterpret_cast<int*>(smem + C::kDocs) + warp * kBN;
+    float far_right = 0.f, far_left = 0.f;                 // sums of dT past the table's reach
+    const bool biased = s.table || s.slopes;
+    int it = 0;
+    for (int jb = next_block(jb0); jb < jb1; jb = next_block(jb + 1), ++it) {
+      if (it % C::NB != w) continue;
+      const int c0 = jb * kBN, st = it % C::kStages;
+      const uint32_t ph = (it / C::NB) & 1;
+      const bool cut = lo_all > c0 || c0 + kBN > hi_all || r_end >= n;
+      const bool by_doc = docs && cls[jb] == 2;
+      rb.lo = lo - c0;
+      rb.hi = hi - c0;
+      rb.docs = nullptr;
+      if (by_doc) {
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < kBN; c += 32) wdocs[c + lane] = c0 + c + lane < n ? docs[c0 + c + lane] : 0;
+        __syncwarp();
+        rb.docs = wdocs;
+      }
+      // Distances key - query of the block, and its bias.
+      const int rel0 = MODE == kDQ ? c0 - pos : pos - c0;  // at column 0
+      const int rel_min = MODE == kDQ ? c0 - r_end : r0 - (c0 + kBN - 1);
+      const int rel_max = MODE == kDQ ? c0 + kBN - 1 - r0 : r_end - c0;
+      const bool ahead = rel_min >= bias.reach;
+      const bool near = biased && !ahead && rel_max > -bias.reach;
+      const float sl = ahead ? -bias.slope2 : bias.slope2;
+      rb.step = MODE == kDQ ? sl : -sl;
+      rb.base = near ? -lse2 : (biased ? (ahead ? bias.right : bias.left) + sl * (float)rel0 : 0.f) - lse2;
+      rb.lut = bias.lut + bias.off + rel0;
+      rb.col = reinterpret_cast<const float*>(smem + C::kCol + st * C::kColBytes);
+      if (!(ok = warp_wait(s_full(w), ph))) break;
+      if (MODE == kDKV && !(ok = warp_wait(b_full(st), (it / C::kStages) & 1))) break;   // the columns' lse2 and D
+      tc_fence_after();
+      const bool mask = cut || by_doc;
+      float sum = 0.f;
+      if (near) {
+        if (MODE == kDQ && partial) {
+          if (cap.on)
+            row_block_m<MODE, true, MODE == kDQ ? 2 : 1>(mask, rb, cap, scale2, lane, sum);
+          else
+            row_block_m<MODE, false, MODE == kDQ ? 2 : 1>(mask, rb, cap, scale2, lane, sum);
+        } else if (cap.on) {
+          row_block_m<MODE, true, 1>(mask, rb, cap, scale2, lane, sum);
+        } else {
+          row_block_m<MODE, false, 1>(mask, rb, cap, scale2, lane, sum);
+        }
+      } else if (cap.on) {
+        row_block_m<MODE, true, 0>(mask, rb, cap, scale2, lane, sum);
+      } else {
+        row_block_m<MODE, false, 0>(mask, rb, cap, scale2, lane, sum);
+      }
+      // Rows of the columns' operands in [n, n rounded up to 16) are read by the products: zeros.
+      const int lim = n - c0, lim16 = (min(kBN, lim) + 15) & ~15;
+      if (lim < lim16 && quad == 0) {
+        const int units = (lim16 - lim) * 8;
+        for (int k = lane; k < units * C::kSub * (MODE == kDKV ? 2 : 1); k += 32) {
+          const int plane = k / units, rr = lim + k % units / 8;             // sub-tiles of B0, then of B1
+          *reinterpret_cast<uint4*>(smem + C::kB + st * C::kStage + plane * C::kBSub + rr * 128 + (k % 8) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(w));
+      if (MODE == kDQ && partial) {
+        if (near) {
+          // diag[k]: the diagonal that left lane 31 at column k; `sum`: the one that is in this lane now.
+          const int first = c0 - (r0 + quad * 32 + 31);    // distance of diag[0]
+          auto bucket_at = [&](int rel) { return (int)bucket_of[max(-s.reach, min(s.reach, rel)) + s.reach]; };
+          add_by_bucket(rb.diag[lane], bucket_at(first + lane), sums, lane);
+          add_by_bucket(rb.diag[lane + 32], bucket_at(first + lane + 32), sums, lane);
+          const float rest = lane == 31 ? 0.f : sum;       // lane 31's has just been added
+          add_by_bucket(rest, bucket_at(c0 + kBN - 1 - (r0 + quad * 32 + lane)), sums, lane);
+        } else if (ahead) {
+          far_right += sum;
+        } else {
+          far_left += sum;
+        }
+      }
+    }
+    if (MODE == kDQ && partial) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        far_right += __shfl_xor_sync(0xffffffffu, far_right, off);
+        far_left += __shfl_xor_sync(0xffffffffu, far_left, off);
+      }
+      if (lane == 0) {
+        sums[score_bucket(s, s.reach)] += far_right;
+        sums[score_bucket(s, -s.reach)] += far_left;
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(C::kRowThreads) : "memory");
+      const float* all = reinterpret_cast<const float*>(smem + C::kSums);
+      for (int k = tid; k < s.buckets; k += C::kRowThreads) {
+        float total = 0.f;
+#pragma unroll
+        for (int v = 0; v < C::NB * 4; ++v) total += all[v * kMaxScoreBuckets + k];
+        partial[(bh * gridDim.x + blk) * s.buckets + k] = total * inv_e;
+      }
+    }
+    // Accumulators: 32 columns at a time to the warpgroups in turn, staged over the rows' operands (their
+    // last reader has completed) in the store's swizzle, one TMA store per 64 columns of a warp's 32 rows.
+    if (ok)
+      for (int k = max(0, it - C::NB); k < it && ok; ++k) ok = warp_wait(done(k % C::NB), (k / C::NB) & 1);
+    if (it == 0) mbar_wait(a_full, 0, kWaitLimitNs);
+    if (ok) {
+      tc_fence_after();
+      constexpr int kCols = D < 64 ? D : 64, kRowBytes = 2 * kCols;
+      constexpr int kParts = (MODE == kDKV ? 2 : 1) * C::kSub;               // pieces of up to 64 columns
+#pragma unroll 1
+      for (int part = w; part < kParts; part += C::NB) {
+        const int acc = part / C::kSub, u = part % C::kSub;                  // acc 0: dQ or dK; 1: dV
+        const float f = !mine ? 0.f : acc == 0 ? s.scale * inv_e : 1.f;
+        uint8_t* tile = smem + part * 16384 + quad * 32 * kRowBytes;
+#pragma unroll 1
+        for (int c = 0; c < kCols; c += 32) {
+          uint32_t oa[32];
+          if (it > 0) tmem_ld_32x32b_x32(t_lane + C::kAcc + acc * D + u * 64 + c, oa);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              v[k] = mine && it > 0 ? half2_of(__uint_as_float(oa[8 * q + 2 * k]) * f, __uint_as_float(oa[8 * q + 2 * k + 1]) * f)
+                                    : 0u;
+            const int unit = c / 8 + q;
+            const int sw = D < 64 ? unit ^ ((lane >> 1) & 3) : unit ^ (lane & 7);
+            *reinterpret_cast<uint4*>(tile + lane * kRowBytes + 16 * sw) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        const int row = r0 + quad * 32;
+        if (lane == 0 && row < S) {
+          tma_store_3d(&tm_out, smem_u32(tile), 64 * u, row, (MODE == kDQ ? 0 : 1 + acc) * planes + (int)bh);
+          bulk_commit_group();
+        }
+      }
+      if (lane == 0) bulk_wait_group_all();
+    }
+  }
+
+  if (!ok) atomicCAS(status, 0, kStatusWaitTimeout);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::NB * 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Per row i: lse in units of log2 (+inf where the row sees nothing or is past
+// n, which makes P zero) and D_i, in rows padded to Sp; per 128 rows, the
+// largest |dO_i|^2 and |v_j|^2.  D / 8 lanes read a row with 16-byte loads.
+constexpr int kStatThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kStatThreads)
+    scored_stats_kernel(const __half* __restrict__ qkv, const __half* __restrict__ ctx,
+                        const __half* __restrict__ dctx, const float* __restrict__ lse,
+                        const int32_t* __restrict__ valid_len, float* __restrict__ rows2, float* __restrict__ norms,
+                        int B, int S, int Sp, int NH) {
+  constexpr int kLanes = D / 8, kRows = kStatThreads / kLanes;
+  __shared__ float wo[kStatThreads / 32], wv[kStatThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int h = blockIdx.y, b = blockIdx.z, r0 = blockIdx.x * 128;
+  const size_t bh = (size_t)b * NH + h, planes = (size_t)B * NH;
+  const int n = score_len(valid_len, b, S);
+  const int gl = threadIdx.x % kLanes;
+  float mo = 0.f, mv = 0.f;
+  auto widen = [](uint4 w, float (&f)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
+      f[2 * k] = v.x;
+      f[2 * k + 1] = v.y;
+    }
+  };
+#pragma unroll 2
+  for (int rr = threadIdx.x / kLanes; rr < 128; rr += kRows) {
+    const int i = r0 + rr;
+    float dot = 0.f, oo = 0.f, vv = 0.f;
+    if (i < n) {
+      float o[8], g[8], v[8];
+      const size_t at = ((size_t)b * S + i) * NH * D + (size_t)h * D + gl * 8;
+      widen(*reinterpret_cast<const uint4*>(ctx + at), o);
+      widen(*reinterpret_cast<const uint4*>(dctx + at), g);
+      widen(*reinterpret_cast<const uint4*>(qkv + ((2 * planes + bh) * S + i) * D + gl * 8), v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        dot = fmaf(o[k], g[k], dot);
+        oo = fmaf(g[k], g[k], oo);
+        vv = fmaf(v[k], v[k], vv);
+      }
+    }
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1) {
+      dot += __shfl_xor_sync(0xffffffffu, dot, off);
+      oo += __shfl_xor_sync(0xffffffffu, oo, off);
+      vv += __shfl_xor_sync(0xffffffffu, vv, off);
+    }
+    mo = fmaxf(mo, oo);
+    mv = fmaxf(mv, vv);
+    if (gl == 0) {
+      const float l = i < n ? lse[bh * S + i] * kLog2e : INFINITY;
+      rows2[bh * Sp + i] = l == -INFINITY ? INFINITY : l;
+      rows2[(planes + bh) * Sp + i] = dot;
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, off));
+    mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, off));
+  }
+  if (threadIdx.x % 32 == 0) {
+    wo[threadIdx.x / 32] = mo;
+    wv[threadIdx.x / 32] = mv;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < kStatThreads / 32; ++k) {
+      mo = fmaxf(mo, wo[k]);
+      mv = fmaxf(mv, wv[k]);
+    }
+    norms[bh * (Sp / 128) + blockIdx.x] = mo;
+    norms[(planes + bh) * (Sp / 128) + blockIdx.x] = mv;
+  }
+}
+
+template <int D, int MODE>
+cudaError_t launch_mode(const ScoreArgs& s, const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0,
+                        const CUtensorMap& b1, const CUtensorMap& out, const int32_t* vl, const float* rows2, int Sp,
+                        const float* norms, float* partial, __half* dqkv, const ScoredShape& sh, int* status,
+                        cudaStream_t stream) {
+  using C = BCfg<D, MODE>;
+  static const cudaError_t attr = cudaFuncSetAttribute(scored_tc_bwd_kernel<D, MODE>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (attr != cudaSuccess) return attr;
+  const dim3 grid((sh.seq + 127) / 128, sh.head_num, sh.batch);
+  return launch_kernel(scored_tc_bwd_kernel<D, MODE>, grid, dim3(C::kThreads), C::smem(s, sh.seq, partial != nullptr),
+                       stream, nullptr, 0, s, a0, a1, b0, b1, out, vl, rows2, Sp, norms, partial, dqkv, sh.batch,
+                       sh.seq, sh.head_num, status);
+}
+
+template <int D>
+cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, const __half* ctx, const float* lse,
+                     const __half* dctx, __half* dqkv, float* partial, void* scratch, const ScoredShape& sh, int* status,
+                     cudaStream_t stream) {
+  const uint64_t planes = (uint64_t)sh.batch * sh.head_num, H = (uint64_t)sh.head_num * D;
+  const int Sp = (sh.seq + 127) / 128 * 128;
+  float* rows2 = static_cast<float*>(scratch);
+  float* norms = rows2 + 2 * planes * Sp;
+  const dim3 grid(Sp / 128, sh.head_num, sh.batch);
+  cudaError_t e = launch_kernel(scored_stats_kernel<D>, grid, dim3(kStatThreads), 0, stream, nullptr, 0, qkv, ctx, dctx,
+                                lse, vl, rows2, norms, sh.batch, sh.seq, Sp, sh.head_num);
+  if (e != cudaSuccess) return e;
+  CUtensorMap rows, cols, drows, dcols, out;
+  if (!encode_operand_map(&rows, qkv, D, sh.seq, 3 * planes, 64, 128) ||
+      !encode_operand_map(&cols, qkv, D, sh.seq, 3 * planes, 64, kBN) ||
+      !encode_operand_map(&drows, dctx, H, sh.seq, sh.batch, 64, 128) ||
+      !encode_operand_map(&dcols, dctx, H, sh.seq, sh.batch, 64, kBN) ||
+      !encode_operand_map(&out, dqkv, D, sh.seq, 3 * planes, D < 64 ? D : 64, 32))
+    return cudaErrorInvalidValue;
+  e = launch_mode<D, kDQ>(s, rows, drows, cols, cols, out, vl, rows2, Sp, norms, partial, dqkv, sh, status, stream);
+  if (e != cudaSuccess) return e;
+  return launch_mode<D, kDKV>(s, rows, rows, cols, dcols, out, vl, rows2, Sp, norms, nullptr, dqkv, sh, status, stream);
+}
+
+}  // namespace
+}  // namespace scored_tc
+
+size_t scored_backward_tc_scratch(const ScoredShape& sh) {
+  const size_t planes = (size_t)sh.batch * sh.head_num, blocks = ((size_t)sh.seq + 127) / 128;
+  return planes * blocks * (2 * 128 + 2) * 4;
+}
+
+cudaError_t launch_scored_backward_tc(const ScoreArgs& s, const __half* qkv, const int32_t* valid_len,
+                                      const __half* ctx, const float* lse, const __half* dctx, __half* dqkv,
+                                      float* partial, void* scratch, const ScoredShape& sh, int* status,
+                                      cudaStream_t stream) {
+  using namespace scored_tc;
+  switch (sh.size_per_head) {
+    case 32: return launch_d<32>(s, qkv, valid_len, ctx, lse, dctx, dqkv, partial, scratch, sh, status, stream);
+    case 64: return launch_d<64>(s, qkv, valid_len, ctx, lse, dctx, dqkv, partial, scratch, sh, status, stream);
+    case 128: return launch_d<128>(s, qkv, valid_len, ctx, lse, dctx, dqkv, partial, scratch, sh, status, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace enc
