@@ -107,15 +107,21 @@ class Scores:
 
     def check(self, head_num: int, batch: Optional[int] = None, seq: Optional[int] = None):
         """Raise ValueError where a tensor does not fit head_num, batch or seq (the C ABI cannot see sizes)."""
-        for name, t, want in (("slopes", self.slopes, (head_num,)),
-                              ("table", self.table, (self.c.num_buckets, head_num)),
-                              ("prefix_len", self.prefix_len, (batch,)), ("doc_ids", self.doc_ids, (batch, seq))):
-            if t is not None and any(w is not None and w != n for w, n in zip(want, t.shape)):
-                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {want}")
+        if self.slopes is not None and self.slopes.shape[0] != head_num:
+            raise ValueError(f"slopes has shape {tuple(self.slopes.shape)}, expected {(head_num,)}")
+        if self.table is not None and self.table.shape[1] != head_num:
+            raise ValueError(f"table has shape {tuple(self.table.shape)}, expected {(self.c.num_buckets, head_num)}")
+        if batch is None:
+            return
+        if self.prefix_len is not None and self.prefix_len.shape[0] != batch:
+            raise ValueError(f"prefix_len has shape {tuple(self.prefix_len.shape)}, expected {(batch,)}")
+        if self.doc_ids is not None and tuple(self.doc_ids.shape) != (batch, seq):
+            raise ValueError(f"doc_ids has shape {tuple(self.doc_ids.shape)}, expected {(batch, seq)}")
 
     @property
-    def pointer(self):
-        return ctypes.cast(ctypes.pointer(self.c), ctypes.c_void_p)
+    def pointer(self) -> int:
+        """Address of the enc_scores struct."""
+        return ctypes.addressof(self.c)
 
 
 class EncError(RuntimeError):
@@ -170,7 +176,7 @@ def _typed_ptr(t, dtype: str, dim: int) -> Optional[int]:
     if t is None:
         return None
     p = _dptr(t)
-    if str(t.dtype) != f"torch.{dtype}" or t.dim() != dim:
+    if t.dtype is not _torch_dtype(dtype) or t.dim() != dim:
         raise ValueError(f"expected a {dim}-dimensional {dtype} tensor, got {tuple(t.shape)} {t.dtype}")
     return p
 
@@ -178,9 +184,19 @@ def _typed_ptr(t, dtype: str, dim: int) -> Optional[int]:
 def _shaped_ptr(t, dtype: str, numel: int) -> int:
     """Device pointer of a contiguous CUDA tensor of that dtype and element count."""
     p = _dptr(t)
-    if str(t.dtype) != f"torch.{dtype}" or t.numel() != numel:
+    if t.dtype is not _torch_dtype(dtype) or t.numel() != numel:
         raise ValueError(f"expected {numel} elements of {dtype}, got {tuple(t.shape)} {t.dtype}")
     return p
+
+
+_torch_dtypes: Dict = {}
+
+
+def _torch_dtype(name: str):
+    if not _torch_dtypes:
+        import torch
+        _torch_dtypes.update({"float16": torch.float16, "float32": torch.float32, "int32": torch.int32})
+    return _torch_dtypes[name]
 
 
 class Encoder:

@@ -147,6 +147,8 @@ struct enc_handle {
   std::vector<cudaEvent_t> trace;   // optional per-kernel events for enc_forward
   bool scored = false;              // enc_set_scores: the forwards' attention has modified scores
   enc::ScoreArgs scores;
+  enc::ScoreArgs bounds_of;         // the table layout whose bucket bounds were worked out last
+  int bounds_distance = 0;
   void* scored_ws = nullptr;        // scratch of the enc_op_scored_* calls
   size_t scored_ws_bytes = 0;
   std::vector<void*> scored_retired;   // smaller scratch that captured graphs may still name
@@ -506,7 +508,7 @@ bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
 }
 
 // Checks an enc_scores and lays it out for the kernels.
-enc_status make_scores(const enc_handle* h, const enc_scores* p, enc::ScoreArgs& s) {
+enc_status make_scores(enc_handle* h, const enc_scores* p, enc::ScoreArgs& s) {
   if (!p) return fail(ENC_ERR_INVALID_ARG, "scores is null");
   if (!std::isfinite(p->scale)) return fail(ENC_ERR_INVALID_ARG, "scale is not finite");
   if (!std::isfinite(p->cap) || p->cap < 0.f) return fail(ENC_ERR_INVALID_ARG, "cap must be finite and >= 0");
@@ -529,6 +531,13 @@ enc_status make_scores(const enc_handle* h, const enc_scores* p, enc::ScoreArgs&
                 enc::kMaxScoreDistance);
   s.buckets = p->num_buckets;
   s.both = both;
+  // The bounds of the last table layout are kept: finding them again would cost microseconds a call.
+  if (h->bounds_of.buckets == s.buckets && h->bounds_of.both == s.both && h->bounds_distance == p->max_distance) {
+    s.num_bounds = h->bounds_of.num_bounds;
+    s.reach = h->bounds_of.reach;
+    memcpy(s.bounds, h->bounds_of.bounds, sizeof(s.bounds));
+    return ENC_OK;
+  }
   // bounds[k - 1]: the first distance whose logarithmic bucket is at least k
   // (k = 1 .. m - e - 1), found next to e (max_distance / e)^(k / (m - e)).
   const double ratio = log((double)p->max_distance / e);
@@ -541,6 +550,8 @@ enc_status make_scores(const enc_handle* h, const enc_scores* p, enc::ScoreArgs&
     s.bounds[s.num_bounds++] = a;
   }
   s.reach = s.num_bounds ? s.bounds[s.num_bounds - 1] : e;
+  h->bounds_of = s;
+  h->bounds_distance = p->max_distance;
   return ENC_OK;
 }
 

@@ -42,11 +42,16 @@ __host__ __device__ __forceinline__ int score_bucket(const ScoreArgs& s, int rel
   return c + (s.both && rel > 0 ? nb : 0);
 }
 
-// The part of t2 that depends on the distance alone.
-__device__ __forceinline__ float score_bias2(const ScoreArgs& s, int nh, int h, float slope, int rel) {
+// The part of t2 that depends on the distance alone; column: the head's column of the table.
+__device__ __forceinline__ float score_bias2(const ScoreArgs& s, const float* column, float slope, int rel) {
   float b = -slope * fabsf(static_cast<float>(rel));
-  if (s.table) b += s.table[static_cast<size_t>(score_bucket(s, rel)) * nh + h];
+  if (s.table) b += column[score_bucket(s, rel)];
   return b * kLog2e;
+}
+// Copies the head's column of the table to shared memory; a barrier must follow.
+__device__ __forceinline__ void load_column(const ScoreArgs& s, float* column, int nh, int h, int t, int threads) {
+  if (s.table)
+    for (int c = t; c < s.buckets; c += threads) column[c] = s.table[static_cast<size_t>(c) * nh + h];
 }
 
 __device__ __forceinline__ int score_len(const int32_t* valid_len, int b, int S) {

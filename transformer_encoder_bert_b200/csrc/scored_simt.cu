@@ -121,14 +121,14 @@ __device__ __forceinline__ void accumulate(const float* P, const float* B, float
 // The biases of the 127 distances of a tile (rel = rel0 + index - 63) and the
 // documents of its rows and columns.
 struct TileInfo {
-  float bias2[2 * kT];
+  float bias2[2 * kT], column[kMaxScoreBuckets];
   int row_doc[kT], col_doc[kT];
 };
 
-__device__ __forceinline__ void fill_bias(TileInfo* ti, const ScoreArgs& s, int nh, int h, float slope, int rel0) {
+__device__ __forceinline__ void fill_bias(TileInfo* ti, const ScoreArgs& s, float slope, int rel0) {
   if (threadIdx.x < 2 * kT - 1)
     ti->bias2[threadIdx.x] =
-        s.table || s.slopes ? score_bias2(s, nh, h, slope, rel0 + (int)threadIdx.x - (kT - 1)) : 0.f;
+        s.table || s.slopes ? score_bias2(s, ti->column, slope, rel0 + (int)threadIdx.x - (kT - 1)) : 0.f;
 }
 
 __device__ __forceinline__ void fill_docs(int* dst, const ScoreArgs& s, int b, int S, int pos0) {
@@ -171,9 +171,11 @@ __global__ void __launch_bounds__(kThreads)
   const int klim = rows > 0 ? score_jlim(s, q0 + rows - 1, n, prefix) : 0;
   load_tile<T, D>(Qs, Qg, q0, n, D);
   fill_docs(ti->row_doc, s, b, S, q0);
+  load_column(s, ti->column, NH, h, threadIdx.x, kThreads);
+  __syncthreads();
   for (int j0 = 0; j0 < klim; j0 += kT) {
     load_tile<T, D>(Ks, Qg + part, j0, n, D);
-    fill_bias(ti, s, NH, h, slope, j0 - q0);
+    fill_bias(ti, s, slope, j0 - q0);
     fill_docs(ti->col_doc, s, b, S, j0);
     __syncthreads();
     float acc[4][4];
@@ -260,6 +262,8 @@ __global__ void __launch_bounds__(kThreads)
   load_tile<T, D>(Qs, Qg, q0, n, D);
   load_tile<T, D>(dOs, dctx + (size_t)b * S * H + h * D, q0, n, H);
   fill_docs(ti->row_doc, s, b, S, q0);
+  load_column(s, ti->column, NH, h, threadIdx.x, kThreads);
+  __syncthreads();
   if (partial && threadIdx.x < kMaxScoreBuckets) bucket_sum[threadIdx.x] = 0.f;
   float lse2[4], dsum[4];
 #pragma unroll
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int j0 = 0; j0 < klim; j0 += kT) {
     load_tile<T, D>(Ks, Qg + part, j0, n, D);
     load_tile<T, D>(Vs, Qg + 2 * part, j0, n, D);
-    fill_bias(ti, s, NH, h, slope, j0 - q0);
+    fill_bias(ti, s, slope, j0 - q0);
     fill_docs(ti->col_doc, s, b, S, j0);
     __syncthreads();
     float acc[4][4], dp[4][4];
@@ -367,11 +371,13 @@ __global__ void __launch_bounds__(kThreads)
   load_tile<T, D>(Ks, Qg + part, j0, n, D);
   load_tile<T, D>(Vs, Qg + 2 * part, j0, n, D);
   fill_docs(ti->row_doc, s, b, S, j0);
+  load_column(s, ti->column, NH, h, threadIdx.x, kThreads);
+  __syncthreads();
   const int qfirst = j0 < n ? score_ilow(s, j0, prefix) / kT * kT : n;
   for (int q0 = qfirst; q0 < n; q0 += kT) {
     load_tile<T, D>(Qs, Qg, q0, n, D);
     load_tile<T, D>(dOs, dctx + (size_t)b * S * H + h * D, q0, n, H);
-    fill_bias(ti, s, NH, h, slope, j0 - q0);
+    fill_bias(ti, s, slope, j0 - q0);
     fill_docs(ti->col_doc, s, b, S, q0);
     if (threadIdx.x < kT) {
       const int i = q0 + threadIdx.x;

@@ -10,9 +10,14 @@
 // order: no scratch in memory, no second launch, and the same result on every
 // run.
 //
-// Inside a CTA a row is read by D * sizeof(T) / 16 neighbouring lanes with one
-// 16-byte load each.  A lane group takes kU rows of K and the same rows of V at
-// a time (2 kU loads in flight), forms the kU scores with shuffles, and keeps a
+// Inside a CTA a row is read by D * sizeof(T) / 16 neighbouring lanes, 16 bytes
+// each.  A lane group takes kU rows of K and the same rows of V at a time,
+// through a ring of kStages stages in shared memory that cp.async fills: every
+// thread reads back only what it asked for itself, so the ring needs no barrier
+// and the loads of two stages (32 KB each) stay in flight under the arithmetic.
+// The kU dot products are added up over the group by halving: each exchange
+// passes half of the rows on, so that a lane ends with the score of one row and
+// bias, cap and exponential are worked out once per row.  The group keeps a
 // running maximum, sum and output (the softmax in one pass); groups, then
 // warps, then CTAs are merged at the end.
 #include "scored.cuh"
@@ -23,7 +28,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kU = 4;                                      // rows of K and of V in flight per lane group
+constexpr int kU = 4;                                      // rows of K and of V per lane group and stage
+constexpr int kStages = 3;
+constexpr int kStageBytes = 2 * kU * kThreads * 16;
 
 template <typename T>
 struct Vec;                                                // the 16 bytes of a lane as floats
@@ -51,8 +58,23 @@ struct Vec<float> {
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // 2^(m - to), 0 for a part that has seen nothing.
-__device__ __forceinline__ float weight2(float m, float to) { return m == -INFINITY ? 0.f : exp2f(m - to); }
+__device__ __forceinline__ float weight2(float m, float to) { return m == -INFINITY ? 0.f : ex2(m - to); }
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool read) {   // zeros where not read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr)
+               : "memory");
+  return v;
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -61,10 +83,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr int N = Vec<T>::N;
   constexpr int kLanes = D / N;                            // lanes of a row
   constexpr int kGroups = kThreads / kLanes;
-  static_assert(kLanes >= kU && kLanes <= 32, "a lane of the group per score");
+  static_assert(kU == 4 && kLanes >= kU && kLanes <= 32, "a lane of the group per row");
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float wm[kWarps], wl[kWarps];
   __shared__ __align__(16) float wo[kWarps][D];
-  __shared__ float part_o[D], part_ml[2];
+  __shared__ float part_o[D], part_ml[2], column[kMaxScoreBuckets];
   pdl_wait();
   pdl_trigger();
   const int h = blockIdx.y, b = blockIdx.z;
@@ -81,66 +104,92 @@ __global__ void __launch_bounds__(kThreads, 2)
   T* kc = cache + bh * (size_t)C * D;
   T* vc = kc + (size_t)B * NH * C * D;
   const int gl = lane % kLanes, group = tid / kLanes;
+  const uint32_t mine = sm100::smem_u32(ring) + tid * 16;
+  constexpr int kStep = kGroups * kU;                      // rows of a stage
+  auto request = [&](int j0, int stage) {                  // position p itself comes from the new token
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int j = j0 + u * kGroups + group;
+      const bool read = j < hi;
+      const T* k = j == p ? qg + part : kc + (size_t)(read ? j : 0) * D;
+      const T* v = j == p ? qg + 2 * part : vc + (size_t)(read ? j : 0) * D;
+      copy16(mine + stage * kStageBytes + (2 * u) * kThreads * 16, k + gl * N, read);
+      copy16(mine + stage * kStageBytes + (2 * u + 1) * kThreads * 16, v + gl * N, read);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int st = 0; st < kStages - 1; ++st) request(lo + st * kStep, st);
+
+  load_column(s, column, NH, h, tid, kThreads);
   float q[N];
   Vec<T>::widen(*reinterpret_cast<const uint4*>(qg + gl * N), q);
 #pragma unroll
   for (int i = 0; i < N; ++i) q[i] *= s.scale;
   const float slope = s.slopes ? s.slopes[h] : 0.f;
   const int doc = s.docs && held ? s.docs[(size_t)b * C + p] : 0;
+  __syncthreads();
 
-  float m = -INFINITY, l = 0.f, o[N] = {};
-  for (int j0 = lo; j0 < hi; j0 += kGroups * kU) {
-    uint4 kr[kU], vr[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {                         // position p itself comes from the new token
-      const int j = j0 + u * kGroups + group;
-      kr[u] = vr[u] = make_uint4(0, 0, 0, 0);
-      if (j < hi) {
-        const T* k = j == p ? qg + part : kc + (size_t)j * D;
-        const T* v = j == p ? qg + 2 * part : vc + (size_t)j * D;
-        kr[u] = *reinterpret_cast<const uint4*>(k + gl * N);
-        vr[u] = *reinterpret_cast<const uint4*>(v + gl * N);
-        if (j == p) {
-          *reinterpret_cast<uint4*>(kc + (size_t)j * D + gl * N) = kr[u];
-          *reinterpret_cast<uint4*>(vc + (size_t)j * D + gl * N) = vr[u];
-        }
-      }
-    }
-    // Lane gl % kU of the group works out the bias and visibility of the group's row gl % kU.
+  float m = -INFINITY, l = 0.f, o[N] = {};                 // l: of the rows that this lane scored
+  int stage = 0;
+  for (int j0 = lo; j0 < hi; j0 += kStep) {
+    const int next = stage == 0 ? kStages - 1 : stage - 1;
+    request(j0 + (kStages - 1) * kStep, next);             // rows past hi read nothing
+    // Bias and visibility of the lane's row, number gl % kU of the group's.
     const int jb = j0 + (gl % kU) * kGroups + group;
     float bias = -INFINITY;
-    if (jb < hi && (!s.docs || s.docs[(size_t)b * C + jb] == doc))
-      bias = s.table || s.slopes ? score_bias2(s, NH, h, slope, jb - p) : 0.f;
-    float t[kU], mx = m;                                   // a row that is not seen has t = -inf
+    if (jb < hi && (!s.docs || s.docs[(size_t)b * C + jb] == doc)) {
+      bias = -slope * static_cast<float>(p - jb);
+      if (s.table) bias += column[score_bucket(s, jb - p)];
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    const uint32_t at = mine + stage * kStageBytes;
+    float dot[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      float kf[N], dot = 0.f;
-      Vec<T>::widen(kr[u], kf);
+      const uint4 kr = shared16(at + (2 * u) * kThreads * 16);
+      const int j = j0 + u * kGroups + group;
+      if (j == p && j < hi) {                              // (not a later CTA's row past this one's end)
+        *reinterpret_cast<uint4*>(kc + (size_t)j * D + gl * N) = kr;
+        *reinterpret_cast<uint4*>(vc + (size_t)j * D + gl * N) = shared16(at + (2 * u + 1) * kThreads * 16);
+      }
+      float kf[N];
+      Vec<T>::widen(kr, kf);
+      dot[u] = 0.f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) dot = fmaf(q[i], kf[i], dot);
-#pragma unroll
-      for (int off = kLanes / 2; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-      if (s.cap > 0.f) dot = s.cap * tanhf(dot / s.cap);
-      const float bu = __shfl_sync(0xffffffffu, bias, (lane - gl) + u);
-      t[u] = bu == -INFINITY ? -INFINITY : fmaf(dot, kLog2e, bu);
-      mx = fmaxf(mx, t[u]);
+      for (int i = 0; i < N; ++i) dot[u] = fmaf(q[i], kf[i], dot[u]);
     }
-    const float a = weight2(m, mx);
+    const bool up2 = lane & 2, up1 = lane & 1;
+    float k0 = up2 ? dot[2] : dot[0], k1 = up2 ? dot[3] : dot[1];
+    k0 += __shfl_xor_sync(0xffffffffu, up2 ? dot[0] : dot[2], 2);
+    k1 += __shfl_xor_sync(0xffffffffu, up2 ? dot[1] : dot[3], 2);
+    float t = (up1 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, up1 ? k0 : k1, 1);
+#pragma unroll
+    for (int off = 4; off < kLanes; off <<= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+    if (s.cap > 0.f) t = s.cap * tanhf(t / s.cap);
+    // A row that is not seen has t = -inf, whatever its K and V hold.
+    t = bias == -INFINITY ? -INFINITY : (t + bias) * kLog2e;
+    float mx = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+    mx = fmaxf(m, fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)));
+    const float a = weight2(m, mx), w = weight2(t, mx);
     m = mx;
-    l *= a;
+    l = fmaf(l, a, w);
 #pragma unroll
     for (int i = 0; i < N; ++i) o[i] *= a;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      if (t[u] == -INFINITY) continue;                     // whatever its V holds
-      const float w = exp2f(t[u] - m);
+      const float wu = __shfl_sync(0xffffffffu, w, (lane & ~3) | u);
+      if (wu == 0.f) continue;
       float vf[N];
-      Vec<T>::widen(vr[u], vf);
-      l += w;
+      Vec<T>::widen(shared16(at + (2 * u + 1) * kThreads * 16), vf);
 #pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = fmaf(w, vf[i], o[i]);
+      for (int i = 0; i < N; ++i) o[i] = fmaf(wu, vf[i], o[i]);
     }
+    stage = stage == kStages - 1 ? 0 : stage + 1;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  l += __shfl_xor_sync(0xffffffffu, l, 1);
+  l += __shfl_xor_sync(0xffffffffu, l, 2);
   // Groups of a warp.
 #pragma unroll
   for (int off = kLanes; off < 32; off <<= 1) {
@@ -189,13 +238,16 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <typename T, int D>
 cudaError_t step_d(const ScoreArgs& s, const void* qkv, void* cache, const int32_t* len, void* ctx, int ranks,
                    const ScoredShape& sh, cudaStream_t stream) {
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      scored_step_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStages * kStageBytes);
+  if (attr != cudaSuccess) return attr;
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;
   cluster.val.clusterDim.x = (unsigned)ranks;
   cluster.val.clusterDim.y = 1;
   cluster.val.clusterDim.z = 1;
-  return launch_kernel(scored_step_kernel<T, D>, dim3((unsigned)ranks, sh.head_num, sh.batch), dim3(kThreads), 0,
-                       stream, &cluster, 1, s, static_cast<const T*>(qkv), static_cast<T*>(cache), len,
+  return launch_kernel(scored_step_kernel<T, D>, dim3((unsigned)ranks, sh.head_num, sh.batch), dim3(kThreads),
+                       kStages * kStageBytes, stream, &cluster, 1, s, static_cast<const T*>(qkv), static_cast<T*>(cache), len,
                        static_cast<T*>(ctx), sh.batch, sh.seq, sh.head_num);
 }
 
@@ -203,10 +255,11 @@ cudaError_t step_d(const ScoreArgs& s, const void* qkv, void* cache, const int32
 
 cudaError_t launch_scored_step(const ScoreArgs& s, const void* qkv, void* cache, const int32_t* len, void* ctx,
                                const ScoredShape& sh, bool half, int num_sms, cudaStream_t stream) {
-  // Enough CTAs for two per SM, each with at least 64 positions of a full cache; 8 is the portable cluster size.
+  // Four waves of two CTAs per SM, so that sequences of different lengths even out, but at least 128 positions
+  // of a full cache to a CTA; 8 is the portable cluster size.
   const long items = (long)sh.batch * sh.head_num;
   int ranks = 1;
-  while (ranks < 8 && items * ranks < 2L * num_sms && sh.seq >= 128 * ranks) ranks *= 2;
+  while (ranks < 8 && items * ranks < 8L * num_sms && sh.seq >= 256 * ranks) ranks *= 2;
   switch (sh.size_per_head) {
     case 32:
       return half ? step_d<__half, 32>(s, qkv, cache, len, ctx, ranks, sh, stream)

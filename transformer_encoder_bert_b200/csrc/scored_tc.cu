@@ -83,7 +83,8 @@ struct Cfg {
   static constexpr int kNumBars = 2 + 4 * kStages + 4 * TILES;
   static constexpr int kSlot = kBars + kNumBars * 8;
   static constexpr int kDocs = (kSlot + 16 + 15) / 16 * 16;            // per softmax warp: the block's documents
-  static constexpr int kLut = kDocs + TILES * 4 * BN * 4;
+  static constexpr int kColumn = kDocs + TILES * 4 * BN * 4;           // the head's column of the bias table
+  static constexpr int kLut = kColumn + kMaxScoreBuckets * 4;
   static constexpr int kS = 0, kP = TILES * BN, kO = kP + TILES * BN / 2;
   static constexpr int kTmemUsed = kO + TILES * D;
   static constexpr int kTmemCols = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, BN>::kThreads, TILES == 1 ? 2 : 
   auto p_full = [&](int t) { return tile_bars + 8 * (2 * TILES + t); };
   auto o_done = [&](int t) { return tile_bars + 8 * (3 * TILES + t); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kSlot);
+  float* column = reinterpret_cast<float*>(smem + C::kColumn);
   float* lut = reinterpret_cast<float*>(smem + C::kLut);
   uint8_t* cls = reinterpret_cast<uint8_t*>(lut + lut_floats(s, BN));   // documents: 0 skip, 1 whole, 2 mask per element
 
@@ -286,8 +288,8 @@ __global__ void __launch_bounds__(Cfg<D, TILES, BN>::kThreads, TILES == 1 ? 2 : 
     const int i = q0 + 128 * t + r;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t t_s = t_lane + C::kS + t * BN, t_p = t_lane + C::kP + t * (BN / 2), t_o = t_lane + C::kO + t * D;
-    const Bias bias = make_bias(s, lut, NH, h, BN, tid, C::kSoftmaxThreads);
-    asm volatile("bar.sync 1, %0;" ::"n"(C::kSoftmaxThreads) : "memory");
+    const Bias bias = make_bias(s, column, lut, NH, h, BN, -min(q0 + 128 * TILES - 1, n - 1), nbmax * BN - 1 - q0, tid,
+                                C::kSoftmaxThreads);
     const Cap cap = make_cap(s);
     const float scale2 = s.scale * kLog2e;
     const int jlim = i < n ? score_jlim(s, i, n, prefix) : 0;

@@ -97,19 +97,29 @@ __host__ __device__ inline int lut_floats(const ScoreArgs& s, int block) {
   return s.table || s.slopes ? (2 * lut_half(s.table ? s.reach : 0, block) + 1 + 3) / 4 * 4 : 0;
 }
 
-// Filled by `threads` threads (t = 0 ..); a barrier must follow.
-__device__ __forceinline__ Bias make_bias(const ScoreArgs& s, float* lut, int nh, int h, int block, int t,
-                                          int threads) {
+// Called by `threads` threads (t = 0 ..) that share named barrier 1.  Distances outside [rel_min, rel_max] are not
+// filled: no visible key is read there.
+__device__ __forceinline__ Bias make_bias(const ScoreArgs& s, float* column, float* lut, int nh, int h, int block,
+                                          int rel_min, int rel_max, int t, int threads) {
   Bias b;
   b.lut = lut;
   b.reach = s.table ? s.reach : 0;
   b.off = lut_half(b.reach, block);
   const float slope = s.slopes ? s.slopes[h] : 0.f;
   b.slope2 = slope * kLog2e;
-  b.right = s.table ? s.table[(size_t)score_bucket(s, s.reach) * nh + h] * kLog2e : 0.f;
-  b.left = s.table ? s.table[(size_t)score_bucket(s, -s.reach) * nh + h] * kLog2e : 0.f;
-  if (s.table || s.slopes)
-    for (int k = t; k <= 2 * b.off; k += threads) lut[k] = score_bias2(s, nh, h, slope, k - b.off);
+  b.right = b.left = 0.f;
+  if (s.table) {
+    load_column(s, column, nh, h, t, threads);
+    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+    b.right = column[score_bucket(s, s.reach)] * kLog2e;
+    b.left = column[score_bucket(s, -s.reach)] * kLog2e;
+  }
+  if (s.table || s.slopes) {
+    const int last = min(2 * b.off, rel_max + b.off);
+    for (int k = max(0, rel_min + b.off) + t; k <= last; k += threads)
+      lut[k] = score_bias2(s, column, slope, k - b.off);
+    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+  }
   return b;
 }
 

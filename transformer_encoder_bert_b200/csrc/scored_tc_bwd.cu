@@ -60,7 +60,8 @@ struct BCfg {
   static constexpr int kDocs = (kSlot + 16 + 15) / 16 * 16;   // per row warp: the block's documents
   static constexpr int kDiag = kDocs + NB * 4 * kBN * 4;      // dQ: per row warp, finished diagonals
   static constexpr int kSums = kDiag + (MODE == kDQ ? NB * 4 * kBN * 4 : 0);   // dQ: per row warp, bucket sums
-  static constexpr int kLut = kSums + (MODE == kDQ ? NB * 4 * kMaxScoreBuckets * 4 : 0);
+  static constexpr int kColumn = kSums + (MODE == kDQ ? NB * 4 * kMaxScoreBuckets * 4 : 0);   // of the bias table
+  static constexpr int kLut = kColumn + kMaxScoreBuckets * 4;
   static constexpr int kS = 0, kDP = NB * kBN, kAcc = 2 * NB * kBN;
   static constexpr int kTmemUsed = kAcc + (MODE == kDKV ? 2 : 1) * D;
   static constexpr int kTmemCols = kTmemUsed <= 256 ? 256 : 512;
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
   auto p_full = [&](int w) { return buf_bars + 8 * (C::NB + w); };
   auto done = [&](int w) { return buf_bars + 8 * (2 * C::NB + w); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kSlot);
+  float* column = reinterpret_cast<float*>(smem + C::kColumn);
   float* lut = reinterpret_cast<float*>(smem + C::kLut);
   uint8_t* bucket_of = reinterpret_cast<uint8_t*>(lut + lut_floats(s, kBN));   // by distance + reach
   uint8_t* cls = bucket_of + (partial ? 2 * s.reach + 1 : 0);   // documents: 0 skip, 1 whole, 2 mask per element
@@ -366,7 +368,9 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
     const int w = warp >> 2, quad = warp & 3, r = quad * 32 + lane;   // warpgroup; row of the tile = TMEM lane
     const int pos = r0 + r;                                // the row's position
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const Bias bias = make_bias(s, lut, NH, h, kBN, tid, C::kRowThreads);
+    const int c_end = jb1 * kBN - 1, row_end = min(r0 + 127, n - 1);
+    const Bias bias = MODE == kDQ ? make_bias(s, column, lut, NH, h, kBN, -row_end, c_end - r0, tid, C::kRowThreads)
+                                  : make_bias(s, column, lut, NH, h, kBN, r0 - c_end, row_end, tid, C::kRowThreads);
     float* sums = reinterpret_cast<float*>(smem + C::kSums) + warp * kMaxScoreBuckets;
     if (MODE == kDQ && partial) {
       for (int k = tid; k <= 2 * s.reach; k += C::kRowThreads)
