@@ -32,12 +32,8 @@ __host__ __device__ __forceinline__ int score_bucket(const ScoreArgs& s, int rel
   const int exact = nb >> 1;
   int c = a;
   if (a >= exact) {
-    int lo = 0, hi = s.num_bounds;          // how many bounds are <= a
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (s.bounds[mid] <= a) lo = mid + 1; else hi = mid;
-    }
-    c = exact + lo;
+    c = exact;                              // and how many bounds are <= a (the same ones for every lane)
+    for (int k = 0; k < s.num_bounds; ++k) c += s.bounds[k] <= a;
   }
   return c + (s.both && rel > 0 ? nb : 0);
 }

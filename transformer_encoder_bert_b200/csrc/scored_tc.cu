@@ -4,18 +4,24 @@
 // A CTA takes TILES tiles of 128 query rows of one (sequence, head) and walks
 // the blocks of BN keys that some row sees.  Warps:
 //   TILES x 4   softmax: thread r of a tile owns query row r = TMEM lane r
-//   1           one thread issues the MMAs
+//   TILES       one thread per tile issues its MMAs
 //                 S = Q K^T    M = 128, N = BN, both operands in shared memory
 //                 O += P V     M = 128, N = D, K = 16 per step, P read from TMEM
 //   1           one thread issues the TMA loads (Q once; K and V through rings)
-// A softmax thread reads its whole row of S into registers and releases S, so
-// that the next block's S is computed during this block's exponentials; it
-// turns the row into t (scale, cap, bias, masks), takes the maximum, writes
-// P = 2^(t2 - m) as FP16 to its own columns of TMEM and adds up l in FP32.
-// m is a reference maximum: it moves only when a block exceeds it by 2^8, and
-// then the thread scales its row of O first.  O / l does not depend on m.
+// A softmax thread reads its whole row of S into registers, turns it into t
+// (scale, cap, bias, masks), takes the maximum, writes P = 2^(t2 - m) as FP16 to
+// TMEM and adds up l in FP32.  m is a reference maximum: it moves only when a
+// block exceeds it by 2^8, and then the thread scales its row of O first.  O / l
+// does not depend on m.
 //
-// TMEM columns: S [TILES][BN], P [TILES][BN / 2], O [TILES][D].
+// What bounds a block is the softmax, not the products: 8 cycles of the
+// special-function unit a score and warp, and a chain of waits and dependent
+// steps around them.  So the tiles are kept small enough that four share an SM
+// (two CTAs of two, or four of one) for heads up to 64: a tile takes 128 TMEM
+// columns, S [64] and O [64], and P goes over S, whose next product waits for
+// P V; the other three tiles work meanwhile.  With heads of 128, two tiles share
+// an SM, and P has columns of its own, so that the next S is computed during
+// this block's exponentials.
 //
 // Keys hidden by length, causal or prefix masks are a suffix of the row, so a
 // block past every row's limit is not visited and only blocks that a row's limit
@@ -64,63 +70,73 @@ namespace {
 
 constexpr float kRescaleLog2 = 8.f;                // P < 2^8 between moves of the reference maximum
 
-template <int D, int TILES, int BN>
+constexpr int BN = 64;                             // keys of a block
+
+template <int D, int TILES>
 struct Cfg {
+  // P over S's columns where O leaves no room for P beside it if four tiles are to share an SM.
+  static constexpr bool kOverlay = D <= 64;
+  static constexpr int kCtasPerSm = (kOverlay ? 4 : 2) / TILES;
   static constexpr int kSoftmaxThreads = TILES * 128;
-  // Two tiles: the other two warps are filled up to a warpgroup, whose registers the softmax warps take
-  // (a row of 128 scores lives in registers): 2 x 128 x 216 + 128 x 72 = 384 x 168.
-  static constexpr bool kSplitRegs = TILES == 2;
-  static constexpr int kThreads = kSoftmaxThreads + (kSplitRegs ? 128 : 64);
+  static constexpr int kMmaWarp = TILES * 4, kTmaWarp = TILES * 5;
+  // The MMA and TMA warps are filled up to a warpgroup, whose registers the softmax warps take.
+  static constexpr int kThreads = kSoftmaxThreads + 128;
+  static constexpr int kRegs = 65536 / kCtasPerSm / kThreads / 8 * 8;      // a thread at launch
+  static constexpr int kOtherRegs = kOverlay ? 32 : 72;
+  static constexpr int kSoftmaxRegs = (kRegs * kThreads - 128 * kOtherRegs) / kSoftmaxThreads / 8 * 8;
   static constexpr int kSub = D > 64 ? D / 64 : 1;         // 64-column sub-tiles of an operand
   static constexpr int kQBytes = kSub * 128 * 128;
   static constexpr int kKVSub = BN * 128;
   static constexpr int kKVBytes = kSub * kKVSub;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = TILES == 1 ? 2 : 3;
   static constexpr int kK = TILES * kQBytes;
   static constexpr int kV = kK + kStages * kKVBytes;
   static constexpr int kBars = kV + kStages * kKVBytes;
-  // q_full, k_full, k_empty, v_full, v_empty (kStages each), s_full, s_free, p_full, o_done (TILES each), drain
-  static constexpr int kNumBars = 2 + 4 * kStages + 4 * TILES;
+  // q_full, k_full, k_empty, v_full, v_empty (kStages each), s_full, s_free, p_full, o_done, drain (TILES each)
+  static constexpr int kNumBars = 1 + 4 * kStages + 5 * TILES;
   static constexpr int kSlot = kBars + kNumBars * 8;
   static constexpr int kDocs = (kSlot + 16 + 15) / 16 * 16;            // per softmax warp: the block's documents
   static constexpr int kColumn = kDocs + TILES * 4 * BN * 4;           // the head's column of the bias table
   static constexpr int kLut = kColumn + kMaxScoreBuckets * 4;
-  static constexpr int kS = 0, kP = TILES * BN, kO = kP + TILES * BN / 2;
+  // TMEM columns of tile t: S at t * BN, P at kP + t * kPStride, O at kO + t * D.
+  static constexpr int kP = kOverlay ? 0 : TILES * BN, kPStride = kOverlay ? BN : BN / 2;
+  static constexpr int kO = kOverlay ? TILES * BN : kP + TILES * kPStride;
   static constexpr int kTmemUsed = kO + TILES * D;
   static constexpr int kTmemCols = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
-  static_assert(kTmemUsed <= 512, "TMEM");
+  static_assert(kTmemCols * kCtasPerSm <= 512 && kTmemUsed <= kTmemCols, "TMEM");
   static size_t smem(const ScoreArgs& s, int seq) {
     return 1024 + kLut + (size_t)lut_floats(s, BN) * 4 + (s.docs ? (size_t)(seq + BN - 1) / BN : 0);
   }
 };
 
-template <int D, int TILES, int BN>
-__global__ void __launch_bounds__(Cfg<D, TILES, BN>::kThreads, TILES == 1 ? 2 : 1)
+template <int D, int TILES>
+__global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasPerSm)
     scored_tc_kernel(const __grid_constant__ ScoreArgs s, const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_ctx,
                      const int32_t* __restrict__ valid_len, __half* __restrict__ ctx, float* __restrict__ lse, int B,
                      int S, int NH, int* __restrict__ status) {
-  using C = Cfg<D, TILES, BN>;
+  using C = Cfg<D, TILES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = sbase + C::kBars;
-  const uint32_t q_full = bar0, drain = bar0 + 8;
-  auto k_full = [&](int st) { return bar0 + 16 + 8 * st; };
-  auto k_empty = [&](int st) { return bar0 + 16 + 8 * (C::kStages + st); };
-  auto v_full = [&](int st) { return bar0 + 16 + 8 * (2 * C::kStages + st); };
-  auto v_empty = [&](int st) { return bar0 + 16 + 8 * (3 * C::kStages + st); };
-  const uint32_t tile_bars = bar0 + 16 + 32 * C::kStages;
+  const uint32_t q_full = bar0;
+  auto k_full = [&](int st) { return bar0 + 8 + 8 * st; };
+  auto k_empty = [&](int st) { return bar0 + 8 + 8 * (C::kStages + st); };
+  auto v_full = [&](int st) { return bar0 + 8 + 8 * (2 * C::kStages + st); };
+  auto v_empty = [&](int st) { return bar0 + 8 + 8 * (3 * C::kStages + st); };
+  const uint32_t tile_bars = bar0 + 8 + 32 * C::kStages;
   auto s_full = [&](int t) { return tile_bars + 8 * t; };
   auto s_free = [&](int t) { return tile_bars + 8 * (TILES + t); };
   auto p_full = [&](int t) { return tile_bars + 8 * (2 * TILES + t); };
   auto o_done = [&](int t) { return tile_bars + 8 * (3 * TILES + t); };
+  auto drain = [&](int t) { return tile_bars + 8 * (4 * TILES + t); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kSlot);
   float* column = reinterpret_cast<float*>(smem + C::kColumn);
   float* lut = reinterpret_cast<float*>(smem + C::kLut);
   uint8_t* cls = reinterpret_cast<uint8_t*>(lut + lut_floats(s, BN));   // documents: 0 skip, 1 whole, 2 mask per element
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int h = blockIdx.y, b = blockIdx.z;
   const int q0 = (gridDim.x - 1 - blockIdx.x) * (128 * TILES);          // long causal rows first
   const int H = NH * D;
@@ -151,9 +167,13 @@ __global__ void __launch_bounds__(Cfg<D, TILES, BN>::kThreads, TILES == 1 ? 2 : 
       mbar_init(s_free(t), 4);
       mbar_init(p_full(t), 4);
     }
+    for (int st = 0; st < C::kStages; ++st) {
+      mbar_init(k_empty(st), TILES);
+      mbar_init(v_empty(st), TILES);
+    }
     fence_barrier_init();
   }
-  if (warp == TILES * 4) {
+  if (warp == C::kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     tmem_relinquish();
   }
@@ -187,7 +207,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, BN>::kThreads, TILES == 1 ? 2 : 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   pdl_trigger();                                           // after taking TMEM
   auto next_block = [&](int jb) {                          // first block at or after jb that is visited
     if (docs)
@@ -197,8 +217,8 @@ __global__ void __launch_bounds__(Cfg<D, TILES, BN>::kThreads, TILES == 1 ? 2 : 
 
   bool ok = true;
   if (warp >= TILES * 4) {
-    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == TILES * 4 + 1 && lane == 0) {              // TMA
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    if (warp == C::kTmaWarp && lane == 0) {                // TMA
       prefetch_tmap(&tm_q);
       prefetch_tmap(&tm_kv);
       const int bh = b * NH + h, plane = B * NH;
@@ -210,12 +230,12 @@ __global__ void __launch_bounds__(Cfg<D, TILES, BN>::kThreads, TILES == 1 ? 2 : 
       for (int jb = next_block(0); jb < nbmax; jb = next_block(jb + 1), ++it) {
         const int st = it % C::kStages;
         const uint32_t ph = ((it / C::kStages) & 1) ^ 1;
-        if (it >= C::kStages && !(ok = mbar_wait(k_empty(st), ph, kWaitLimitNs))) break;
+        if (it >= C::kStages && !(ok = one_wait(k_empty(st), ph))) break;
         mbar_arrive_expect_tx(k_full(st), C::kKVBytes);
         for (int u = 0; u < C::kSub; ++u)
           tma_load_3d(&tm_kv, sbase + C::kK + st * C::kKVBytes + u * C::kKVSub, k_full(st), 64 * u, jb * BN, plane + bh);
-        if (it >= C::kStages && !(ok = mbar_wait(v_empty(st), ph, kWaitLimitNs))) {
-          mbar_wait(k_full(st), ph ^ 1, kWaitLimitNs);
+        if (it >= C::kStages && !(ok = one_wait(v_empty(st), ph))) {
+          one_wait(k_full(st), ph ^ 1);
           break;
         }
         mbar_arrive_expect_tx(v_full(st), C::kKVBytes);
@@ -224,74 +244,87 @@ __global__ void __launch_bounds__(Cfg<D, TILES, BN>::kThreads, TILES == 1 ? 2 : 
                       2 * plane + bh);
       }
       // Every load has landed before the CTA exits.
-      mbar_wait(q_full, 0, kWaitLimitNs);
+      one_wait(q_full, 0);
       for (int k = it > C::kStages ? it - C::kStages : 0; k < it; ++k) {
-        mbar_wait(k_full(k % C::kStages), (k / C::kStages) & 1, kWaitLimitNs);
-        mbar_wait(v_full(k % C::kStages), (k / C::kStages) & 1, kWaitLimitNs);
+        one_wait(k_full(k % C::kStages), (k / C::kStages) & 1);
+        one_wait(v_full(k % C::kStages), (k / C::kStages) & 1);
       }
-    } else if (warp == TILES * 4 && lane == 0) {           // MMA
+    } else if (warp < C::kTmaWarp) {                       // MMA of tile t
+      const int t = warp - C::kMmaWarp;
+      int nbt = nb[0];
+      if (TILES > 1 && t > 0) nbt = nb[TILES - 1];
+      const int kl = TILES > 1 && t > 0 ? klim[TILES - 1] : klim[0];
       constexpr uint32_t idesc_s = idesc_f16_f32(128, BN);
       constexpr uint32_t idesc_o = idesc_bmn(128, D);
-      auto issue_s = [&](int t, int st) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t u = kk / 4, o = (kk % 4) * 32;
-          mma_f16_ss(tmem + C::kS + t * BN, smem_desc_sw128(sbase + t * C::kQBytes + u * 16384 + o),
-                     smem_desc_sw128(sbase + C::kK + st * C::kKVBytes + u * C::kKVSub + o), idesc_s, kk > 0 ? 1u : 0u);
+      const uint64_t q_desc = smem_desc_sw128(sbase + t * C::kQBytes), k_desc = smem_desc_sw128(sbase + C::kK);
+      const uint64_t v_desc = desc_mn_sw128(sbase + C::kV, C::kKVSub);
+      const uint32_t t_s = tmem + t * BN, t_p = tmem + C::kP + t * C::kPStride, t_o = tmem + C::kO + t * D;
+      // Waits for K of block number `it` and for the columns of S (read, or with P in them, P V done), then issues
+      // S; a tile that is past its last block only releases.
+      auto scores = [&](int it, int st, bool active) {
+        if (!warp_wait(k_full(st), (it / C::kStages) & 1)) return false;
+        if (!active) {
+          if (elect_one()) mbar_arrive(k_empty(st));
+          return true;
         }
-        mma_commit(s_full(t));
-      };
-      int jb = next_block(0);
-      ok = mbar_wait(q_full, 0, kWaitLimitNs) && mbar_wait(k_full(0), 0, kWaitLimitNs);
-      if (ok) {
+        if (it > 0 && !warp_wait(C::kOverlay ? o_done(t) : s_free(t), (it - 1) & 1)) return false;
         tc_fence_after();
-        for (int t = 0; t < TILES; ++t)
-          if (jb < nb[t]) issue_s(t, 0);
-        mma_commit(k_empty(0));
-      }
-      for (int it = 0; ok && jb < nbmax; ++it) {
-        const int nxt = next_block(jb + 1), st = it % C::kStages;
-        if (nxt < nbmax) {
-          const int sn = (it + 1) % C::kStages;
-          if (!(ok = mbar_wait(k_full(sn), ((it + 1) / C::kStages) & 1, kWaitLimitNs))) break;
-          for (int t = 0; t < TILES && ok; ++t)
-            if (nxt < nb[t]) {
-              if (!(ok = mbar_wait(s_free(t), it & 1, kWaitLimitNs))) break;
-              tc_fence_after();
-              issue_s(t, sn);
-            }
-          if (!ok) break;
-          mma_commit(k_empty(sn));
-        }
-        if (!(ok = mbar_wait(v_full(st), (it / C::kStages) & 1, kWaitLimitNs))) break;
-        for (int t = 0; t < TILES && ok; ++t)
-          if (jb < nb[t]) {
-            if (!(ok = mbar_wait(p_full(t), it & 1, kWaitLimitNs))) break;
-            tc_fence_after();
-            const int ksteps = (min(BN, klim[t] - jb * BN) + 15) >> 4;
-            for (int kk = 0; kk < ksteps; ++kk)
-              mma_f16_ts(tmem + C::kO + t * D, tmem + C::kP + t * (BN / 2) + 8 * kk,
-                         desc_mn_sw128(sbase + C::kV + st * C::kKVBytes + kk * 2048, C::kKVSub), idesc_o,
-                         (it > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(o_done(t));
+        if (elect_one()) {
+          const uint64_t k_st = desc_at(k_desc, st * C::kKVBytes);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t u = kk / 4, o = (kk % 4) * 32;
+            mma_f16_ss(t_s, desc_at(q_desc, u * 16384 + o), desc_at(k_st, u * C::kKVSub + o), idesc_s, kk > 0 ? 1u : 0u);
           }
-        if (!ok) break;
-        mma_commit(v_empty(st));
+          mma_commit(s_full(t));
+          mma_commit(k_empty(st));
+        }
+        __syncwarp();
+        return true;
+      };
+      int jb = next_block(0), st = 0;
+      ok = warp_wait(q_full, 0) && scores(0, 0, jb < nbt);
+      for (int it = 0; ok && jb < nbmax; ++it) {
+        const int nxt = next_block(jb + 1), st_next = st + 1 == C::kStages ? 0 : st + 1;
+        if (!C::kOverlay && nxt < nbmax && !(ok = scores(it + 1, st_next, nxt < nbt))) break;
+        if (!(ok = warp_wait(v_full(st), (it / C::kStages) & 1))) break;
+        if (jb < nbt) {
+          if (!(ok = warp_wait(p_full(t), it & 1))) break;
+          tc_fence_after();
+          const int keys = kl - jb * BN;
+          if (elect_one()) {
+            const uint64_t v_st = desc_at(v_desc, st * C::kKVBytes);
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+              if (16 * kk < keys)
+                mma_f16_ts(t_o, t_p + 8 * kk, desc_at(v_st, kk * 2048), idesc_o, it > 0 || kk > 0 ? 1u : 0u);
+            mma_commit(o_done(t));
+            mma_commit(v_empty(st));
+          }
+          __syncwarp();
+        } else if (elect_one()) {
+          mbar_arrive(v_empty(st));
+        }
+        if (C::kOverlay && nxt < nbmax && !(ok = scores(it + 1, st_next, nxt < nbt))) break;
         jb = nxt;
+        st = st_next;
       }
-      mma_commit(drain);                                   // every MMA issued here has completed
-      mbar_wait(drain, 0, kWaitLimitNs);
+      if (elect_one()) mma_commit(drain(t));               // every MMA issued here has completed
+      __syncwarp();
+      warp_wait(drain(t), 0);
     }
   } else {
-    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;   // tile, row of the tile = TMEM lane
     const int i = q0 + 128 * t + r;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t t_s = t_lane + C::kS + t * BN, t_p = t_lane + C::kP + t * (BN / 2), t_o = t_lane + C::kO + t * D;
+    const uint32_t t_s = t_lane + t * BN, t_p = t_lane + C::kP + t * C::kPStride, t_o = t_lane + C::kO + t * D;
     const Bias bias = make_bias(s, column, lut, NH, h, BN, -min(q0 + 128 * TILES - 1, n - 1), nbmax * BN - 1 - q0, tid,
                                 C::kSoftmaxThreads);
     const Cap cap = make_cap(s);
-    const float scale2 = s.scale * kLog2e;
+    const float cap_in2 = 2.f * kLog2e * cap.in;
+    const uint64_t scale2 = f2_pack(s.scale * kLog2e, s.scale * kLog2e), cap_in = f2_pack(cap.in, cap.in);
+    const bool biased = s.table || s.slopes;
     const int jlim = i < n ? score_jlim(s, i, n, prefix) : 0;
     const int i_first = q0 + 128 * t, i_last = i_first + 127;
     // Keys that every valid row of the tile sees (as far as length and causality go).
@@ -300,79 +333,117 @@ __global__ void __launch_bounds__(Cfg<D, TILES, BN>::kThreads, TILES == 1 ? 2 : 
     int* wdocs = reinterpret_cast<int*>(smem + C::kDocs) + warp * BN;
     float m_ref = -INFINITY;
     uint64_t sum2 = 0;                                     // two partial row sums (0.0f, 0.0f)
+    const int nb_mine = TILES == 2 && t == 1 ? nb[TILES - 1] : nb[0];
     int it = 0;
-    for (int jb = next_block(0); jb < nb[t]; jb = next_block(jb + 1), ++it) {
+    for (int jb = next_block(0); jb < nb_mine; jb = next_block(jb + 1), ++it) {
       const int j0 = jb * BN;
       if (!(ok = warp_wait(s_full(t), it & 1))) break;
       tc_fence_after();
-      uint32_t sv[BN / 32][32];
+      uint64_t x[BN / 2];                                  // the row, two scores to a register pair
+      {
+        uint32_t sv[BN / 32][32];
 #pragma unroll
-      for (int c = 0; c < BN / 32; ++c) tmem_ld_32x32b_x32_async(t_s + 32 * c, sv[c]);
+        for (int c = 0; c < BN / 32; ++c) tmem_ld_32x32b_x32_async(t_s + 32 * c, sv[c]);
 #pragma unroll
-      for (int c = 0; c < BN / 32; ++c) tmem_wait_ld(sv[c]);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(s_free(t));
+        for (int c = 0; c < BN / 32; ++c) tmem_wait_ld(sv[c]);
+#pragma unroll
+        for (int k = 0; k < BN; k += 2)
+          x[k / 2] = f2_pack(__uint_as_float(sv[k / 32][k % 32]), __uint_as_float(sv[k / 32][k % 32 + 1]));
+      }
+      if constexpr (!C::kOverlay) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free(t));
+      }
 
-      auto x = [&](int k) -> uint32_t& { return sv[k / 32][k % 32]; };
       // t2 of the row.
-      const bool near = (s.table || s.slopes) && j0 - i_last < bias.reach && j0 + BN - 1 - i_first > -bias.reach;
+      const bool near = biased && j0 - i_last < bias.reach && j0 + BN - 1 - i_first > -bias.reach;
       const bool ahead = j0 - i_last >= bias.reach;
       const float step = ahead ? -bias.slope2 : bias.slope2;
       const float base = (ahead ? bias.right : bias.left) + step * (float)(j0 - i);
       const float* row = bias.lut + bias.off + (j0 - i);   // read only where the block is near
+      uint64_t mul = scale2;                               // t2 = x * mul + bias
       if (cap.on) {
+        float top = 0.f;                                   // (of valid rows and keys, so that no other decides)
+        const int keys = n - j0;
+        if (keys >= BN) {
 #pragma unroll
-        for (int k = 0; k < BN; ++k)
-          x(k) = __float_as_uint(
-              fmaf(-2.f * cap.cap2, rcp(1.f + ex2(__uint_as_float(x(k)) * cap.in)), cap.cap2));
-        if (near) {
+          for (int k = 0; k < BN / 2; ++k) {
+            float a, c;
+            f2_unpack(x[k], a, c);
+            top = fmaxf(fmaxf(top, fabsf(a)), fabsf(c));
+          }
+        } else {
 #pragma unroll
-          for (int k = 0; k < BN; ++k) x(k) = __float_as_uint(__uint_as_float(x(k)) + row[k]);
-        } else if (s.table || s.slopes) {
-#pragma unroll
-          for (int k = 0; k < BN; ++k)
-            x(k) = __float_as_uint(__uint_as_float(x(k)) + fmaf((float)k, step, base));
+          for (int k = 0; k < BN / 2; ++k) {
+            float a, c;
+            f2_unpack(x[k], a, c);
+            top = fmaxf(fmaxf(top, 2 * k < keys ? fabsf(a) : 0.f), 2 * k + 1 < keys ? fabsf(c) : 0.f);
+          }
         }
-      } else if (near) {
+        if (!any_warp(i < n && top * fabsf(cap.in) > kCapPoly)) {
 #pragma unroll
-        for (int k = 0; k < BN; ++k) x(k) = __float_as_uint(fmaf(__uint_as_float(x(k)), scale2, row[k]));
+          for (int k = 0; k < BN / 2; ++k) {
+            const uint64_t y = f2_mul(x[k], cap_in);
+            x[k] = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < BN / 2; ++k) {
+            float a, c;
+            f2_unpack(x[k], a, c);
+            x[k] = f2_pack(tanh_of(a, cap_in2), tanh_of(c, cap_in2));
+          }
+        }
+        mul = f2_pack(cap.cap2, cap.cap2);
+      }
+      if (near) {
+#pragma unroll
+        for (int k = 0; k < BN / 2; ++k) x[k] = f2_fma(x[k], mul, f2_pack(row[2 * k], row[2 * k + 1]));
       } else if (s.slopes) {
 #pragma unroll
-        for (int k = 0; k < BN; ++k)
-          x(k) = __float_as_uint(fmaf(__uint_as_float(x(k)), scale2, fmaf((float)k, step, base)));
+        for (int k = 0; k < BN / 2; ++k)
+          x[k] = f2_fma(x[k], mul, f2_pack(fmaf((float)(2 * k), step, base), fmaf((float)(2 * k + 1), step, base)));
       } else {
-        const float add = s.table ? base : 0.f;
+        const uint64_t add = s.table ? f2_pack(base, base) : 0;   // (0.0f, 0.0f)
 #pragma unroll
-        for (int k = 0; k < BN; ++k) x(k) = __float_as_uint(fmaf(__uint_as_float(x(k)), scale2, add));
+        for (int k = 0; k < BN / 2; ++k) x[k] = f2_fma(x[k], mul, add);
       }
-      if (j0 + BN > jall) {
+      const bool by_doc = docs && cls[jb] == 2;
+      if (j0 + BN > jall || by_doc) {
+        if (by_doc) {
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < BN; c += 32) wdocs[c + lane] = j0 + c + lane < n ? docs[j0 + c + lane] : 0;
+          __syncwarp();
+        }
         const int lim = jlim - j0;
 #pragma unroll
-        for (int k = 0; k < BN; ++k)
-          if (k >= lim) x(k) = __float_as_uint(-INFINITY);
-      }
-      if (docs && cls[jb] == 2) {
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < BN; c += 32) wdocs[c + lane] = j0 + c + lane < n ? docs[j0 + c + lane] : 0;
-        __syncwarp();
-#pragma unroll
         for (int k = 0; k < BN; k += 4) {
-          const int4 dj = *reinterpret_cast<const int4*>(wdocs + k);
-          if (dj.x != doc) x(k) = __float_as_uint(-INFINITY);
-          if (dj.y != doc) x(k + 1) = __float_as_uint(-INFINITY);
-          if (dj.z != doc) x(k + 2) = __float_as_uint(-INFINITY);
-          if (dj.w != doc) x(k + 3) = __float_as_uint(-INFINITY);
+          int4 dj = make_int4(doc, doc, doc, doc);
+          if (by_doc) dj = *reinterpret_cast<const int4*>(wdocs + k);
+          float a, c, e, f;
+          f2_unpack(x[k / 2], a, c);
+          f2_unpack(x[k / 2 + 1], e, f);
+          a = k < lim && dj.x == doc ? a : -INFINITY;
+          c = k + 1 < lim && dj.y == doc ? c : -INFINITY;
+          e = k + 2 < lim && dj.z == doc ? e : -INFINITY;
+          f = k + 3 < lim && dj.w == doc ? f : -INFINITY;
+          x[k / 2] = f2_pack(a, c);
+          x[k / 2 + 1] = f2_pack(e, f);
         }
       }
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int k = 0; k < BN; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(x(k)));
+      for (int k = 0; k < BN / 2; ++k) {
+        float a, c;
+        f2_unpack(x[k], a, c);
+        m4[k & 3] = fmaxf(fmaxf(m4[k & 3], a), c);
+      }
       const float bmax = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
 
-      // P's columns are free, and O is whole, once the previous P V has completed.
-      if (it > 0 && !(ok = warp_wait(o_done(t), (it - 1) & 1))) break;
+      // P's columns are free, and O is whole, once the previous P V has completed (S over P was waited for).
+      if (!C::kOverlay && it > 0 && !(ok = warp_wait(o_done(t), (it - 1) & 1))) break;
       // Until a key has been seen m_ref is -inf, and O and l are zeros.
       const bool moved = bmax > m_ref + kRescaleLog2;
       if (any_warp(moved)) {
@@ -399,7 +470,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, BN>::kThreads, TILES == 1 ? 2 : 
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
           float t0, t1;
-          f2_unpack(f2_add(f2_pack(__uint_as_float(x(c + k)), __uint_as_float(x(c + k + 1))), neg_m2), t0, t1);
+          f2_unpack(f2_add(x[(c + k) / 2], neg_m2), t0, t1);
           const float p0 = ex2(t0), p1 = ex2(t1);
           sum2 = f2_add(sum2, f2_pack(p0, p1));
           pk[k / 2] = half2_of(p0, p1);
@@ -434,7 +505,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES, BN>::kThreads, TILES == 1 ? 2 : 
       // The row as FP16 into the Q tile (its readers, the MMAs of S, have completed), swizzled as the
       // store's box is; then one TMA store per 64 columns of the warp's 32 rows.
       constexpr int kCols = D < 64 ? D : 64, kRowBytes = 2 * kCols;
-      if (it == 0) mbar_wait(q_full, 0, kWaitLimitNs);     // no MMA read Q: its load must have landed
+      if (it == 0) one_wait(q_full, 0);     // no MMA read Q: its load must have landed
       uint8_t* out = smem + t * C::kQBytes;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
@@ -462,24 +533,24 @@ __global__ void __launch_bounds__(Cfg<D, TILES, BN>::kThreads, TILES == 1 ? 2 : 
         bulk_commit_group();
       }
       if (lse && i < S) lse[((size_t)b * NH + h) * S + i] = seen ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
-      if (lane == 0) bulk_wait_group_all();
+      if (lane == 0) bulk_wait_group_read<0>();            // shared memory has been read
     }
   }
 
   if (!ok) atomicCAS(status, 0, kStatusWaitTimeout);
   tc_fence_before();
   __syncthreads();
-  if (warp == TILES * 4) {
+  if (warp == C::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
-template <int D, int TILES, int BN>
+template <int D, int TILES>
 cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, __half* ctx, float* lse,
                      const ScoredShape& sh, int* status, cudaStream_t stream) {
-  using C = Cfg<D, TILES, BN>;
-  static const cudaError_t attr = cudaFuncSetAttribute(scored_tc_kernel<D, TILES, BN>,
+  using C = Cfg<D, TILES>;
+  static const cudaError_t attr = cudaFuncSetAttribute(scored_tc_kernel<D, TILES>,
                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (attr != cudaSuccess) return attr;
   const uint64_t planes = 3ull * sh.batch * sh.head_num;
@@ -489,7 +560,7 @@ cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, _
       !encode_operand_map(&tc, ctx, (uint64_t)sh.head_num * D, sh.seq, sh.batch, D < 64 ? D : 64, 32))
     return cudaErrorInvalidValue;
   const dim3 grid((sh.seq + 128 * TILES - 1) / (128 * TILES), sh.head_num, sh.batch);
-  return launch_kernel(scored_tc_kernel<D, TILES, BN>, grid, dim3(C::kThreads), C::smem(s, sh.seq), stream, nullptr, 0,
+  return launch_kernel(scored_tc_kernel<D, TILES>, grid, dim3(C::kThreads), C::smem(s, sh.seq), stream, nullptr, 0,
                        s, tq, tkv, tc, vl, ctx, lse, sh.batch, sh.seq, sh.head_num, status);
 }
 
@@ -502,14 +573,14 @@ cudaError_t launch_scored_tc(const ScoreArgs& s, const __half* qkv, const int32_
   const bool wide = sh.seq > 128;
   switch (sh.size_per_head) {
     case 32:
-      return wide ? launch_d<32, 2, 128>(s, qkv, valid_len, ctx, lse, sh, status, stream)
-                  : launch_d<32, 1, 64>(s, qkv, valid_len, ctx, lse, sh, status, stream);
+      return wide ? launch_d<32, 2>(s, qkv, valid_len, ctx, lse, sh, status, stream)
+                  : launch_d<32, 1>(s, qkv, valid_len, ctx, lse, sh, status, stream);
     case 64:
-      return wide ? launch_d<64, 2, 128>(s, qkv, valid_len, ctx, lse, sh, status, stream)
-                  : launch_d<64, 1, 64>(s, qkv, valid_len, ctx, lse, sh, status, stream);
+      return wide ? launch_d<64, 2>(s, qkv, valid_len, ctx, lse, sh, status, stream)
+                  : launch_d<64, 1>(s, qkv, valid_len, ctx, lse, sh, status, stream);
     case 128:
-      return wide ? launch_d<128, 2, 64>(s, qkv, valid_len, ctx, lse, sh, status, stream)
-                  : launch_d<128, 1, 64>(s, qkv, valid_len, ctx, lse, sh, status, stream);
+      return wide ? launch_d<128, 2>(s, qkv, valid_len, ctx, lse, sh, status, stream)
+                  : launch_d<128, 1>(s, qkv, valid_len, ctx, lse, sh, status, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -52,6 +52,10 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t mn_by
   d |= static_cast<uint64_t>(2u) << 61;
   return d;
 }
+// A descriptor `bytes` further on (a multiple of 16; the address field does not overflow within shared memory).  An
+// MMA's address costs the issuing thread one addition this way, where forming each descriptor anew took longer than
+// the MMA itself.
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 __host__ __device__ constexpr uint32_t idesc_bmn(int m, int n) { return idesc_f16_f32(m, n) | (1u << 16); }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -68,12 +72,30 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Waits on one lane, result broadcast to the warp.
+// Bounded waits: by every lane of a warp (no divergence, no broadcast; true in all lanes or in none), and by a
+// single thread.  A waiting thread sleeps up to kSleepNs at a time, so that it leaves its issue slots to others.
+constexpr uint32_t kSleepNs = 20000;
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  int got = 0;
-  if ((threadIdx.x & 31) == 0) got = mbar_wait(bar, parity, kWaitLimitNs) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, got, 0) != 0;
+  bool got = mbar_try_wait<kSleepNs>(bar, parity);
+  if (!__all_sync(0xffffffffu, got)) got = mbar_wait<kSleepNs>(bar, parity, kWaitLimitNs);
+  return __all_sync(0xffffffffu, got);
 }
+__device__ __forceinline__ bool one_wait(uint32_t bar, uint32_t parity) {
+  return mbar_wait<kSleepNs>(bar, parity, kWaitLimitNs);
+}
+// One lane of the warp.  The warps that issue MMAs and TMA loads run their loops with all lanes and elect a lane for
+// the instructions alone: descriptors and addresses are then the same in every lane and stay in uniform registers,
+// where a loop run by one lane has to move each operand there first (measured: 60 to 90 cycles an MMA).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 r;\n\t"
+      "elect.sync r|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ bool any_warp(bool p) { return __any_sync(0xffffffffu, p); }
 
 // Distance bias of a 128-row tile of positions against a block of positions.
@@ -123,10 +145,14 @@ __device__ __forceinline__ Bias make_bias(const ScoreArgs& s, float* column, flo
   return b;
 }
 
-// Constants of the cap: tanh(u / cap) = 1 - 2 r, r = 1 / (1 + 2^(s * in)),
-// t2 = cap2 - 2 cap2 r, and the derivative 1 - tanh^2 = 4 r (1 - r).  r comes
-// from ex2 and rcp approximations (relative error about 2^-22), so t is off by
-// about cap * 2^-21.
+// The cap, t2 = cap2 tanh(x) with x = s * in = u / cap.  The exact form,
+// tanh(x) = 1 - 2 / (1 + 2^(2 x log2 e)), costs two special-function operations
+// a score (a quarter of the FMA rate each, besides the softmax's own); where
+// every |x| of a warp's block is at most kCapPoly, a polynomial x P(x^2) does it
+// on the FMA pipe.  P is a least-maximum fit of degree 7, found by reweighted
+// least squares: |x P(x^2) - tanh(x)| <= 3.5e-8, 1.3e-7 with FP32 rounding.  The
+// exact form is off by about 2^-22.
+constexpr float kCapPoly = 1.25f;
 struct Cap {
   float in, cap2;
   bool on;
@@ -134,10 +160,21 @@ struct Cap {
 __device__ __forceinline__ Cap make_cap(const ScoreArgs& s) {
   Cap c;
   c.on = s.cap > 0.f;
-  c.in = c.on ? 2.f * kLog2e * s.scale / s.cap : 0.f;
+  c.in = c.on ? s.scale / s.cap : 0.f;
   c.cap2 = s.cap * kLog2e;
   return c;
 }
+// tanh(x) / x of two scores from x^2, |x| <= kCapPoly.
+__device__ __forceinline__ uint64_t tanh_over_x2(uint64_t z) {
+  constexpr float c[8] = {0.9999995231628418f,  -0.3333173394203186f,  0.13317924737930298f,  -0.0532919205725193f,
+                          0.02024945616722107f, -0.006540181580930948f, 0.0014795474708080292f, -0.0001641625858610496f};
+  uint64_t p = f2_pack(c[7], c[7]);
+#pragma unroll
+  for (int k = 6; k >= 0; --k) p = f2_fma(p, z, f2_pack(c[k], c[k]));
+  return p;
+}
+// tanh(s in) of any size; in2 = 2 in log2 e.
+__device__ __forceinline__ float tanh_of(float s, float in2) { return fmaf(-2.f, rcp(1.f + ex2(s * in2)), 1.f); }
 
 }  // namespace scored_tc
 }  // namespace enc

@@ -119,15 +119,15 @@ __device__ __forceinline__ void row_block(const RowBlock& rb, const Cap& cap, fl
         const float add = NEAR ? base + (MODE == kDQ ? lut[k + q] : lut[-(k + q)]) : fmaf((float)(k + q), rb.step, base);
         float t, r = 0.f;
         if (CAP) {
-          r = rcp(1.f + ex2(s * cap.in));
-          t = fmaf(-2.f * cap.cap2, r, cap.cap2) + add;
+          r = tanh_of(s, 2.f * kLog2e * cap.in);
+          t = fmaf(cap.cap2, r, add);
         } else {
           t = fmaf(s, scale2, add);
         }
         if (MODE == kDKV) t -= nl[q];
         p[q] = ex2(t);
         float dt = p[q] * fmaf(__uint_as_float(dp[k + q]), rb.e, MODE == kDKV ? -dcol[q] : -rb.de);
-        u[q] = CAP ? dt * (4.f * r * (1.f - r)) : dt;
+        u[q] = CAP ? dt * fmaf(-r, r, 1.f) : dt;
         if (MASK) {                                        // (hidden scores may be NaN)
           const bool see = k + q >= lo && k + q < hi && (!rb.docs || djs[q] == rb.doc);
           p[q] = see ? p[q] : 0.f;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
   uint8_t* bucket_of = reinterpret_cast<uint8_t*>(lut + lut_floats(s, kBN));   // by distance + reach
   uint8_t* cls = bucket_of + (partial ? 2 * s.reach + 1 : 0);   // documents: 0 skip, 1 whole, 2 mask per element
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int h = blockIdx.y, b = blockIdx.z;
   const int blk = MODE == kDQ ? gridDim.x - 1 - blockIdx.x : blockIdx.x;    // long causal rows first
   const int r0 = blk * 128;
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   pdl_trigger();                                           // after taking TMEM
   auto next_block = [&](int jb) {
     if (docs)
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
       int it = 0;
       for (int jb = next_block(jb0); jb < jb1; jb = next_block(jb + 1), ++it) {
         const int st = it % C::kStages, c0 = jb * kBN;
-        if (it >= C::kStages && !(ok = mbar_wait(b_empty(st), ((it / C::kStages) & 1) ^ 1, kWaitLimitNs))) break;
+        if (it >= C::kStages && !(ok = one_wait(b_empty(st), ((it / C::kStages) & 1) ^ 1))) break;
         const uint32_t dst = sbase + C::kB + st * C::kStage;
         mbar_arrive_expect_tx(b_full(st), C::kStage + (MODE == kDKV ? C::kColBytes : 0));
         for (int u = 0; u < C::kSub; ++u) {
@@ -307,63 +307,75 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
             bulk_load(sbase + C::kCol + st * C::kColBytes + k * kBN * 4, rows2 + ((size_t)k * planes + bh) * Sp + c0,
                       kBN * 4, b_full(st));
       }
-      mbar_wait(a_full, 0, kWaitLimitNs);                  // every load has landed before the CTA exits
+      one_wait(a_full, 0);                  // every load has landed before the CTA exits
       for (int k = it > C::kStages ? it - C::kStages : 0; k < it; ++k)
-        mbar_wait(b_full(k % C::kStages), (k / C::kStages) & 1, kWaitLimitNs);
+        one_wait(b_full(k % C::kStages), (k / C::kStages) & 1);
     }
-  } else if (warp == C::NB * 4) {
-    if (lane == 0) {                                       // MMA
-      constexpr uint32_t idesc_s = idesc_f16_f32(128, kBN);
-      constexpr uint32_t idesc_o = idesc_bmn(128, D);
-      auto issue_scores = [&](int it) {                    // S and dP of block number `it`
-        const int w = it % C::NB;
-        const uint32_t st = sbase + C::kB + (it % C::kStages) * C::kStage;
+  } else if (warp == C::NB * 4) {                          // MMA
+    constexpr uint32_t idesc_s = idesc_f16_f32(128, kBN);
+    constexpr uint32_t idesc_o = idesc_bmn(128, D);
+    const uint64_t a_desc = smem_desc_sw128(sbase), b_desc = smem_desc_sw128(sbase + C::kB);
+    const uint64_t bt_desc = desc_mn_sw128(sbase + C::kB, C::kBSub);           // the columns' operands, transposed
+    auto issue_scores = [&](int w, int st) {               // S and dP of the block in stage st, for warpgroup w
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t b_st = desc_at(b_desc, st * C::kStage);
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t u = kk / 4, o = (kk % 4) * 32;
-            mma_f16_ss(tmem + (a ? C::kDP : C::kS) + w * kBN, smem_desc_sw128(sbase + a * C::kABytes + u * 16384 + o),
-                       smem_desc_sw128(st + a * C::kBBytes + u * C::kBSub + o), idesc_s, kk > 0 ? 1u : 0u);
+            mma_f16_ss(tmem + (a ? C::kDP : C::kS) + w * kBN, desc_at(a_desc, a * C::kABytes + u * 16384 + o),
+                       desc_at(b_st, a * C::kBBytes + u * C::kBSub + o), idesc_s, kk > 0 ? 1u : 0u);
           }
         mma_commit(s_full(w));
-      };
-      ok = mbar_wait(a_full, 0, kWaitLimitNs);
-      int jb = next_block(jb0), ahead = jb;                // block of `it`, and the next whose scores are not issued
-      int issued = 0;
-      for (; issued < C::NB && ok && ahead < jb1; ++issued) {
-        if (!(ok = mbar_wait(b_full(issued % C::kStages), 0, kWaitLimitNs))) break;
-        tc_fence_after();
-        issue_scores(issued);
+      }
+      __syncwarp();
+    };
+    ok = warp_wait(a_full, 0);
+    int jb = next_block(jb0), ahead = jb;                  // block of `it`, and the next whose scores are not issued
+    int issued = 0, st_issue = 0, st = 0;                  // blocks whose scores are issued; stages of both
+    for (; issued < C::NB && ok && ahead < jb1; ++issued, ++st_issue) {
+      if (!(ok = warp_wait(b_full(st_issue), 0))) break;
+      issue_scores(issued, st_issue);
+      ahead = next_block(ahead + 1);
+    }
+    for (int it = 0; ok && jb < jb1; ++it, jb = next_block(jb + 1)) {
+      const int w = it % C::NB;
+      if (!(ok = warp_wait(p_full(w), (it / C::NB) & 1))) break;
+      tc_fence_after();
+      const int columns = n - jb * kBN;
+      if (elect_one()) {
+        const uint64_t bt = desc_at(bt_desc, st * C::kStage);
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk)
+          if (16 * kk < columns)
+            mma_f16_ts(tmem + C::kAcc, tmem + C::kDP + w * kBN + 8 * kk, desc_at(bt, kk * 2048), idesc_o,
+                       it > 0 || kk > 0 ? 1u : 0u);
+        if (MODE == kDKV) {
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            if (16 * kk < columns)
+              mma_f16_ts(tmem + C::kAcc + D, tmem + C::kS + w * kBN + 8 * kk, desc_at(bt, C::kBBytes + kk * 2048),
+                         idesc_o, it > 0 || kk > 0 ? 1u : 0u);
+        }
+        mma_commit(done(w));
+        mma_commit(b_empty(st));
+      }
+      __syncwarp();
+      if (ahead < jb1) {                                   // S and dP may be overwritten once P and dU have been read
+        if (!(ok = warp_wait(b_full(st_issue), (issued / C::kStages) & 1))) break;
+        if (!(ok = warp_wait(done(w), (it / C::NB) & 1))) break;
+        issue_scores(w, st_issue);
+        ++issued;
+        st_issue = st_issue + 1 == C::kStages ? 0 : st_issue + 1;
         ahead = next_block(ahead + 1);
       }
-      for (int it = 0; ok && jb < jb1; ++it, jb = next_block(jb + 1)) {
-        const int w = it % C::NB;
-        const uint32_t st = sbase + C::kB + (it % C::kStages) * C::kStage;
-        if (!(ok = mbar_wait(p_full(w), (it / C::NB) & 1, kWaitLimitNs))) break;
-        tc_fence_after();
-        const int ksteps = (min(kBN, n - jb * kBN) + 15) >> 4;
-        for (int kk = 0; kk < ksteps; ++kk)
-          mma_f16_ts(tmem + C::kAcc, tmem + C::kDP + w * kBN + 8 * kk, desc_mn_sw128(st + kk * 2048, C::kBSub), idesc_o,
-                     (it > 0 || kk > 0) ? 1u : 0u);
-        if (MODE == kDKV)
-          for (int kk = 0; kk < ksteps; ++kk)
-            mma_f16_ts(tmem + C::kAcc + D, tmem + C::kS + w * kBN + 8 * kk,
-                       desc_mn_sw128(st + C::kBBytes + kk * 2048, C::kBSub), idesc_o, (it > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(done(w));
-        mma_commit(b_empty(it % C::kStages));
-        if (ahead < jb1) {                                 // S and dP may be overwritten once P and dU have been read
-          if (!(ok = mbar_wait(b_full(issued % C::kStages), (issued / C::kStages) & 1, kWaitLimitNs))) break;
-          if (!(ok = mbar_wait(done(w), (it / C::NB) & 1, kWaitLimitNs))) break;
-          tc_fence_after();
-          issue_scores(issued);
-          ++issued;
-          ahead = next_block(ahead + 1);
-        }
-      }
-      mma_commit(drain);                                   // every MMA issued here has completed
-      mbar_wait(drain, 0, kWaitLimitNs);
+      st = st + 1 == C::kStages ? 0 : st + 1;
     }
+    if (elect_one()) mma_commit(drain);                    // every MMA issued here has completed
+    __syncwarp();
+    warp_wait(drain, 0);
   } else {
     const int w = warp >> 2, quad = warp & 3, r = quad * 32 + lane;   // warpgroup; row of the tile = TMEM lane
     const int pos = r0 + r;                                // the row's position
@@ -522,7 +534,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
     // last reader has completed) in the store's swizzle, one TMA store per 64 columns of a warp's 32 rows.
     if (ok)
       for (int k = max(0, it - C::NB); k < it && ok; ++k) ok = warp_wait(done(k % C::NB), (k / C::NB) & 1);
-    if (it == 0) mbar_wait(a_full, 0, kWaitLimitNs);
+    if (it == 0) one_wait(a_full, 0);
     if (ok) {
       tc_fence_after();
       constexpr int kCols = D < 64 ? D : 64, kRowBytes = 2 * kCols;
