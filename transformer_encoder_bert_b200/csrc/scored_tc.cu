@@ -8,20 +8,18 @@
 //                 S = Q K^T    M = 128, N = BN, both operands in shared memory
 //                 O += P V     M = 128, N = D, K = 16 per step, P read from TMEM
 //   1           one thread issues the TMA loads (Q once; K and V through rings)
-// A softmax thread reads its whole row of S into registers, turns it into t
-// (scale, cap, bias, masks), takes the maximum, writes P = 2^(t2 - m) as FP16 to
-// TMEM and adds up l in FP32.  m is a reference maximum: it moves only when a
-// block exceeds it by 2^8, and then the thread scales its row of O first.  O / l
-// does not depend on m.
+// A softmax thread reads its whole row of S into registers and releases S, so
+// that the next block's S is computed during this block's exponentials; it
+// turns the row into t (scale, cap, bias, masks), takes the maximum, writes
+// P = 2^(t2 - m) as FP16 to TMEM and adds up l in FP32.  m is a reference
+// maximum: it moves only when a block exceeds it by 2^8, and then the thread
+// scales its row of O first.  O / l does not depend on m.
 //
 // What bounds a block is the softmax, not the products: 8 cycles of the
 // special-function unit a score and warp, and a chain of waits and dependent
-// steps around them.  So the tiles are kept small enough that four share an SM
-// (two CTAs of two, or four of one) for heads up to 64: a tile takes 128 TMEM
-// columns, S [64] and O [64], and P goes over S, whose next product waits for
-// P V; the other three tiles work meanwhile.  With heads of 128, two tiles share
-// an SM, and P has columns of its own, so that the next S is computed during
-// this block's exponentials.
+// steps around them.  So as many tiles share an SM as TMEM holds: three CTAs of
+// one tile for heads up to 64, one CTA of two tiles (which share K and V) or
+// two of one for heads of 128.
 //
 // Keys hidden by length, causal or prefix masks are a suffix of the row, so a
 // block past every row's limit is not visited and only blocks that a row's limit
@@ -74,21 +72,22 @@ constexpr int BN = 64;                             // keys of a block
 
 template <int D, int TILES>
 struct Cfg {
-  // P over S's columns where O leaves no room for P beside it if four tiles are to share an SM.
-  static constexpr bool kOverlay = D <= 64;
-  static constexpr int kCtasPerSm = (kOverlay ? 4 : 2) / TILES;
+  static constexpr int kCtasPerSm = D > 64 ? 2 / TILES : 3;
   static constexpr int kSoftmaxThreads = TILES * 128;
   static constexpr int kMmaWarp = TILES * 4, kTmaWarp = TILES * 5;
   // The MMA and TMA warps are filled up to a warpgroup, whose registers the softmax warps take.
   static constexpr int kThreads = kSoftmaxThreads + 128;
-  static constexpr int kRegs = 65536 / kCtasPerSm / kThreads / 8 * 8;      // a thread at launch
-  static constexpr int kOtherRegs = kOverlay ? 32 : 72;
-  static constexpr int kSoftmaxRegs = (kRegs * kThreads - 128 * kOtherRegs) / kSoftmaxThreads / 8 * 8;
+  static constexpr int kRegs = 65536 / kCtasPerSm / kThreads / 8 * 8;          // a thread at launch
+  static constexpr int kOtherRegs = D > 64 ? 72 : 40;
+  static constexpr int kSoftmaxRegs =
+      (kRegs * kThreads - 128 * kOtherRegs) / kSoftmaxThreads / 8 * 8 < 216
+          ? (kRegs * kThreads - 128 * kOtherRegs) / kSoftmaxThreads / 8 * 8
+          : 216;
   static constexpr int kSub = D > 64 ? D / 64 : 1;         // 64-column sub-tiles of an operand
   static constexpr int kQBytes = kSub * 128 * 128;
   static constexpr int kKVSub = BN * 128;
   static constexpr int kKVBytes = kSub * kKVSub;
-  static constexpr int kStages = TILES == 1 ? 2 : 3;
+  static constexpr int kStages = D > 64 && TILES == 1 ? 2 : 3;      // two CTAs' shared memory
   static constexpr int kK = TILES * kQBytes;
   static constexpr int kV = kK + kStages * kKVBytes;
   static constexpr int kBars = kV + kStages * kKVBytes;
@@ -98,18 +97,165 @@ struct Cfg {
   static constexpr int kDocs = (kSlot + 16 + 15) / 16 * 16;            // per softmax warp: the block's documents
   static constexpr int kColumn = kDocs + TILES * 4 * BN * 4;           // the head's column of the bias table
   static constexpr int kLut = kColumn + kMaxScoreBuckets * 4;
-  // TMEM columns of tile t: S at t * BN, P at kP + t * kPStride, O at kO + t * D.
-  static constexpr int kP = kOverlay ? 0 : TILES * BN, kPStride = kOverlay ? BN : BN / 2;
-  static constexpr int kO = kOverlay ? TILES * BN : kP + TILES * kPStride;
+  // TMEM columns of tile t: S at t * BN, O at kO + t * D, P at kP + t * BN / 2; for heads of 64 P is an allocation
+  // of its own, as 128 + 32 columns fit an SM three times where 160 would be rounded up to 256.
+  static constexpr bool kOwnP = D == 64;
+  static constexpr int kP = kOwnP ? 0 : TILES * BN, kO = kP + (kOwnP ? BN : TILES * BN / 2);
   static constexpr int kTmemUsed = kO + TILES * D;
   static constexpr int kTmemCols = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
-  static_assert(kTmemCols * kCtasPerSm <= 512 && kTmemUsed <= kTmemCols, "TMEM");
+  static_assert(!kOwnP || TILES == 1, "one tile");
+  static_assert((kTmemCols + (kOwnP ? 32 : 0)) * kCtasPerSm <= 512 && kTmemUsed <= kTmemCols, "TMEM");
   static size_t smem(const ScoreArgs& s, int seq) {
     return 1024 + kLut + (size_t)lut_floats(s, BN) * 4 + (s.docs ? (size_t)(seq + BN - 1) / BN : 0);
   }
 };
 
-template <int D, int TILES>
+// One row's block of BN keys: from S in TMEM to P in TMEM, the reference maximum
+// and the row's sum.  BIAS 0: none; 1: base; 2: base + step * column; 3: from the
+// table in shared memory.  Every variant is a body of its own from the load to the store:
+// with the row in registers, each place where two ways of preparing it join costs
+// moves of the whole row (measured with heads of 64 and 1024 keys, no bias: 456 us
+// with branches inside one body, 265 us without them).
+struct SoftmaxBlock {
+  uint32_t t_s, t_p, t_o;   // TMEM addresses of the row's S, P and O
+  uint32_t s_free, o_done;  // barriers: S has been read; P V is done
+  int it;                   // blocks before this one
+  uint64_t scale2, cap2;    // pairs: of the scores; cap log2 e
+  float cap_in;
+  float base, step;
+  const float* lut;         // at column 0
+  int lim;                  // visible columns, as far as length and causality go
+  const int* docs;          // documents of the columns (shared memory), or nullptr
+  int doc;
+  int keys;                 // columns that are valid keys (any number)
+  bool mine;                // the row is a valid query
+};
+
+template <int D, bool CAP, int BIAS, bool MASK>
+__device__ __forceinline__ bool softmax_block(const SoftmaxBlock& sb, int lane, float& m_ref, uint64_t& sum2) {
+  uint64_t x[BN / 2];                                      // the row, two scores to a register pair
+  {
+    uint32_t sv[BN / 32][32];
+#pragma unroll
+    for (int c = 0; c < BN / 32; ++c) tmem_ld_32x32b_x32_async(sb.t_s + 32 * c, sv[c]);
+#pragma unroll
+    for (int c = 0; c < BN / 32; ++c) tmem_wait_ld(sv[c]);
+#pragma unroll
+    for (int k = 0; k < BN; k += 2)
+      x[k / 2] = f2_pack(__uint_as_float(sv[k / 32][k % 32]), __uint_as_float(sv[k / 32][k % 32 + 1]));
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(sb.s_free);
+
+  // t2 of the row: x * mul + bias.
+  if constexpr (CAP) {
+    float top = 0.f;                                       // (of valid rows and keys, so that no other decides)
+#pragma unroll
+    for (int k = 0; k < BN / 2; ++k) {
+      float a, c;
+      f2_unpack(x[k], a, c);
+      if (MASK) {
+        a = 2 * k < sb.keys ? a : 0.f;
+        c = 2 * k + 1 < sb.keys ? c : 0.f;
+      }
+      top = fmaxf(fmaxf(top, fabsf(a)), fabsf(c));
+    }
+    const uint64_t in = f2_pack(sb.cap_in, sb.cap_in);
+    const bool small = !any_warp(sb.mine && top * fabsf(sb.cap_in) > kCapPoly);
+    if (small) {
+#pragma unroll
+      for (int k = 0; k < BN / 2; ++k) {
+        const uint64_t y = f2_mul(x[k], in);
+        x[k] = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
+      }
+    } else {
+      const float in2 = 2.f * kLog2e * sb.cap_in;
+#pragma unroll
+      for (int k = 0; k < BN / 2; ++k) {
+        float a, c;
+        f2_unpack(x[k], a, c);
+        x[k] = f2_pack(tanh_of(a, in2), tanh_of(c, in2));
+      }
+    }
+  }
+  const uint64_t mul = CAP ? sb.cap2 : sb.scale2;
+#pragma unroll
+  for (int k = 0; k < BN / 2; ++k) {
+    if (BIAS == 0)
+      x[k] = f2_mul(x[k], mul);
+    else if (BIAS == 1)
+      x[k] = f2_fma(x[k], mul, f2_pack(sb.base, sb.base));
+    else if (BIAS == 2)
+      x[k] = f2_fma(x[k], mul, f2_pack(fmaf((float)(2 * k), sb.step, sb.base), fmaf((float)(2 * k + 1), sb.step, sb.base)));
+    else
+      x[k] = f2_fma(x[k], mul, f2_pack(sb.lut[2 * k], sb.lut[2 * k + 1]));
+  }
+  if constexpr (MASK) {
+#pragma unroll
+    for (int k = 0; k < BN; k += 4) {
+      int4 dj = make_int4(sb.doc, sb.doc, sb.doc, sb.doc);
+      if (sb.docs) dj = *reinterpret_cast<const int4*>(sb.docs + k);
+      float a, c, e, f;
+      f2_unpack(x[k / 2], a, c);
+      f2_unpack(x[k / 2 + 1], e, f);
+      a = k < sb.lim && dj.x == sb.doc ? a : -INFINITY;
+      c = k + 1 < sb.lim && dj.y == sb.doc ? c : -INFINITY;
+      e = k + 2 < sb.lim && dj.z == sb.doc ? e : -INFINITY;
+      f = k + 3 < sb.lim && dj.w == sb.doc ? f : -INFINITY;
+      x[k / 2] = f2_pack(a, c);
+      x[k / 2 + 1] = f2_pack(e, f);
+    }
+  }
+  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int k = 0; k < BN / 2; ++k) {
+    float a, c;
+    f2_unpack(x[k], a, c);
+    m4[k & 3] = fmaxf(fmaxf(m4[k & 3], a), c);
+  }
+  const float bmax = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+
+  // P's columns are free, and O is whole, once the previous P V has completed.
+  if (sb.it > 0 && !warp_wait(sb.o_done, (sb.it - 1) & 1)) return false;
+  // Until a key has been seen m_ref is -inf, and O and l are zeros.
+  const bool moved = bmax > m_ref + kRescaleLog2;
+  if (any_warp(moved)) {
+    const float alpha = moved ? ex2(m_ref - bmax) : 1.f;
+    if (moved) m_ref = bmax;
+    if (sb.it > 0) {
+      tc_fence_after();
+      uint32_t oa[32];
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        tmem_ld_32x32b_x32(sb.t_o + c, oa);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) oa[k] = __float_as_uint(__uint_as_float(oa[k]) * alpha);
+        tmem_st_32x32b_x32(sb.t_o + c, oa);
+      }
+    }
+    sum2 = f2_mul(sum2, f2_pack(alpha, alpha));
+  }
+  const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+  const uint64_t neg_m2 = f2_pack(-mu, -mu);
+#pragma unroll
+  for (int c = 0; c < BN; c += 32) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      float t0, t1;
+      f2_unpack(f2_add(x[(c + k) / 2], neg_m2), t0, t1);
+      const float p0 = ex2(t0), p1 = ex2(t1);
+      sum2 = f2_add(sum2, f2_pack(p0, p1));
+      pk[k / 2] = half2_of(p0, p1);
+    }
+    tmem_st_32x32b_x16_async(sb.t_p + c / 2, pk);
+  }
+  return true;
+}
+
+// CAP: scores are capped.  BIAS 0: none; 1: a table; 2: slopes, with or without a table.
+template <int D, int TILES, bool CAP, int BIAS>
 __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasPerSm)
     scored_tc_kernel(const __grid_constant__ ScoreArgs s, const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_ctx,
@@ -175,6 +321,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasP
   }
   if (warp == C::kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    if constexpr (C::kOwnP) tmem_alloc(smem_u32(tmem_slot) + 4, 32);
     tmem_relinquish();
   }
   const int32_t* docs = s.docs ? s.docs + (size_t)b * S : nullptr;
@@ -207,7 +354,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasP
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = uniform(*tmem_slot);
+  const uint32_t tmem = uniform(tmem_slot[0]), tmem_p = C::kOwnP ? uniform(tmem_slot[1]) : tmem + C::kP;
   pdl_trigger();                                           // after taking TMEM
   auto next_block = [&](int jb) {                          // first block at or after jb that is visited
     if (docs)
@@ -258,16 +405,15 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasP
       constexpr uint32_t idesc_o = idesc_bmn(128, D);
       const uint64_t q_desc = smem_desc_sw128(sbase + t * C::kQBytes), k_desc = smem_desc_sw128(sbase + C::kK);
       const uint64_t v_desc = desc_mn_sw128(sbase + C::kV, C::kKVSub);
-      const uint32_t t_s = tmem + t * BN, t_p = tmem + C::kP + t * C::kPStride, t_o = tmem + C::kO + t * D;
-      // Waits for K of block number `it` and for the columns of S (read, or with P in them, P V done), then issues
-      // S; a tile that is past its last block only releases.
+      const uint32_t t_s = tmem + t * BN, t_p = tmem_p + t * (BN / 2), t_o = tmem + C::kO + t * D;
+      // Waits for K of block number `it` and for S's columns to have been read, then issues S; a tile that is past its last block only releases.
       auto scores = [&](int it, int st, bool active) {
         if (!warp_wait(k_full(st), (it / C::kStages) & 1)) return false;
         if (!active) {
           if (elect_one()) mbar_arrive(k_empty(st));
           return true;
         }
-        if (it > 0 && !warp_wait(C::kOverlay ? o_done(t) : s_free(t), (it - 1) & 1)) return false;
+        if (it > 0 && !warp_wait(s_free(t), (it - 1) & 1)) return false;
         tc_fence_after();
         if (elect_one()) {
           const uint64_t k_st = desc_at(k_desc, st * C::kKVBytes);
@@ -286,7 +432,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasP
       ok = warp_wait(q_full, 0) && scores(0, 0, jb < nbt);
       for (int it = 0; ok && jb < nbmax; ++it) {
         const int nxt = next_block(jb + 1), st_next = st + 1 == C::kStages ? 0 : st + 1;
-        if (!C::kOverlay && nxt < nbmax && !(ok = scores(it + 1, st_next, nxt < nbt))) break;
+        if (nxt < nbmax && !(ok = scores(it + 1, st_next, nxt < nbt))) break;
         if (!(ok = warp_wait(v_full(st), (it / C::kStages) & 1))) break;
         if (jb < nbt) {
           if (!(ok = warp_wait(p_full(t), it & 1))) break;
@@ -305,7 +451,6 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasP
         } else if (elect_one()) {
           mbar_arrive(v_empty(st));
         }
-        if (C::kOverlay && nxt < nbmax && !(ok = scores(it + 1, st_next, nxt < nbt))) break;
         jb = nxt;
         st = st_next;
       }
@@ -317,19 +462,26 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasP
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;   // tile, row of the tile = TMEM lane
     const int i = q0 + 128 * t + r;
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t t_s = t_lane + t * BN, t_p = t_lane + C::kP + t * C::kPStride, t_o = t_lane + C::kO + t * D;
+    const uint32_t lane_bits = static_cast<uint32_t>((warp & 3) * 32) << 16, t_lane = tmem + lane_bits;
+    const uint32_t t_s = t_lane + t * BN, t_p = tmem_p + lane_bits + t * (BN / 2), t_o = t_lane + C::kO + t * D;
     const Bias bias = make_bias(s, column, lut, NH, h, BN, -min(q0 + 128 * TILES - 1, n - 1), nbmax * BN - 1 - q0, tid,
                                 C::kSoftmaxThreads);
     const Cap cap = make_cap(s);
-    const float cap_in2 = 2.f * kLog2e * cap.in;
-    const uint64_t scale2 = f2_pack(s.scale * kLog2e, s.scale * kLog2e), cap_in = f2_pack(cap.in, cap.in);
-    const bool biased = s.table || s.slopes;
     const int jlim = i < n ? score_jlim(s, i, n, prefix) : 0;
     const int i_first = q0 + 128 * t, i_last = i_first + 127;
     // Keys that every valid row of the tile sees (as far as length and causality go).
     const int jall = i_first < n ? score_jlim(s, i_first, n, prefix) : 0;
-    const int doc = docs && i < n ? docs[i] : 0;
+    SoftmaxBlock sb;
+    sb.t_s = t_s;
+    sb.t_p = t_p;
+    sb.t_o = t_o;
+    sb.s_free = s_free(t);
+    sb.o_done = o_done(t);
+    sb.scale2 = f2_pack(s.scale * kLog2e, s.scale * kLog2e);
+    sb.cap2 = f2_pack(cap.cap2, cap.cap2);
+    sb.cap_in = cap.in;
+    sb.doc = docs && i < n ? docs[i] : 0;
+    sb.mine = i < n;
     int* wdocs = reinterpret_cast<int*>(smem + C::kDocs) + warp * BN;
     float m_ref = -INFINITY;
     uint64_t sum2 = 0;                                     // two partial row sums (0.0f, 0.0f)
@@ -339,144 +491,32 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasP
       const int j0 = jb * BN;
       if (!(ok = warp_wait(s_full(t), it & 1))) break;
       tc_fence_after();
-      uint64_t x[BN / 2];                                  // the row, two scores to a register pair
-      {
-        uint32_t sv[BN / 32][32];
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) tmem_ld_32x32b_x32_async(t_s + 32 * c, sv[c]);
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) tmem_wait_ld(sv[c]);
-#pragma unroll
-        for (int k = 0; k < BN; k += 2)
-          x[k / 2] = f2_pack(__uint_as_float(sv[k / 32][k % 32]), __uint_as_float(sv[k / 32][k % 32 + 1]));
-      }
-      if constexpr (!C::kOverlay) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free(t));
-      }
-
-      // t2 of the row.
-      const bool near = biased && j0 - i_last < bias.reach && j0 + BN - 1 - i_first > -bias.reach;
+      // How the block is biased and masked.
+      sb.it = it;
+      const bool near = BIAS && j0 - i_last < bias.reach && j0 + BN - 1 - i_first > -bias.reach;
       const bool ahead = j0 - i_last >= bias.reach;
-      const float step = ahead ? -bias.slope2 : bias.slope2;
-      const float base = (ahead ? bias.right : bias.left) + step * (float)(j0 - i);
-      const float* row = bias.lut + bias.off + (j0 - i);   // read only where the block is near
-      uint64_t mul = scale2;                               // t2 = x * mul + bias
-      if (cap.on) {
-        float top = 0.f;                                   // (of valid rows and keys, so that no other decides)
-        const int keys = n - j0;
-        if (keys >= BN) {
-#pragma unroll
-          for (int k = 0; k < BN / 2; ++k) {
-            float a, c;
-            f2_unpack(x[k], a, c);
-            top = fmaxf(fmaxf(top, fabsf(a)), fabsf(c));
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < BN / 2; ++k) {
-            float a, c;
-            f2_unpack(x[k], a, c);
-            top = fmaxf(fmaxf(top, 2 * k < keys ? fabsf(a) : 0.f), 2 * k + 1 < keys ? fabsf(c) : 0.f);
-          }
-        }
-        if (!any_warp(i < n && top * fabsf(cap.in) > kCapPoly)) {
-#pragma unroll
-          for (int k = 0; k < BN / 2; ++k) {
-            const uint64_t y = f2_mul(x[k], cap_in);
-            x[k] = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < BN / 2; ++k) {
-            float a, c;
-            f2_unpack(x[k], a, c);
-            x[k] = f2_pack(tanh_of(a, cap_in2), tanh_of(c, cap_in2));
-          }
-        }
-        mul = f2_pack(cap.cap2, cap.cap2);
-      }
-      if (near) {
-#pragma unroll
-        for (int k = 0; k < BN / 2; ++k) x[k] = f2_fma(x[k], mul, f2_pack(row[2 * k], row[2 * k + 1]));
-      } else if (s.slopes) {
-#pragma unroll
-        for (int k = 0; k < BN / 2; ++k)
-          x[k] = f2_fma(x[k], mul, f2_pack(fmaf((float)(2 * k), step, base), fmaf((float)(2 * k + 1), step, base)));
-      } else {
-        const uint64_t add = s.table ? f2_pack(base, base) : 0;   // (0.0f, 0.0f)
-#pragma unroll
-        for (int k = 0; k < BN / 2; ++k) x[k] = f2_fma(x[k], mul, add);
-      }
+      sb.step = ahead ? -bias.slope2 : bias.slope2;
+      sb.base = (ahead ? bias.right : bias.left) + sb.step * (float)(j0 - i);
+      sb.lut = bias.lut + bias.off + (j0 - i);
+      sb.lim = jlim - j0;
+      sb.keys = n - j0;
       const bool by_doc = docs && cls[jb] == 2;
-      if (j0 + BN > jall || by_doc) {
-        if (by_doc) {
-          __syncwarp();
+      sb.docs = nullptr;
+      if (by_doc) {
+        __syncwarp();
 #pragma unroll
-          for (int c = 0; c < BN; c += 32) wdocs[c + lane] = j0 + c + lane < n ? docs[j0 + c + lane] : 0;
-          __syncwarp();
-        }
-        const int lim = jlim - j0;
-#pragma unroll
-        for (int k = 0; k < BN; k += 4) {
-          int4 dj = make_int4(doc, doc, doc, doc);
-          if (by_doc) dj = *reinterpret_cast<const int4*>(wdocs + k);
-          float a, c, e, f;
-          f2_unpack(x[k / 2], a, c);
-          f2_unpack(x[k / 2 + 1], e, f);
-          a = k < lim && dj.x == doc ? a : -INFINITY;
-          c = k + 1 < lim && dj.y == doc ? c : -INFINITY;
-          e = k + 2 < lim && dj.z == doc ? e : -INFINITY;
-          f = k + 3 < lim && dj.w == doc ? f : -INFINITY;
-          x[k / 2] = f2_pack(a, c);
-          x[k / 2 + 1] = f2_pack(e, f);
-        }
+        for (int c = 0; c < BN; c += 32) wdocs[c + lane] = j0 + c + lane < n ? docs[j0 + c + lane] : 0;
+        __syncwarp();
+        sb.docs = wdocs;
       }
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int k = 0; k < BN / 2; ++k) {
-        float a, c;
-        f2_unpack(x[k], a, c);
-        m4[k & 3] = fmaxf(fmaxf(m4[k & 3], a), c);
-      }
-      const float bmax = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-
-      // P's columns are free, and O is whole, once the previous P V has completed (S over P was waited for).
-      if (!C::kOverlay && it > 0 && !(ok = warp_wait(o_done(t), (it - 1) & 1))) break;
-      // Until a key has been seen m_ref is -inf, and O and l are zeros.
-      const bool moved = bmax > m_ref + kRescaleLog2;
-      if (any_warp(moved)) {
-        const float alpha = moved ? ex2(m_ref - bmax) : 1.f;
-        if (moved) m_ref = bmax;
-        if (it > 0) {
-          tc_fence_after();
-          uint32_t oa[32];
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            tmem_ld_32x32b_x32(t_o + c, oa);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) oa[k] = __float_as_uint(__uint_as_float(oa[k]) * alpha);
-            tmem_st_32x32b_x32(t_o + c, oa);
-          }
-        }
-        sum2 = f2_mul(sum2, f2_pack(alpha, alpha));
-      }
-      const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-      const uint64_t neg_m2 = f2_pack(-mu, -mu);
-#pragma unroll
-      for (int c = 0; c < BN; c += 32) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          float t0, t1;
-          f2_unpack(f2_add(x[(c + k) / 2], neg_m2), t0, t1);
-          const float p0 = ex2(t0), p1 = ex2(t1);
-          sum2 = f2_add(sum2, f2_pack(p0, p1));
-          pk[k / 2] = half2_of(p0, p1);
-        }
-        tmem_st_32x32b_x16_async(t_p + c / 2, pk);
-      }
+      const bool mask = j0 + BN > jall || by_doc;
+      if (BIAS && near)
+        ok = mask ? softmax_block<D, CAP, BIAS ? 3 : 0, true>(sb, lane, m_ref, sum2)
+                  : softmax_block<D, CAP, BIAS ? 3 : 0, false>(sb, lane, m_ref, sum2);
+      else
+        ok = mask ? softmax_block<D, CAP, BIAS, true>(sb, lane, m_ref, sum2)
+                  : softmax_block<D, CAP, BIAS, false>(sb, lane, m_ref, sum2);
+      if (!ok) break;
       // V rows of keys in [n, n rounded up to 16) are read by P V: zeros, whatever memory holds there.
       const int lim = n - j0, lim16 = (min(BN, klim[t] - j0) + 15) & ~15;
       if (lim < lim16 && (warp & 3) == 0) {
@@ -543,14 +583,15 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasP
   if (warp == C::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
+    if constexpr (C::kOwnP) tmem_dealloc(tmem_p, 32);
   }
 }
 
-template <int D, int TILES>
-cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, __half* ctx, float* lse,
+template <int D, int TILES, bool CAP, int BIAS>
+cudaError_t launch_v(const ScoreArgs& s, const __half* qkv, const int32_t* vl, __half* ctx, float* lse,
                      const ScoredShape& sh, int* status, cudaStream_t stream) {
   using C = Cfg<D, TILES>;
-  static const cudaError_t attr = cudaFuncSetAttribute(scored_tc_kernel<D, TILES>,
+  static const cudaError_t attr = cudaFuncSetAttribute(scored_tc_kernel<D, TILES, CAP, BIAS>,
                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (attr != cudaSuccess) return attr;
   const uint64_t planes = 3ull * sh.batch * sh.head_num;
@@ -560,8 +601,20 @@ cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, _
       !encode_operand_map(&tc, ctx, (uint64_t)sh.head_num * D, sh.seq, sh.batch, D < 64 ? D : 64, 32))
     return cudaErrorInvalidValue;
   const dim3 grid((sh.seq + 128 * TILES - 1) / (128 * TILES), sh.head_num, sh.batch);
-  return launch_kernel(scored_tc_kernel<D, TILES>, grid, dim3(C::kThreads), C::smem(s, sh.seq), stream, nullptr, 0,
-                       s, tq, tkv, tc, vl, ctx, lse, sh.batch, sh.seq, sh.head_num, status);
+  return launch_kernel(scored_tc_kernel<D, TILES, CAP, BIAS>, grid, dim3(C::kThreads), C::smem(s, sh.seq), stream,
+                       nullptr, 0, s, tq, tkv, tc, vl, ctx, lse, sh.batch, sh.seq, sh.head_num, status);
+}
+
+template <int D, int TILES>
+cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, __half* ctx, float* lse,
+                     const ScoredShape& sh, int* status, cudaStream_t stream) {
+  if (s.cap > 0.f)
+    return s.slopes  ? launch_v<D, TILES, true, 2>(s, qkv, vl, ctx, lse, sh, status, stream)
+           : s.table ? launch_v<D, TILES, true, 1>(s, qkv, vl, ctx, lse, sh, status, stream)
+                     : launch_v<D, TILES, true, 0>(s, qkv, vl, ctx, lse, sh, status, stream);
+  return s.slopes  ? launch_v<D, TILES, false, 2>(s, qkv, vl, ctx, lse, sh, status, stream)
+         : s.table ? launch_v<D, TILES, false, 1>(s, qkv, vl, ctx, lse, sh, status, stream)
+                   : launch_v<D, TILES, false, 0>(s, qkv, vl, ctx, lse, sh, status, stream);
 }
 
 }  // namespace
@@ -570,17 +623,12 @@ cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, _
 cudaError_t launch_scored_tc(const ScoreArgs& s, const __half* qkv, const int32_t* valid_len, __half* ctx, float* lse,
                              const ScoredShape& sh, int* status, cudaStream_t stream) {
   using namespace scored_tc;
-  const bool wide = sh.seq > 128;
   switch (sh.size_per_head) {
-    case 32:
-      return wide ? launch_d<32, 2>(s, qkv, valid_len, ctx, lse, sh, status, stream)
-                  : launch_d<32, 1>(s, qkv, valid_len, ctx, lse, sh, status, stream);
-    case 64:
-      return wide ? launch_d<64, 2>(s, qkv, valid_len, ctx, lse, sh, status, stream)
-                  : launch_d<64, 1>(s, qkv, valid_len, ctx, lse, sh, status, stream);
+    case 32: return launch_d<32, 1>(s, qkv, valid_len, ctx, lse, sh, status, stream);
+    case 64: return launch_d<64, 1>(s, qkv, valid_len, ctx, lse, sh, status, stream);
     case 128:
-      return wide ? launch_d<128, 2>(s, qkv, valid_len, ctx, lse, sh, status, stream)
-                  : launch_d<128, 1>(s, qkv, valid_len, ctx, lse, sh, status, stream);
+      return sh.seq > 128 ? launch_d<128, 2>(s, qkv, valid_len, ctx, lse, sh, status, stream)
+                          : launch_d<128, 1>(s, qkv, valid_len, ctx, lse, sh, status, stream);
   }
   return cudaErrorInvalidValue;
 }
