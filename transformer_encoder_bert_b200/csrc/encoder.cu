@@ -315,7 +315,10 @@ enc_status step_scored(enc_handle* h, const enc::ScoreArgs& s, const void* qkv, 
                        float* lse, int batch, int seq, cudaStream_t st) {
   const enc::ScoredShape sh{batch, seq, h->nh, h->d};
   cudaError_t e;
-  if (h->dtype == ENC_FP16 && h->tc_attn)
+  if (h->dtype == ENC_FP16 && h->tc_attn && seq <= enc::kScoredShort)
+    e = enc::launch_scored_tc_short(s, static_cast<const __half*>(qkv), vl, static_cast<__half*>(ctx), lse, sh,
+                                    h->status, h->num_sms, st);
+  else if (h->dtype == ENC_FP16 && h->tc_attn)
     e = enc::launch_scored_tc(s, static_cast<const __half*>(qkv), vl, static_cast<__half*>(ctx), lse, sh, h->status, st);
   else
     e = enc::launch_scored_simt(s, qkv, vl, ctx, lse, sh, h->dtype == ENC_FP16, st);

@@ -237,6 +237,10 @@ cudaError_t launch_scored_simt(const ScoreArgs& s, const void* qkv, const int32_
 // The same on the tensor cores, FP16 (scored_tc.cu).
 cudaError_t launch_scored_tc(const ScoreArgs& s, const __half* qkv, const int32_t* valid_len, __half* ctx, float* lse,
                              const ScoredShape& sh, int* status, cudaStream_t stream);
+// The same for seq <= kScoredShort: one block of keys, persistent CTAs (scored_tc_short.cu).
+constexpr int kScoredShort = 128;
+cudaError_t launch_scored_tc_short(const ScoreArgs& s, const __half* qkv, const int32_t* valid_len, __half* ctx,
+                                   float* lse, const ScoredShape& sh, int* status, int num_sms, cudaStream_t stream);
 // Row sums D_i = dctx_i . ctx_i (0 for i >= n) -> rowsum [B, nh, S].
 cudaError_t launch_scored_rowsum(const void* ctx, const void* dctx, const int32_t* valid_len, float* rowsum,
                                  const ScoredShape& sh, bool half, cudaStream_t stream);

@@ -33,6 +33,7 @@ __host__ __device__ __forceinline__ int score_bucket(const ScoreArgs& s, int rel
   int c = a;
   if (a >= exact) {
     c = exact;                              // and how many bounds are <= a (the same ones for every lane)
+#pragma unroll 8
     for (int k = 0; k < s.num_bounds; ++k) c += s.bounds[k] <= a;
   }
   return c + (s.both && rel > 0 ? nb : 0);
