@@ -24,7 +24,8 @@ LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libbertenc.so")
 SOURCES = ["gemm_tc.cu", "gemm_f32.cu", "attention.cu", "attention_tc.cu", "layernorm.cu", "pack.cu",
            "persistent.cu", "decoder_attention.cu", "scored_simt.cu", "scored_step.cu",
-           "scored_tc.cu", "scored_tc_short.cu", "scored_tc_bwd.cu", "encoder.cu"]
+           "scored_tc.cu", "scored_tc_short.cu",
+           "scored_tc_bwd.cu", "scored_tc_bwd_short.cu", "encoder.cu"]
 
 
 def nvcc_path() -> str:

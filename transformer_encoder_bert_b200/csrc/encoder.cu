@@ -1609,11 +1609,18 @@ enc_status enc_op_scored_attention_backward(enc_t h, const enc_scores* scores, c
   const enc::ScoredShape sh{batch, seq, h->nh, h->d};
   cudaError_t e;
   int rows;                                                // of a query block of `partial`
-  if (h->dtype == ENC_FP16 && h->tc_attn) {
+  if (h->dtype == ENC_FP16 && h->tc_attn && seq <= enc::kScoredShort) {
+    rows = enc::kScoredShort;
+    e = enc::launch_scored_backward_tc_short(a, static_cast<const __half*>(qkv), valid_len,
+                                             static_cast<const __half*>(ctx), lse, static_cast<const __half*>(dctx),
+                                             static_cast<__half*>(dqkv), partial, sh, h->status, h->num_sms, st);
+    if (e == cudaSuccess) h->launches += 1;
+  } else if (h->dtype == ENC_FP16 && h->tc_attn) {
     rows = enc::kScoredTcRows;
     e = enc::launch_scored_backward_tc(a, static_cast<const __half*>(qkv), valid_len, static_cast<const __half*>(ctx),
                                        lse, static_cast<const __half*>(dctx), static_cast<__half*>(dqkv), partial,
                                        h->scored_ws, sh, h->status, st);
+    if (e == cudaSuccess) h->launches += 3;
   } else {
     const bool half = h->dtype == ENC_FP16;
     float* rowsum = static_cast<float*>(h->scored_ws);
@@ -1621,9 +1628,9 @@ enc_status enc_op_scored_attention_backward(enc_t h, const enc_scores* scores, c
     e = enc::launch_scored_rowsum(ctx, dctx, valid_len, rowsum, sh, half, st);
     if (e == cudaSuccess)
       e = enc::launch_scored_backward_simt(a, qkv, valid_len, dctx, lse, rowsum, dqkv, partial, sh, half, st);
+    if (e == cudaSuccess) h->launches += 3;
   }
   if (e != cudaSuccess) return cuda_fail(e, "scored attention backward launch");
-  h->launches += 3;
   const int blocks = (seq + rows - 1) / rows;
   if (dtable) {
     e = enc::launch_scored_table_grad(partial, dtable, batch, blocks, a.buckets, h->nh, st);

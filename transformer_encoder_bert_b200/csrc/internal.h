@@ -262,6 +262,11 @@ cudaError_t launch_scored_backward_tc(const ScoreArgs& s, const __half* qkv, con
                                       const __half* ctx, const float* lse, const __half* dctx, __half* dqkv,
                                       float* partial, void* scratch, const ScoredShape& sh, int* status,
                                       cudaStream_t stream);
+// The same for seq <= kScoredShort in one pass (scored_tc_bwd_short.cu): one query block, no scratch.
+cudaError_t launch_scored_backward_tc_short(const ScoreArgs& s, const __half* qkv, const int32_t* valid_len,
+                                            const __half* ctx, const float* lse, const __half* dctx, __half* dqkv,
+                                            float* partial, const ScoredShape& sh, int* status, int num_sms,
+                                            cudaStream_t stream);
 // dtable [buckets, nh] = the partial sums added over the batch and the query blocks, in a fixed order.
 cudaError_t launch_scored_table_grad(const float* partial, float* dtable, int batch, int blocks, int buckets,
                                      int head_num, cudaStream_t stream);

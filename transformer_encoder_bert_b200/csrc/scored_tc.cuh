@@ -176,5 +176,19 @@ __device__ __forceinline__ uint64_t tanh_over_x2(uint64_t z) {
 // tanh(s in) of any size; in2 = 2 in log2 e.
 __device__ __forceinline__ float tanh_of(float s, float in2) { return fmaf(-2.f, rcp(1.f + ex2(s * in2)), 1.f); }
 
+// Adds 32 lanes' values to the warp's bucket sums.  The lanes' distances are consecutive (up or down), so a
+// bucket's lanes are neighbours: a segmented scan, then the last lane of each run adds.
+__device__ __forceinline__ void add_by_bucket(float v, int bucket, float* sums, int lane) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const float w = __shfl_up_sync(0xffffffffu, v, off);
+    const int bk = __shfl_up_sync(0xffffffffu, bucket, off);
+    if (lane >= off && bk == bucket) v += w;
+  }
+  const int after = __shfl_down_sync(0xffffffffu, bucket, 1);
+  if (lane == 31 || after != bucket) sums[bucket] += v;
+  __syncwarp();
+}
+
 }  // namespace scored_tc
 }  // namespace enc

@@ -167,20 +167,6 @@ __device__ __forceinline__ void row_block_m(bool mask, const RowBlock& rb, const
     row_block<MODE, CAP, NEAR, false>(rb, cap, scale2, lane, sum);
 }
 
-// Adds 32 lanes' values to the warp's bucket sums.  The lanes' distances are consecutive (up or down), so a
-// bucket's lanes are neighbours: a segmented scan, then the last lane of each run adds.
-__device__ __forceinline__ void add_by_bucket(float v, int bucket, float* sums, int lane) {
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const float w = __shfl_up_sync(0xffffffffu, v, off);
-    const int bk = __shfl_up_sync(0xffffffffu, bucket, off);
-    if (lane >= off && bk == bucket) v += w;
-  }
-  const int after = __shfl_down_sync(0xffffffffu, bucket, 1);
-  if (lane == 31 || after != bucket) sums[bucket] += v;
-  __syncwarp();
-}
-
 template <int D, int MODE>
 __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
     scored_tc_bwd_kernel(const __grid_constant__ ScoreArgs s, const __grid_constant__ CUtensorMap tm_a0,

@@ -1,0 +1,574 @@
+// Backward of attention with modified scores for sequences of at most 128: one
+// pass that forms the scores once, persistent CTAs over (sequence, head) items.
+//
+// With one block of keys and one of queries, dQ needs no sum over blocks, so
+// all five products run on one pair of score tiles (formulas in
+// scored_tc_bwd.cu):
+//   S^T = K Q^T, dP^T = V dO^T        M = 128 keys, N = 128 queries, K = D
+//   dV = P^T dO                       A = P^T from TMEM
+//   dK = dU^T Q                       A = dU^T from shared memory
+//   dQ = dU K                         A = the same tile, read M-major
+// Threads own key rows (TMEM lanes); two warpgroups share the 128 columns, w
+// taking queries 64 g + 32 w .. + 31 for g = 0, 1, so that the FP16 P^T of each
+// lands over S columns that it has read itself: P^T in columns [0, 64) of S, and
+// dV's accumulator in [64, 128); dK and dQ go over dP (heads of 128: dV and dQ
+// have columns of their own).  dU^T goes to shared memory as rows of keys, 64
+// queries (128 bytes) to a swizzled row, which is a K-major operand for dK and
+// an M-major one for dQ.
+//
+// The row statistics that the long kernels take from a kernel of their own (D_i
+// and the norms for dU's scale) are worked out here while the tiles load.  The
+// chain of an item's latencies is again what counts: two CTAs share an SM (one
+// for heads of 128), and the next item's Q and K load under the output of this
+// one.
+#include "scored_tc.cuh"
+
+namespace enc {
+namespace scored_tc {
+namespace {
+
+constexpr int kRowWarps = 8;
+constexpr int kThreads = 32 * (kRowWarps + 1);
+
+template <int D>
+struct SBCfg {
+  static constexpr int kCtasPerSm = D > 64 ? 1 : 2;
+  static constexpr int kSub = D > 64 ? D / 64 : 1;
+  static constexpr int kTile = kSub * 128 * 128;
+  static constexpr int kQ = 0, kK = kTile, kDO = 2 * kTile, kV = 3 * kTile;
+  static constexpr int kDU = 4 * kTile;                    // dU^T: 2 sub-tiles of 64 queries
+  static constexpr int kOut = kDO;                         // output rows, over dO, V and dU^T
+  static constexpr int kBars = kDU + 2 * 16384;
+  // qk_full, vo_full, s_full, p_full, acc_full, free, group, drain
+  static constexpr int kSlot = kBars + 64;
+  static constexpr int kMax = kSlot + 16;                  // per row warp: norms of dO and V
+  static constexpr int kCol = kMax + 2 * kRowWarps * 4;    // lse2 [128], D [128]
+  static constexpr int kDocs = kCol + 256 * 4;
+  static constexpr int kColumn = kDocs + 128 * 4;          // the head's column of the bias table
+  static constexpr int kLut = kColumn + kMaxScoreBuckets * 4;   // bias of distance k - 127
+  static constexpr int kDiag = kLut + 256 * 4;             // per row warp, finished diagonals
+  static constexpr int kSums = kDiag + kRowWarps * 32 * 4; // per row warp, bucket sums
+  static constexpr int kBucket = kSums + kRowWarps * kMaxScoreBuckets * 4;   // bucket of distance k - 127
+  static constexpr int kSmem = 1024 + kBucket + 256;
+  // TMEM: S [0, 128) with P^T in [0, 64), dP [128, 256).
+  static constexpr int kDP = 128, kDK = 128;
+  static constexpr int kDQ = D > 64 ? 256 : 192, kDV = D > 64 ? 384 : 64;
+  static constexpr int kTmemCols = D > 64 ? 512 : 256;
+  static_assert(3 * (D / 32) * 8192 <= 2 * kTile + 2 * 16384, "output rows");
+  static_assert(kCtasPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
+};
+
+// Load 16 consecutive 32-bit columns without waiting; tmem_wait_ld16 names the registers.
+__device__ __forceinline__ void tmem_ld_32x32b_x16_async(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x8_async(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// 16 queries of a key row: from S^T and dP^T to P^T (TMEM) and dU^T (shared memory).
+struct BwdChunk {
+  uint32_t t_s, t_dp, t_p;  // TMEM addresses
+  const float* lut;         // the row's bias at the chunk's first query; falls with the query
+  const float* col;         // lse2 [128] and D [128] at the first query
+  int lo, hi;               // visible queries, as far as length and causality go
+  const int* docs;          // documents of the queries, or nullptr
+  int doc;
+  float e;                  // dU's scale
+  uint8_t* du;              // the row of dU^T (64 queries), and the swizzle and 16-byte unit of the chunk
+  int swizzle, unit;
+};
+
+// DIAG: sums of dT along diagonals (run: the partial sum in this lane; diag: where lane 31 leaves finished ones).
+template <bool CAP, bool BIAS, bool DIAG, bool MASK>
+__device__ __forceinline__ void bwd_chunk(const BwdChunk& ch, const Cap& cap, float scale2, int lane, float& run,
+                                          float* diag) {
+  uint32_t sv[16], dp[16];
+  tmem_ld_32x32b_x16_async(ch.t_s, sv);
+  tmem_ld_32x32b_x16_async(ch.t_dp, dp);
+  tmem_wait_ld16(sv);
+  tmem_wait_ld16(dp);
+  uint32_t pp[8], pu[8];
+#pragma unroll
+  for (int k = 0; k < 16; k += 4) {
+    const float4 l4 = *reinterpret_cast<const float4*>(ch.col + k);
+    const float4 d4 = *reinterpret_cast<const float4*>(ch.col + 128 + k);
+    const float nl[4] = {l4.x, l4.y, l4.z, l4.w}, dc[4] = {d4.x, d4.y, d4.z, d4.w};
+    int4 dj = make_int4(0, 0, 0, 0);
+    if (MASK && ch.docs) dj = *reinterpret_cast<const int4*>(ch.docs + k);
+    const int djs[4] = {dj.x, dj.y, dj.z, dj.w};
+    float p[4], u[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float s = __uint_as_float(sv[k + q]);
+      const float add = BIAS ? ch.lut[-(k + q)] - nl[q] : -nl[q];
+      float t, th = 0.f;
+      if (CAP) {
+        th = tanh_of(s, 2.f * kLog2e * cap.in);
+        t = fmaf(cap.cap2, th, add);
+      } else {
+        t = fmaf(s, scale2, add);
+      }
+      p[q] = ex2(t);
+      float dt = p[q] * ((__uint_as_float(dp[k + q]) - dc[q]) * ch.e);
+      u[q] = CAP ? dt * fmaf(-th, th, 1.f) : dt;
+      if (MASK) {                                          // (hidden scores may be NaN)
+        const bool see = k + q >= ch.lo && k + q < ch.hi && (!ch.docs || djs[q] == ch.doc);
+        p[q] = see ? p[q] : 0.f;
+        dt = see ? dt : 0.f;
+        u[q] = see ? u[q] : 0.f;
+      }
+      if (DIAG) {
+        const float up = __shfl_up_sync(0xffffffffu, run, 1);
+        run = lane == 0 ? dt : up + dt;
+        if (lane == 31) diag[k + q] = run;
+      }
+    }
+    pp[k / 2] = half2_of(p[0], p[1]);
+    pp[k / 2 + 1] = half2_of(p[2], p[3]);
+    pu[k / 2] = half2_of(u[0], u[1]);
+    pu[k / 2 + 1] = half2_of(u[2], u[3]);
+  }
+  tmem_st_32x32b_x8_async(ch.t_p, pp);                     // over columns that this lane has read
+  *reinterpret_cast<uint4*>(ch.du + 16 * (ch.unit ^ ch.swizzle)) = make_uint4(pu[0], pu[1], pu[2], pu[3]);
+  *reinterpret_cast<uint4*>(ch.du + 16 * ((ch.unit + 1) ^ ch.swizzle)) = make_uint4(pu[4], pu[5], pu[6], pu[7]);
+}
+
+template <int D, bool CAP, bool BIAS, bool DIAG>
+__global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
+    scored_tc_bwd_short_kernel(const __grid_constant__ ScoreArgs s, const __grid_constant__ CUtensorMap tm_qkv,
+                               const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_out,
+                               const int32_t* __restrict__ valid_len, const __half* __restrict__ qkv,
+                               const __half* __restrict__ ctx, const float* __restrict__ lse,
+                               const __half* __restrict__ dctx, __half* __restrict__ dqkv, float* __restrict__ partial,
+                               int B, int S, int NH, int* __restrict__ status) {
+  using C = SBCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::kBars;
+  const uint32_t qk_full = bar0, vo_full = bar0 + 8, s_full = bar0 + 16, p_full = bar0 + 24, acc_full = bar0 + 32,
+                 free_bar = bar0 + 40, group = bar0 + 48, drain = bar0 + 56;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kSlot);
+  float* warp_max = reinterpret_cast<float*>(smem + C::kMax);
+  float* col = reinterpret_cast<float*>(smem + C::kCol);
+  int* pos_docs = reinterpret_cast<int*>(smem + C::kDocs);
+  float* column = reinterpret_cast<float*>(smem + C::kColumn);
+  float* lut = reinterpret_cast<float*>(smem + C::kLut);
+  uint8_t* bucket_of = smem + C::kBucket;
+
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  if (tid == 0) {
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t bar = bar0 + 8 * k;
+      mbar_init(bar, bar == p_full || bar == free_bar || bar == group ? kRowWarps : 1);
+    }
+    fence_barrier_init();
+  }
+  pdl_wait();
+  if (warp == kRowWarps) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = uniform(*tmem_slot);
+  pdl_trigger();                                           // after taking TMEM
+
+  // Items [first, last) of B * NH, item = head * B + sequence.
+  const int items = B * NH, ctas = gridDim.x, cta = blockIdx.x;
+  const int first = (int)((long long)items * cta / ctas), last = (int)((long long)items * (cta + 1) / ctas);
+  auto length = [&](int item) { return score_len(valid_len, item % B, S); };
+  bool ok = true;
+  if (warp == kRowWarps) {
+    prefetch_tmap(&tm_qkv);
+    prefetch_tmap(&tm_do);
+    constexpr uint32_t idesc_s = idesc_f16_f32(128, 128);
+    constexpr uint32_t idesc_o = idesc_bmn(128, D);        // A K-major (or in TMEM), B N-major
+    constexpr uint32_t idesc_q = idesc_o | (1u << 15);     // A M-major too
+    const uint64_t q_desc = smem_desc_sw128(sbase + C::kQ), k_desc = smem_desc_sw128(sbase + C::kK);
+    const uint64_t v_desc = smem_desc_sw128(sbase + C::kV), do_desc = smem_desc_sw128(sbase + C::kDO);
+    const uint64_t du_desc = smem_desc_sw128(sbase + C::kDU);
+    const uint64_t du_m = desc_mn_sw128(sbase + C::kDU, 16384);
+    const uint64_t q_n = desc_mn_sw128(sbase + C::kQ, 16384), k_n = desc_mn_sw128(sbase + C::kK, 16384);
+    const uint64_t do_n = desc_mn_sw128(sbase + C::kDO, 16384);
+    auto next_loaded = [&](int item) {
+      while (item < last && length(item) == 0) ++item;
+      return item;
+    };
+    auto load_qk = [&](int item) {
+      mbar_arrive_expect_tx(qk_full, 2 * C::kTile);
+      for (int part = 0; part < 2; ++part)
+        for (int u = 0; u < C::kSub; ++u)
+          tma_load_3d(&tm_qkv, sbase + (part ? C::kK : C::kQ) + u * 16384, qk_full, 64 * u, 0,
+                      (part * B + item % B) * NH + item / B);
+    };
+    auto load_vo = [&](int item) {
+      mbar_arrive_expect_tx(vo_full, 2 * C::kTile);
+      for (int u = 0; u < C::kSub; ++u) {
+        tma_load_3d(&tm_qkv, sbase + C::kV + u * 16384, vo_full, 64 * u, 0, (2 * B + item % B) * NH + item / B);
+        tma_load_3d(&tm_do, sbase + C::kDO + u * 16384, vo_full, (item / B) * D + 64 * u, 0, item % B);
+      }
+    };
+    int qk_loads = 0, vo_loads = 0, it = 0;
+    int cur = next_loaded(first);
+    if (cur < last) {
+      if (elect_one()) load_qk(cur);
+      qk_loads = 1;
+    }
+    for (; cur < last; ++it) {
+      const uint32_t ph = it & 1;
+      const int n = length(cur), nxt = next_loaded(cur + 1);
+      // The previous item's accumulators have been read, and its output rows over dO, V and dU^T stored.
+      if (it > 0 && !(ok = warp_wait(free_bar, ph ^ 1))) break;
+      if (elect_one()) load_vo(cur);
+      ++vo_loads;
+      if (!(ok = warp_wait(qk_full, ph))) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = (kk / 4) * 16384 + (kk % 4) * 32;
+          mma_f16_ss(tmem, desc_at(k_desc, o), desc_at(q_desc, o), idesc_s, kk > 0 ? 1u : 0u);
+        }
+      }
+      __syncwarp();
+      if (!(ok = warp_wait(vo_full, ph))) break;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = (kk / 4) * 16384 + (kk % 4) * 32;
+          mma_f16_ss(tmem + C::kDP, desc_at(v_desc, o), desc_at(do_desc, o), idesc_s, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(s_full);
+      }
+      __syncwarp();
+      if (!(ok = warp_wait(p_full, ph))) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)                     // 16 queries: their P^T is in warpgroup (kk / 2) % 2's columns
+          if (16 * kk < n)
+            mma_f16_ts(tmem + C::kDV, tmem + 32 * ((kk >> 1) & 1) + 16 * (kk >> 2) + 8 * (kk & 1),
+                       desc_at(do_n, kk * 2048), idesc_o, kk > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          if (16 * kk < n)
+            mma_f16_ss(tmem + C::kDK, desc_at(du_desc, (kk / 4) * 16384 + (kk % 4) * 32), desc_at(q_n, kk * 2048), idesc_o,
+                       kk > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)                     // 16 keys
+          if (16 * kk < n)
+            mma_f16_ss(tmem + C::kDQ, desc_at(du_m, kk * 2048), desc_at(k_n, kk * 2048), idesc_q, kk > 0 ? 1u : 0u);
+        mma_commit(acc_full);
+      }
+      __syncwarp();
+      if (nxt < last) {                                    // Q and K have been read
+        if (!(ok = warp_wait(acc_full, ph))) break;
+        if (elect_one()) load_qk(nxt);
+        ++qk_loads;
+      }
+      cur = nxt;
+    }
+    if (elect_one()) mma_commit(drain);                    // every MMA issued here has completed
+    __syncwarp();
+    warp_wait(drain, 0);
+    if (qk_loads) warp_wait(qk_full, (qk_loads - 1) & 1);  // and every load has landed
+    if (vo_loads) warp_wait(vo_full, (vo_loads - 1) & 1);
+  } else {
+    const int w = warp >> 2, quad = warp & 3, r = quad * 32 + lane;          // warpgroup; key row = TMEM lane
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const Cap cap = make_cap(s);
+    const float scale2 = s.scale * kLog2e;
+    float* sums = reinterpret_cast<float*>(smem + C::kSums) + warp * kMaxScoreBuckets;
+    float* diag = reinterpret_cast<float*>(smem + C::kDiag) + warp * 32;
+    int it = 0, built = -1;
+    uint32_t group_ph = 0;
+    auto group_sync = [&] {                                // the row warps, bounded
+      __syncwarp();
+      if (lane == 0) mbar_arrive(group);
+      ok = ok && warp_wait(group, group_ph);
+      group_ph ^= 1;
+    };
+    for (int item = first; item < last; ++item) {
+      const int b = item % B, h = item / B;
+      const size_t bh = (size_t)b * NH + h;
+      const int n = score_len(valid_len, b, S), prefix = score_prefix(s, b);
+      if (BIAS && h != built) {                            // the head's bias, for distances within the sequence
+        built = h;
+        group_sync();                                      // the previous head's has been read
+        load_column(s, column, NH, h, tid, 32 * kRowWarps);
+        group_sync();
+        const float slope = s.slopes ? s.slopes[h] : 0.f;
+        for (int k = 128 - S + tid; k <= 126 + S; k += 32 * kRowWarps) {
+          lut[k] = score_bias2(s, column, slope, k - 127);
+          if (DIAG) bucket_of[k] = static_cast<uint8_t>(score_bucket(s, k - 127));
+        }
+        group_sync();
+        if (!ok) break;
+      }
+      if (n == 0) {                                        // zero gradients
+        for (int part = 0; part < 3; ++part) {
+          uint4* out = reinterpret_cast<uint4*>(dqkv + (((size_t)part * B * NH + bh) * S) * D);
+          for (int k = tid; k < S * (D / 8); k += 32 * kRowWarps) out[k] = make_uint4(0, 0, 0, 0);
+        }
+        if (DIAG)
+          for (int k = tid; k < s.buckets; k += 32 * kRowWarps) partial[bh * s.buckets + k] = 0.f;
+        continue;
+      }
+      const uint32_t ph = it & 1;
+      ++it;
+      // Row statistics while the tiles load: D / 8 lanes to a row.
+      {
+        constexpr int kLanes = D / 8;
+        const int gl = tid % kLanes;
+        float mo = 0.f, mv = 0.f;
+        group_sync();                                      // the previous item's have been read
+#pragma unroll
+        for (int pass = 0; pass < 128 * kLanes / (32 * kRowWarps); ++pass) {
+          const int i = pass * (32 * kRowWarps / kLanes) + tid / kLanes;
+          float dot = 0.f, oo = 0.f, vv = 0.f;
+          if (i < n) {
+            const size_t at = ((size_t)b * S + i) * NH * D + (size_t)h * D + gl * 8;
+            const uint4 o4 = *reinterpret_cast<const uint4*>(ctx + at), g4 = *reinterpret_cast<const uint4*>(dctx + at);
+            const uint4 v4 = *reinterpret_cast<const uint4*>(qkv + ((2 * (size_t)B * NH + bh) * S + i) * D + gl * 8);
+            const uint32_t ow[4] = {o4.x, o4.y, o4.z, o4.w}, gw[4] = {g4.x, g4.y, g4.z, g4.w},
+                           vw[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&ow[k]));
+              const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&gw[k]));
+              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&vw[k]));
+              dot = fmaf(o.x, g.x, fmaf(o.y, g.y, dot));
+              oo = fmaf(g.x, g.x, fmaf(g.y, g.y, oo));
+              vv = fmaf(v.x, v.x, fmaf(v.y, v.y, vv));
+            }
+          }
+#pragma unroll
+          for (int off = kLanes / 2; off > 0; off >>= 1) {
+            dot += __shfl_xor_sync(0xffffffffu, dot, off);
+            oo += __shfl_xor_sync(0xffffffffu, oo, off);
+            vv += __shfl_xor_sync(0xffffffffu, vv, off);
+          }
+          mo = fmaxf(mo, oo);
+          mv = fmaxf(mv, vv);
+          if (gl == 0) {
+            const float l = i < n ? lse[bh * S + i] * kLog2e : INFINITY;
+            col[i] = l == -INFINITY ? INFINITY : l;
+            col[128 + i] = dot;
+          }
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+          mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, off));
+          mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, off));
+        }
+        if (lane == 0) {
+          warp_max[warp] = mo;
+          warp_max[kRowWarps + warp] = mv;
+        }
+        if (s.docs && tid < 128) pos_docs[tid] = tid < n ? s.docs[(size_t)b * S + tid] : 0;
+        if (DIAG)
+          for (int k = lane; k < s.buckets; k += 32) sums[k] = 0.f;
+        group_sync();
+        if (!ok) break;
+      }
+      float mo = 0.f, mv = 0.f;
+#pragma unroll
+      for (int k = 0; k < kRowWarps; ++k) {
+        mo = fmaxf(mo, warp_max[k]);
+        mv = fmaxf(mv, warp_max[kRowWarps + k]);
+      }
+      const float prod = sqrtf(mo) * sqrtf(mv);
+      int ex = 0;
+      if (prod > 0.f && prod < INFINITY) frexpf(prod, &ex);                  // prod in [2^(ex-1), 2^ex)
+      ex = max(-100, min(100, 14 - ex));
+      const float e = exp2f((float)ex), inv_e = exp2f((float)-ex);
+
+      const bool mine = r < n;
+      const int w0 = quad * 32, w1 = w0 + 31;              // the warp's keys
+      const int ilow = score_ilow(s, r, prefix), ilow_first = score_ilow(s, w0, prefix);
+      const int ilow_all = max(score_ilow(s, w1, prefix), ilow_first);
+      BwdChunk ch;
+      ch.doc = s.docs ? pos_docs[r] : 0;
+      ch.e = e;
+      ch.swizzle = r & 7;
+      if (!(ok = warp_wait(s_full, ph))) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int g = 0; g < 2; ++g) {
+        float run = 0.f;
+        const int i0 = 64 * g + 32 * w;
+        const bool none = w0 >= n || i0 >= n || i0 + 32 <= min(ilow_first, score_ilow(s, min(w1, n - 1), prefix));
+#pragma unroll 1
+        for (int c = 0; c < 32; c += 16) {
+          const int i = i0 + c;
+          ch.t_s = t_row + i;
+          ch.t_dp = t_row + C::kDP + i;
+          ch.t_p = t_row + 32 * w + 16 * g + c / 2;
+          ch.lut = lut + 127 + r - i;
+          ch.col = col + i;
+          ch.lo = ilow - i;
+          ch.hi = mine ? n - i : 0;
+          ch.docs = s.docs ? pos_docs + i : nullptr;
+          ch.du = smem + C::kDU + g * 16384 + r * 128;
+          ch.unit = 4 * w + c / 8;
+          if (none) {
+            const uint32_t zero[8] = {};
+            tmem_st_32x32b_x8_async(ch.t_p, zero);
+            *reinterpret_cast<uint4*>(ch.du + 16 * (ch.unit ^ ch.swizzle)) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(ch.du + 16 * ((ch.unit + 1) ^ ch.swizzle)) = make_uint4(0, 0, 0, 0);
+          } else if (s.docs || w1 >= n || i + 16 > n || i < ilow_all) {
+            bwd_chunk<CAP, BIAS, DIAG, true>(ch, cap, scale2, lane, run, diag + c);
+          } else {
+            bwd_chunk<CAP, BIAS, DIAG, false>(ch, cap, scale2, lane, run, diag + c);
+          }
+        }
+        if (DIAG && !none) {
+          // diag[k]: the diagonal that left lane 31 at column k, distance w1 - (i0 + k); run: the one in this lane.
+          // Distances outside the sequence have sums of 0 and may go anywhere.
+          auto bucket_at = [&](int rel) { return (int)bucket_of[127 + max(1 - S, min(S - 1, rel))]; };
+          __syncwarp();
+          add_by_bucket(diag[lane], bucket_at(w1 - i0 - lane), sums, lane);
+          add_by_bucket(lane == 31 ? 0.f : run, bucket_at(w0 + lane - (i0 + 31)), sums, lane);
+        }
+      }
+      // Rows in [n, n rounded up to 16) of the operands that the last three products sum over: zeros, whatever
+      // memory holds there.
+      const int n16 = (n + 15) & ~15;
+      if (n < n16 && quad == (n >> 5)) {
+        const int units = (n16 - n) * 8;
+        for (int k = w * 32 + lane; k < units * C::kSub * 3; k += 64) {
+          const int plane = k / units, rr = n + k % units / 8;               // sub-tiles of Q, K, dO
+          *reinterpret_cast<uint4*>(smem + plane * 16384 + rr * 128 + (k % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      fence_proxy_async_smem();                            // dU^T and the zeros visible to the tensor core
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+      if (DIAG) {
+        group_sync();
+        if (!ok) break;
+        const float* all = reinterpret_cast<const float*>(smem + C::kSums);
+        for (int k = tid; k < s.buckets; k += 32 * kRowWarps) {
+          float total = 0.f;
+#pragma unroll
+          for (int v = 0; v < kRowWarps; ++v) total += all[v * kMaxScoreBuckets + k];
+          partial[bh * s.buckets + k] = total * inv_e;
+        }
+      }
+      if (!(ok = warp_wait(acc_full, ph))) break;
+      tc_fence_after();
+      // 32 columns of an accumulator at a time, the warpgroups in turn: FP16 rows of 64 bytes over dO, V and dU^T
+      // in the store's swizzle, one TMA store for a warp's 32 rows.
+      constexpr int kPieces = 3 * (D / 32);
+#pragma unroll 1
+      for (int piece = w; piece < kPieces; piece += 2) {
+        const int part = piece / (D / 32), c = piece % (D / 32) * 32;        // 0: dQ, 1: dK, 2: dV
+        const float f = !mine ? 0.f : part == 2 ? 1.f : s.scale * inv_e;
+        uint32_t oa[32];
+        tmem_ld_32x32b_x32(t_row + (part == 0 ? C::kDQ : part == 1 ? C::kDK : C::kDV) + c, oa);
+        uint8_t* tile = smem + C::kOut + piece * 8192 + quad * 2048;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            v[k] = mine ? half2_of(__uint_as_float(oa[8 * q + 2 * k]) * f, __uint_as_float(oa[8 * q + 2 * k + 1]) * f) : 0u;
+          *reinterpret_cast<uint4*>(tile + lane * 64 + 16 * (q ^ ((lane >> 1) & 3))) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && w0 < S) {                         // rows at or past S are outside the map
+          tma_store_3d(&tm_out, smem_u32(tile), c, w0, part * B * NH + (int)bh);
+          bulk_commit_group();
+        }
+      }
+      tc_fence_before();
+      if (lane == 0) {
+        bulk_wait_group_read<0>();
+        mbar_arrive(free_bar);
+      }
+      __syncwarp();
+    }
+  }
+
+  if (!ok) atomicCAS(status, 0, kStatusWaitTimeout);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kRowWarps) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int D, bool CAP, bool BIAS, bool DIAG>
+cudaError_t launch_v(const ScoreArgs& s, const __half* qkv, const int32_t* vl, const __half* ctx, const float* lse,
+                     const __half* dctx, __half* dqkv, float* partial, const ScoredShape& sh, int* status, int num_sms,
+                     cudaStream_t stream) {
+  using C = SBCfg<D>;
+  auto kern = scored_tc_bwd_short_kernel<D, CAP, BIAS, DIAG>;
+  static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (attr != cudaSuccess) return attr;
+  const uint64_t planes = 3ull * sh.batch * sh.head_num;
+  CUtensorMap tq, td, to;
+  if (!encode_operand_map(&tq, qkv, D, sh.seq, planes, 64, 128) ||
+      !encode_operand_map(&td, dctx, (uint64_t)sh.head_num * D, sh.seq, sh.batch, 64, 128) ||
+      !encode_operand_map(&to, dqkv, D, sh.seq, planes, 32, 32))
+    return cudaErrorInvalidValue;
+  const long items = (long)sh.batch * sh.head_num, resident = (long)C::kCtasPerSm * num_sms;
+  return launch_kernel(kern, dim3((unsigned)(items < resident ? items : resident)), dim3(kThreads), C::kSmem, stream,
+                       nullptr, 0, s, tq, td, to, vl, qkv, ctx, lse, dctx, dqkv, partial, sh.batch, sh.seq, sh.head_num,
+                       status);
+}
+
+template <int D, bool CAP>
+cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, const __half* ctx, const float* lse,
+                     const __half* dctx, __half* dqkv, float* partial, const ScoredShape& sh, int* status, int num_sms,
+                     cudaStream_t stream) {
+  if (partial) return launch_v<D, CAP, true, true>(s, qkv, vl, ctx, lse, dctx, dqkv, partial, sh, status, num_sms, stream);
+  return s.table || s.slopes
+             ? launch_v<D, CAP, true, false>(s, qkv, vl, ctx, lse, dctx, dqkv, partial, sh, status, num_sms, stream)
+             : launch_v<D, CAP, false, false>(s, qkv, vl, ctx, lse, dctx, dqkv, partial, sh, status, num_sms, stream);
+}
+
+}  // namespace
+}  // namespace scored_tc
+
+cudaError_t launch_scored_backward_tc_short(const ScoreArgs& s, const __half* qkv, const int32_t* valid_len,
+                                            const __half* ctx, const float* lse, const __half* dctx, __half* dqkv,
+                                            float* partial, const ScoredShape& sh, int* status, int num_sms,
+                                            cudaStream_t stream) {
+  using namespace scored_tc;
+  auto run = [&](auto d, auto cap) {
+    return launch_d<decltype(d)::value, decltype(cap)::value>(s, qkv, valid_len, ctx, lse, dctx, dqkv, partial, sh, status,
+                                                              num_sms, stream);
+  };
+  auto capped = [&](auto d) { return s.cap > 0.f ? run(d, std::true_type()) : run(d, std::false_type()); };
+  switch (sh.size_per_head) {
+    case 32: return capped(std::integral_constant<int, 32>());
+    case 64: return capped(std::integral_constant<int, 64>());
+    case 128: return capped(std::integral_constant<int, 128>());
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace enc
