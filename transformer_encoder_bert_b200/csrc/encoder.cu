@@ -560,14 +560,15 @@ enc_status make_scores(enc_handle* h, const enc_scores* p, enc::ScoreArgs& s) {
 
 // Scratch of the backward pass: the row statistics (of either kernels), then
 // each query block's sums of the table's gradient (for the smallest block and
-// the largest table).
+// the largest table, or the sums by distance).
 size_t scored_rows_bytes(const enc_handle* h, int batch, int seq) {
   return align_up(std::max((size_t)batch * seq * h->nh * 4,
                            enc::scored_backward_tc_scratch(enc::ScoredShape{batch, seq, h->nh, h->d})), 256);
 }
 size_t scored_ws_bytes(const enc_handle* h, int batch, int seq) {
   const size_t blocks = ((size_t)seq + enc::kScoredSimtRows - 1) / enc::kScoredSimtRows;
-  return scored_rows_bytes(h, batch, seq) + (size_t)batch * h->nh * blocks * enc::kMaxScoreBuckets * 4;
+  return scored_rows_bytes(h, batch, seq) +
+         (size_t)batch * h->nh * std::max<size_t>(256, blocks * enc::kMaxScoreBuckets) * 4;
 }
 
 enc_status ensure_scored_ws(enc_handle* h, int batch, int seq, bool have_stream, cudaStream_t st) {
@@ -1608,9 +1609,10 @@ enc_status enc_op_scored_attention_backward(enc_t h, const enc_scores* scores, c
       dtable ? reinterpret_cast<float*>(static_cast<char*>(h->scored_ws) + scored_rows_bytes(h, batch, seq)) : nullptr;
   const enc::ScoredShape sh{batch, seq, h->nh, h->d};
   cudaError_t e;
-  int rows;                                                // of a query block of `partial`
+  int rows, short_ctas = 0;                                // of a query block of `partial`
   if (h->dtype == ENC_FP16 && h->tc_attn && seq <= enc::kScoredShort) {
     rows = enc::kScoredShort;
+    short_ctas = enc::scored_short_ctas(sh, h->num_sms);
     e = enc::launch_scored_backward_tc_short(a, static_cast<const __half*>(qkv), valid_len,
                                              static_cast<const __half*>(ctx), lse, static_cast<const __half*>(dctx),
                                              static_cast<__half*>(dqkv), partial, sh, h->status, h->num_sms, st);
@@ -1633,7 +1635,7 @@ enc_status enc_op_scored_attention_backward(enc_t h, const enc_scores* scores, c
   if (e != cudaSuccess) return cuda_fail(e, "scored attention backward launch");
   const int blocks = (seq + rows - 1) / rows;
   if (dtable) {
-    e = enc::launch_scored_table_grad(partial, dtable, batch, blocks, a.buckets, h->nh, st);
+    e = enc::launch_scored_table_grad(a, partial, dtable, blocks, short_ctas, sh, st);
     if (e != cudaSuccess) return cuda_fail(e, "table gradient launch");
     ++h->launches;
   }

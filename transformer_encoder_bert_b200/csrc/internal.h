@@ -250,10 +250,6 @@ constexpr int kScoredSimtRows = 64;
 cudaError_t launch_scored_backward_simt(const ScoreArgs& s, const void* qkv, const int32_t* valid_len,
                                         const void* dctx, const float* lse, const float* rowsum, void* dqkv,
                                         float* partial, const ScoredShape& sh, bool half, cudaStream_t stream);
-// One new token per sequence: qkv [3, B, nh, 1, d], cache [2, B, nh, capacity, d] (sh.seq = capacity),
-// position len[b]; ctx [B, nh*d].  docs is [B, capacity].
-cudaError_t launch_scored_step(const ScoreArgs& s, const void* qkv, void* cache, const int32_t* len, void* ctx,
-                               const ScoredShape& sh, bool half, int num_sms, cudaStream_t stream);
 // The same on the tensor cores, FP16 (scored_tc_bwd.cu), the row sums included; partial has query blocks of
 // kScoredTcRows; scratch: scored_backward_tc_scratch bytes.
 constexpr int kScoredTcRows = 128;
@@ -262,14 +258,22 @@ cudaError_t launch_scored_backward_tc(const ScoreArgs& s, const __half* qkv, con
                                       const __half* ctx, const float* lse, const __half* dctx, __half* dqkv,
                                       float* partial, void* scratch, const ScoredShape& sh, int* status,
                                       cudaStream_t stream);
-// The same for seq <= kScoredShort in one pass (scored_tc_bwd_short.cu): one query block, no scratch.
+// The same for seq <= kScoredShort in one pass (scored_tc_bwd_short.cu), without scratch.  partial [nh * B, 256]
+// holds sums by distance (distance + 127) of the items head * B + sequence that each of the scored_short_ctas CTAs has
+// of a head, at the first of them.
+int scored_short_ctas(const ScoredShape& sh, int num_sms);
 cudaError_t launch_scored_backward_tc_short(const ScoreArgs& s, const __half* qkv, const int32_t* valid_len,
                                             const __half* ctx, const float* lse, const __half* dctx, __half* dqkv,
                                             float* partial, const ScoredShape& sh, int* status, int num_sms,
                                             cudaStream_t stream);
-// dtable [buckets, nh] = the partial sums added over the batch and the query blocks, in a fixed order.
-cudaError_t launch_scored_table_grad(const float* partial, float* dtable, int batch, int blocks, int buckets,
-                                     int head_num, cudaStream_t stream);
+// dtable [buckets, nh] = the partial sums added up in a fixed order: over the batch and the query blocks
+// (short_ctas = 0), or the sums by distance of that many CTAs.
+cudaError_t launch_scored_table_grad(const ScoreArgs& s, const float* partial, float* dtable, int blocks, int short_ctas,
+                                     const ScoredShape& sh, cudaStream_t stream);
+// One new token per sequence: qkv [3, B, nh, 1, d], cache [2, B, nh, capacity, d] (sh.seq = capacity),
+// position len[b]; ctx [B, nh*d].  docs is [B, capacity].
+cudaError_t launch_scored_step(const ScoreArgs& s, const void* qkv, void* cache, const int32_t* len, void* ctx,
+                               const ScoredShape& sh, bool half, int num_sms, cudaStream_t stream);
 
 // ---- weight repack, encoder.cu ----
 int device_sm_count();

@@ -67,4 +67,12 @@ __device__ __forceinline__ int score_ilow(const ScoreArgs& s, int j, int prefix)
   return s.causal && j >= prefix ? j : 0;
 }
 
+// Persistent CTAs over `items`: CTA c of `ctas` takes [first_item(c), first_item(c + 1)).
+__host__ __device__ __forceinline__ int first_item(int c, int items, int ctas) {
+  return static_cast<int>(static_cast<long long>(items) * c / ctas);
+}
+__host__ __device__ __forceinline__ int cta_of_item(int item, int items, int ctas) {
+  return static_cast<int>((static_cast<long long>(item + 1) * ctas - 1) / items);
+}
+
 }  // namespace enc

@@ -453,23 +453,48 @@ __global__ void __launch_bounds__(kThreads)
   if (lane == 0) rowsum[((size_t)b * NH + h) * S + i] = sum;
 }
 
-// Block (head, 32 buckets): 8 warps take the partial sums in turn, lane = bucket.
+// Block (head, bucket): the bucket's entries of the partial sums, added up by threads in a fixed order.  They are
+// [B, nh, blocks, buckets], or with short_ctas sums by distance (entry distance + 127 of 256) at the first item of
+// each CTA's run of the head's items; a bucket's distances are consecutive entries.
 __global__ void __launch_bounds__(kThreads)
-    scored_table_grad_kernel(const float* __restrict__ partial, float* __restrict__ dtable, int B, int blocks,
-                             int buckets, int NH) {
-  __shared__ double sums[8][32];
-  pdl_wait();
-  pdl_trigger();
-  const int h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.y * 32 + lane;
+    scored_table_grad_kernel(const __grid_constant__ ScoreArgs s, const float* __restrict__ partial,
+                             float* __restrict__ dtable, int B, int blocks, int short_ctas, int S, int NH) {
+  __shared__ double sums[kThreads / 32];
+  __shared__ int range[2];
+  const int h = blockIdx.x, c = blockIdx.y, t = threadIdx.x;
   double sum = 0.0;
-  if (c < buckets)
-    for (int k = warp; k < B * blocks; k += 8)
-      sum += partial[(((size_t)(k / blocks) * NH + h) * blocks + k % blocks) * buckets + c];
-  sums[warp][lane] = sum;
-  __syncthreads();
-  if (warp == 0 && c < buckets) {
+  if (short_ctas) {
+    if (t < 2) range[t] = t == 0 ? 256 : 0;
+    __syncthreads();
+    if (t >= 128 - S && t <= 126 + S && score_bucket(s, t - 127) == c) {
+      atomicMin(&range[0], t);
+      atomicMax(&range[1], t + 1);
+    }
+    __syncthreads();
+    const int at = range[0], count = max(0, range[1] - at), items = B * NH;
+    const int first = cta_of_item(h * B, items, short_ctas), last = cta_of_item(h * B + B - 1, items, short_ctas);
+    pdl_wait();
+    pdl_trigger();
+    const int total = (last - first + 1) * count;
+#pragma unroll 4
+    for (int k = t; k < total; k += kThreads) {
+      const int item = max(h * B, first_item(first + k / count, items, short_ctas));
+      sum += partial[(size_t)item * 256 + at + k % count];
+    }
+  } else {
+    pdl_wait();
+    pdl_trigger();
+#pragma unroll 4
+    for (int k = t; k < B * blocks; k += kThreads)
+      sum += partial[(((size_t)(k / blocks) * NH + h) * blocks + k % blocks) * s.buckets + c];
+  }
 #pragma unroll
-    for (int w = 1; w < 8; ++w) sum += sums[w][lane];
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (t % 32 == 0) sums[t / 32] = sum;
+  __syncthreads();
+  if (t == 0) {
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) sum += sums[w];
     dtable[(size_t)c * NH + h] = static_cast<float>(sum);
   }
 }
@@ -555,10 +580,10 @@ cudaError_t launch_scored_backward_simt(const ScoreArgs& s, const void* qkv, con
   });
 }
 
-cudaError_t launch_scored_table_grad(const float* partial, float* dtable, int batch, int blocks, int buckets,
-                                     int head_num, cudaStream_t stream) {
-  return launch_kernel(scored_table_grad_kernel, dim3(head_num, (buckets + 31) / 32), dim3(kThreads), 0, stream,
-                       nullptr, 0, partial, dtable, batch, blocks, buckets, head_num);
+cudaError_t launch_scored_table_grad(const ScoreArgs& s, const float* partial, float* dtable, int blocks, int short_ctas,
+                                     const ScoredShape& sh, cudaStream_t stream) {
+  return launch_kernel(scored_table_grad_kernel, dim3(sh.head_num, s.buckets), dim3(kThreads), 0, stream, nullptr, 0, s,
+                       partial, dtable, sh.batch, blocks, short_ctas, sh.seq, sh.head_num);
 }
 
 }  // namespace enc

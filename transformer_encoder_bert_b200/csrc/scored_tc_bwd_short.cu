@@ -17,10 +17,20 @@
 // an M-major one for dQ.
 //
 // The row statistics that the long kernels take from a kernel of their own (D_i
-// and the norms for dU's scale) are worked out here while the tiles load.  The
-// chain of an item's latencies is again what counts: two CTAs share an SM (one
-// for heads of 128), and the next item's Q and K load under the output of this
-// one.
+// and the norms for dU's scale) are worked out here from the tiles and a row of
+// O, under the first two products.  The chain of an item's latencies is again
+// what counts: two CTAs share an SM (one for heads of 128), and once the last
+// products are done the next item's tiles load (and its O, into registers) and,
+// as soon as the accumulators have been read, its first products run, under the
+// output of this one, which goes through dU^T's tile.
+//
+// The table's gradient leaves the kernel as sums of dT by distance (255 floats
+// for each head that a CTA has items of, at the place of the first of them).  For a column k of a 32 x 32 block, lane t takes the value of row
+// (t + k) mod 32: all 32 lie on distinct diagonals, and over the columns lane t
+// adds up the two diagonals whose row less column is t and t - 32, with no
+// shuffle that waits for the one before (a partial sum passed from lane to lane
+// along the diagonal took 64 dependent steps a row: 8,400 cycles an item against
+// 2,400 without the sums).
 #include "scored_tc.cuh"
 
 namespace enc {
@@ -37,24 +47,20 @@ struct SBCfg {
   static constexpr int kTile = kSub * 128 * 128;
   static constexpr int kQ = 0, kK = kTile, kDO = 2 * kTile, kV = 3 * kTile;
   static constexpr int kDU = 4 * kTile;                    // dU^T: 2 sub-tiles of 64 queries
-  static constexpr int kOut = kDO;                         // output rows, over dO, V and dU^T
   static constexpr int kBars = kDU + 2 * 16384;
-  // qk_full, vo_full, s_full, p_full, acc_full, free, group, drain
+  // full, s_full, p_full, acc_full, free, group, drain
   static constexpr int kSlot = kBars + 64;
   static constexpr int kMax = kSlot + 16;                  // per row warp: norms of dO and V
   static constexpr int kCol = kMax + 2 * kRowWarps * 4;    // lse2 [128], D [128]
   static constexpr int kDocs = kCol + 256 * 4;
   static constexpr int kColumn = kDocs + 128 * 4;          // the head's column of the bias table
   static constexpr int kLut = kColumn + kMaxScoreBuckets * 4;   // bias of distance k - 127
-  static constexpr int kDiag = kLut + 256 * 4;             // per row warp, finished diagonals
-  static constexpr int kSums = kDiag + kRowWarps * 32 * 4; // per row warp, bucket sums
-  static constexpr int kBucket = kSums + kRowWarps * kMaxScoreBuckets * 4;   // bucket of distance k - 127
-  static constexpr int kSmem = 1024 + kBucket + 256;
+  static constexpr int kDiag = kLut + 256 * 4;             // per row warp and g: 64 diagonals
+  static constexpr int kSmem = 1024 + kDiag + kRowWarps * 2 * 64 * 4;
   // TMEM: S [0, 128) with P^T in [0, 64), dP [128, 256).
   static constexpr int kDP = 128, kDK = 128;
   static constexpr int kDQ = D > 64 ? 256 : 192, kDV = D > 64 ? 384 : 64;
   static constexpr int kTmemCols = D > 64 ? 512 : 256;
-  static_assert(3 * (D / 32) * 8192 <= 2 * kTile + 2 * 16384, "output rows");
   static_assert(kCtasPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
@@ -94,10 +100,17 @@ struct BwdChunk {
   int swizzle, unit;
 };
 
-// DIAG: sums of dT along diagonals (run: the partial sum in this lane; diag: where lane 31 leaves finished ones).
+// (Two predicated additions; a choice of addends costs two more instructions a score.)
+__device__ __forceinline__ void add_either(bool first, float v, float& a, float& b) {
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t@p add.f32 %0, %0, %3;\n\t@!p add.f32 %1, %1, %3;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "r"((int)first), "f"(v));
+}
+
+// DIAG: adds dT to the lane's two diagonals of the 32 x 32 block (k0: the chunk's first column in it).
 template <bool CAP, bool BIAS, bool DIAG, bool MASK>
-__device__ __forceinline__ void bwd_chunk(const BwdChunk& ch, const Cap& cap, float scale2, int lane, float& run,
-                                          float* diag) {
+__device__ __forceinline__ void bwd_chunk(const BwdChunk& ch, const Cap& cap, float scale2, int lane, int k0, float& pos,
+                                          float& neg) {
   uint32_t sv[16], dp[16];
   tmem_ld_32x32b_x16_async(ch.t_s, sv);
   tmem_ld_32x32b_x16_async(ch.t_dp, dp);
@@ -134,9 +147,8 @@ __device__ __forceinline__ void bwd_chunk(const BwdChunk& ch, const Cap& cap, fl
         u[q] = see ? u[q] : 0.f;
       }
       if (DIAG) {
-        const float up = __shfl_up_sync(0xffffffffu, run, 1);
-        run = lane == 0 ? dt : up + dt;
-        if (lane == 31) diag[k + q] = run;
+        const int row = lane + k0 + k + q;                 // (mod 32)
+        add_either(row < 32, __shfl_sync(0xffffffffu, dt, row), pos, neg);
       }
     }
     pp[k / 2] = half2_of(p[0], p[1]);
@@ -153,30 +165,28 @@ template <int D, bool CAP, bool BIAS, bool DIAG>
 __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
     scored_tc_bwd_short_kernel(const __grid_constant__ ScoreArgs s, const __grid_constant__ CUtensorMap tm_qkv,
                                const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_out,
-                               const int32_t* __restrict__ valid_len, const __half* __restrict__ qkv,
-                               const __half* __restrict__ ctx, const float* __restrict__ lse,
-                               const __half* __restrict__ dctx, __half* __restrict__ dqkv, float* __restrict__ partial,
+                               const int32_t* __restrict__ valid_len, const __half* __restrict__ ctx,
+                               const float* __restrict__ lse, __half* __restrict__ dqkv, float* __restrict__ partial,
                                int B, int S, int NH, int* __restrict__ status) {
   using C = SBCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = sbase + C::kBars;
-  const uint32_t qk_full = bar0, vo_full = bar0 + 8, s_full = bar0 + 16, p_full = bar0 + 24, acc_full = bar0 + 32,
-                 free_bar = bar0 + 40, group = bar0 + 48, drain = bar0 + 56;
+  const uint32_t full = bar0, s_full = bar0 + 8, p_full = bar0 + 16, acc_full = bar0 + 24, acc_free = bar0 + 32,
+                 group = bar0 + 40, drain = bar0 + 48;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kSlot);
   float* warp_max = reinterpret_cast<float*>(smem + C::kMax);
   float* col = reinterpret_cast<float*>(smem + C::kCol);
   int* pos_docs = reinterpret_cast<int*>(smem + C::kDocs);
   float* column = reinterpret_cast<float*>(smem + C::kColumn);
   float* lut = reinterpret_cast<float*>(smem + C::kLut);
-  uint8_t* bucket_of = smem + C::kBucket;
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   if (tid == 0) {
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 7; ++k) {
       const uint32_t bar = bar0 + 8 * k;
-      mbar_init(bar, bar == p_full || bar == free_bar || bar == group ? kRowWarps : 1);
+      mbar_init(bar, bar == p_full || bar == acc_free || bar == group ? kRowWarps : 1);
     }
     fence_barrier_init();
   }
@@ -192,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
   pdl_trigger();                                           // after taking TMEM
 
   // Items [first, last) of B * NH, item = head * B + sequence.
-  const int items = B * NH, ctas = gridDim.x, cta = blockIdx.x;
-  const int first = (int)((long long)items * cta / ctas), last = (int)((long long)items * (cta + 1) / ctas);
+  const int items = B * NH;
+  const int first = first_item(blockIdx.x, items, gridDim.x), last = first_item(blockIdx.x + 1, items, gridDim.x);
   auto length = [&](int item) { return score_len(valid_len, item % B, S); };
   bool ok = true;
   if (warp == kRowWarps) {
@@ -212,34 +222,26 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
       while (item < last && length(item) == 0) ++item;
       return item;
     };
-    auto load_qk = [&](int item) {
-      mbar_arrive_expect_tx(qk_full, 2 * C::kTile);
-      for (int part = 0; part < 2; ++part)
+    auto load = [&](int item) {
+      const int b = item % B, h = item / B;
+      mbar_arrive_expect_tx(full, 4 * C::kTile);
+      for (int part = 0; part < 3; ++part)
         for (int u = 0; u < C::kSub; ++u)
-          tma_load_3d(&tm_qkv, sbase + (part ? C::kK : C::kQ) + u * 16384, qk_full, 64 * u, 0,
-                      (part * B + item % B) * NH + item / B);
+          tma_load_3d(&tm_qkv, sbase + (part == 0 ? C::kQ : part == 1 ? C::kK : C::kV) + u * 16384, full, 64 * u, 0,
+                      (part * B + b) * NH + h);
+      for (int u = 0; u < C::kSub; ++u) tma_load_3d(&tm_do, sbase + C::kDO + u * 16384, full, h * D + 64 * u, 0, b);
     };
-    auto load_vo = [&](int item) {
-      mbar_arrive_expect_tx(vo_full, 2 * C::kTile);
-      for (int u = 0; u < C::kSub; ++u) {
-        tma_load_3d(&tm_qkv, sbase + C::kV + u * 16384, vo_full, 64 * u, 0, (2 * B + item % B) * NH + item / B);
-        tma_load_3d(&tm_do, sbase + C::kDO + u * 16384, vo_full, (item / B) * D + 64 * u, 0, item % B);
-      }
-    };
-    int qk_loads = 0, vo_loads = 0, it = 0;
+    int loads = 0, it = 0;
     int cur = next_loaded(first);
     if (cur < last) {
-      if (elect_one()) load_qk(cur);
-      qk_loads = 1;
+      if (elect_one()) load(cur);
+      loads = 1;
     }
     for (; cur < last; ++it) {
       const uint32_t ph = it & 1;
       const int n = length(cur), nxt = next_loaded(cur + 1);
-      // The previous item's accumulators have been read, and its output rows over dO, V and dU^T stored.
-      if (it > 0 && !(ok = warp_wait(free_bar, ph ^ 1))) break;
-      if (elect_one()) load_vo(cur);
-      ++vo_loads;
-      if (!(ok = warp_wait(qk_full, ph))) break;
+      if (!(ok = warp_wait(full, ph))) break;
+      if (it > 0 && !(ok = warp_wait(acc_free, ph ^ 1))) break;              // the previous item's accumulators
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -247,10 +249,6 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
           const uint32_t o = (kk / 4) * 16384 + (kk % 4) * 32;
           mma_f16_ss(tmem, desc_at(k_desc, o), desc_at(q_desc, o), idesc_s, kk > 0 ? 1u : 0u);
         }
-      }
-      __syncwarp();
-      if (!(ok = warp_wait(vo_full, ph))) break;
-      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t o = (kk / 4) * 16384 + (kk % 4) * 32;
@@ -279,25 +277,23 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
         mma_commit(acc_full);
       }
       __syncwarp();
-      if (nxt < last) {                                    // Q and K have been read
+      if (nxt < last) {                                    // the tiles have been read
         if (!(ok = warp_wait(acc_full, ph))) break;
-        if (elect_one()) load_qk(nxt);
-        ++qk_loads;
+        if (elect_one()) load(nxt);
+        ++loads;
       }
       cur = nxt;
     }
     if (elect_one()) mma_commit(drain);                    // every MMA issued here has completed
     __syncwarp();
     warp_wait(drain, 0);
-    if (qk_loads) warp_wait(qk_full, (qk_loads - 1) & 1);  // and every load has landed
-    if (vo_loads) warp_wait(vo_full, (vo_loads - 1) & 1);
+    if (loads) warp_wait(full, (loads - 1) & 1);           // and every load has landed
   } else {
     const int w = warp >> 2, quad = warp & 3, r = quad * 32 + lane;          // warpgroup; key row = TMEM lane
     const uint32_t t_row = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const Cap cap = make_cap(s);
     const float scale2 = s.scale * kLog2e;
-    float* sums = reinterpret_cast<float*>(smem + C::kSums) + warp * kMaxScoreBuckets;
-    float* diag = reinterpret_cast<float*>(smem + C::kDiag) + warp * 32;
+    float* diag = reinterpret_cast<float*>(smem + C::kDiag);     // [row warp][g][64]: row less column + 32
     int it = 0, built = -1;
     uint32_t group_ph = 0;
     auto group_sync = [&] {                                // the row warps, bounded
@@ -306,8 +302,27 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
       ok = ok && warp_wait(group, group_ph);
       group_ph ^= 1;
     };
+    // Half a row of O, and the row's lse, of an item (two threads to a row), asked for one item ahead.
+    constexpr int kUnits = D / 16;                         // 16-byte units of half a row
+    const int srow = tid >> 1, shalf = tid & 1;
+    uint4 o_row[kUnits];
+    float lse_row = 0.f;
+    auto ask = [&](int item) {
+      const int b = item % B, h = item / B;
+      if (item >= last || srow >= score_len(valid_len, b, S)) return;
+      const uint4* at = reinterpret_cast<const uint4*>(ctx + ((size_t)b * S + srow) * NH * D + (size_t)h * D) + shalf * kUnits;
+#pragma unroll
+      for (int k = 0; k < kUnits; ++k) o_row[k] = at[k];
+      lse_row = lse[((size_t)b * NH + h) * S + srow];
+    };
+    ask(first);
+    float by_distance = 0.f;                               // of distance tid - 127, over a head's items here
     for (int item = first; item < last; ++item) {
       const int b = item % B, h = item / B;
+      if (DIAG && item > first && b == 0) {
+        partial[(size_t)max(first, item - B) * 256 + tid] = by_distance;
+        by_distance = 0.f;
+      }
       const size_t bh = (size_t)b * NH + h;
       const int n = score_len(valid_len, b, S), prefix = score_prefix(s, b);
       if (BIAS && h != built) {                            // the head's bias, for distances within the sequence
@@ -316,10 +331,7 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
         load_column(s, column, NH, h, tid, 32 * kRowWarps);
         group_sync();
         const float slope = s.slopes ? s.slopes[h] : 0.f;
-        for (int k = 128 - S + tid; k <= 126 + S; k += 32 * kRowWarps) {
-          lut[k] = score_bias2(s, column, slope, k - 127);
-          if (DIAG) bucket_of[k] = static_cast<uint8_t>(score_bucket(s, k - 127));
-        }
+        for (int k = 128 - S + tid; k <= 126 + S; k += 32 * kRowWarps) lut[k] = score_bias2(s, column, slope, k - 127);
         group_sync();
         if (!ok) break;
       }
@@ -328,54 +340,44 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
           uint4* out = reinterpret_cast<uint4*>(dqkv + (((size_t)part * B * NH + bh) * S) * D);
           for (int k = tid; k < S * (D / 8); k += 32 * kRowWarps) out[k] = make_uint4(0, 0, 0, 0);
         }
-        if (DIAG)
-          for (int k = tid; k < s.buckets; k += 32 * kRowWarps) partial[bh * s.buckets + k] = 0.f;
+        ask(item + 1);
         continue;
       }
       const uint32_t ph = it & 1;
       ++it;
-      // Row statistics while the tiles load: D / 8 lanes to a row.
+      // Row statistics: two threads to a row.
       {
-        constexpr int kLanes = D / 8;
-        const int gl = tid % kLanes;
-        float mo = 0.f, mv = 0.f;
-        group_sync();                                      // the previous item's have been read
+        const float l = srow < n ? lse_row * kLog2e : INFINITY;
+        if (s.docs && shalf == 0) pos_docs[srow] = srow < n ? s.docs[(size_t)b * S + srow] : 0;
+        if (!(ok = warp_wait(full, ph))) break;
+        float dot = 0.f, oo = 0.f, vv = 0.f;
+        if (srow < n) {
 #pragma unroll
-        for (int pass = 0; pass < 128 * kLanes / (32 * kRowWarps); ++pass) {
-          const int i = pass * (32 * kRowWarps / kLanes) + tid / kLanes;
-          float dot = 0.f, oo = 0.f, vv = 0.f;
-          if (i < n) {
-            const size_t at = ((size_t)b * S + i) * NH * D + (size_t)h * D + gl * 8;
-            const uint4 o4 = *reinterpret_cast<const uint4*>(ctx + at), g4 = *reinterpret_cast<const uint4*>(dctx + at);
-            const uint4 v4 = *reinterpret_cast<const uint4*>(qkv + ((2 * (size_t)B * NH + bh) * S + i) * D + gl * 8);
-            const uint32_t ow[4] = {o4.x, o4.y, o4.z, o4.w}, gw[4] = {g4.x, g4.y, g4.z, g4.w},
+          for (int k = 0; k < kUnits; ++k) {
+            const int u = shalf * kUnits + k, at = (u / 8) * 16384 + srow * 128 + 16 * ((u % 8) ^ (srow & 7));
+            const uint4 g4 = *reinterpret_cast<const uint4*>(smem + C::kDO + at);
+            const uint4 v4 = *reinterpret_cast<const uint4*>(smem + C::kV + at);
+            const uint32_t ow[4] = {o_row[k].x, o_row[k].y, o_row[k].z, o_row[k].w}, gw[4] = {g4.x, g4.y, g4.z, g4.w},
                            vw[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&ow[k]));
-              const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&gw[k]));
-              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&vw[k]));
+            for (int q = 0; q < 4; ++q) {
+              const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&ow[q]));
+              const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&gw[q]));
+              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&vw[q]));
               dot = fmaf(o.x, g.x, fmaf(o.y, g.y, dot));
               oo = fmaf(g.x, g.x, fmaf(g.y, g.y, oo));
               vv = fmaf(v.x, v.x, fmaf(v.y, v.y, vv));
             }
           }
-#pragma unroll
-          for (int off = kLanes / 2; off > 0; off >>= 1) {
-            dot += __shfl_xor_sync(0xffffffffu, dot, off);
-            oo += __shfl_xor_sync(0xffffffffu, oo, off);
-            vv += __shfl_xor_sync(0xffffffffu, vv, off);
-          }
-          mo = fmaxf(mo, oo);
-          mv = fmaxf(mv, vv);
-          if (gl == 0) {
-            const float l = i < n ? lse[bh * S + i] * kLog2e : INFINITY;
-            col[i] = l == -INFINITY ? INFINITY : l;
-            col[128 + i] = dot;
-          }
+        }
+        dot += __shfl_xor_sync(0xffffffffu, dot, 1);
+        float mo = oo + __shfl_xor_sync(0xffffffffu, oo, 1), mv = vv + __shfl_xor_sync(0xffffffffu, vv, 1);
+        if (shalf == 0) {
+          col[srow] = l == -INFINITY ? INFINITY : l;
+          col[128 + srow] = dot;
         }
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
+        for (int off = 16; off > 1; off >>= 1) {
           mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, off));
           mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, off));
         }
@@ -383,9 +385,7 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
           warp_max[warp] = mo;
           warp_max[kRowWarps + warp] = mv;
         }
-        if (s.docs && tid < 128) pos_docs[tid] = tid < n ? s.docs[(size_t)b * S + tid] : 0;
-        if (DIAG)
-          for (int k = lane; k < s.buckets; k += 32) sums[k] = 0.f;
+        if (lane == 0) bulk_wait_group_read<0>();          // the last output rows have left dU^T's tile
         group_sync();
         if (!ok) break;
       }
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
       tc_fence_after();
 #pragma unroll 1
       for (int g = 0; g < 2; ++g) {
-        float run = 0.f;
+        float pos = 0.f, neg = 0.f;                        // diagonals lane and lane - 32
         const int i0 = 64 * g + 32 * w;
         const bool none = w0 >= n || i0 >= n || i0 + 32 <= min(ilow_first, score_ilow(s, min(w1, n - 1), prefix));
 #pragma unroll 1
@@ -435,18 +435,14 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
             *reinterpret_cast<uint4*>(ch.du + 16 * (ch.unit ^ ch.swizzle)) = make_uint4(0, 0, 0, 0);
             *reinterpret_cast<uint4*>(ch.du + 16 * ((ch.unit + 1) ^ ch.swizzle)) = make_uint4(0, 0, 0, 0);
           } else if (s.docs || w1 >= n || i + 16 > n || i < ilow_all) {
-            bwd_chunk<CAP, BIAS, DIAG, true>(ch, cap, scale2, lane, run, diag + c);
+            bwd_chunk<CAP, BIAS, DIAG, true>(ch, cap, scale2, lane, c, pos, neg);
           } else {
-            bwd_chunk<CAP, BIAS, DIAG, false>(ch, cap, scale2, lane, run, diag + c);
+            bwd_chunk<CAP, BIAS, DIAG, false>(ch, cap, scale2, lane, c, pos, neg);
           }
         }
-        if (DIAG && !none) {
-          // diag[k]: the diagonal that left lane 31 at column k, distance w1 - (i0 + k); run: the one in this lane.
-          // Distances outside the sequence have sums of 0 and may go anywhere.
-          auto bucket_at = [&](int rel) { return (int)bucket_of[127 + max(1 - S, min(S - 1, rel))]; };
-          __syncwarp();
-          add_by_bucket(diag[lane], bucket_at(w1 - i0 - lane), sums, lane);
-          add_by_bucket(lane == 31 ? 0.f : run, bucket_at(w0 + lane - (i0 + 31)), sums, lane);
+        if (DIAG) {
+          diag[(warp * 2 + g) * 64 + 32 + lane] = pos;
+          diag[(warp * 2 + g) * 64 + lane] = neg;
         }
       }
       // Rows in [n, n rounded up to 16) of the operands that the last three products sum over: zeros, whatever
@@ -467,18 +463,20 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
       if (DIAG) {
         group_sync();
         if (!ok) break;
-        const float* all = reinterpret_cast<const float*>(smem + C::kSums);
-        for (int k = tid; k < s.buckets; k += 32 * kRowWarps) {
-          float total = 0.f;
+        // Distance tid - 127: block (quad, i0 / 32) has it at row less column tid - 127 - 32 (quad - i0 / 32).
+        float total = 0.f;
 #pragma unroll
-          for (int v = 0; v < kRowWarps; ++v) total += all[v * kMaxScoreBuckets + k];
-          partial[bh * s.buckets + k] = total * inv_e;
+        for (int v = 0; v < kRowWarps * 2; ++v) {          // row warp v / 2, g = v % 2
+          const int d = tid - 127 - 32 * ((v / 2) % 4 - (2 * (v % 2) + v / 8));
+          if (d >= -32 && d < 32) total += diag[v * 64 + 32 + d];
         }
+        by_distance += total * inv_e;                      // (the 256th is not used)
       }
+      ask(item + 1);
       if (!(ok = warp_wait(acc_full, ph))) break;
       tc_fence_after();
-      // 32 columns of an accumulator at a time, the warpgroups in turn: FP16 rows of 64 bytes over dO, V and dU^T
-      // in the store's swizzle, one TMA store for a warp's 32 rows.
+      // 32 columns of an accumulator at a time, the warpgroups in turn: FP16 rows of 64 bytes in the store's swizzle
+      // over dU^T's tile, in one of the warp's two places in turn, and a TMA store for its 32 rows.
       constexpr int kPieces = 3 * (D / 32);
 #pragma unroll 1
       for (int piece = w; piece < kPieces; piece += 2) {
@@ -486,7 +484,16 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
         const float f = !mine ? 0.f : part == 2 ? 1.f : s.scale * inv_e;
         uint32_t oa[32];
         tmem_ld_32x32b_x32(t_row + (part == 0 ? C::kDQ : part == 1 ? C::kDK : C::kDV) + c, oa);
-        uint8_t* tile = smem + C::kOut + piece * 8192 + quad * 2048;
+        uint8_t* tile = smem + C::kDU + warp * 4096 + ((piece >> 1) & 1) * 2048;
+        if (piece >= 4) {
+          if (lane == 0) bulk_wait_group_read<1>();
+          __syncwarp();
+        }
+        if (piece + 2 >= kPieces) {                        // all that this warp reads has been read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(acc_free);
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t v[4];
@@ -502,13 +509,9 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
           bulk_commit_group();
         }
       }
-      tc_fence_before();
-      if (lane == 0) {
-        bulk_wait_group_read<0>();
-        mbar_arrive(free_bar);
-      }
-      __syncwarp();
     }
+    if (DIAG && first < last) partial[(size_t)max(first, (last - 1) / B * B) * 256 + tid] = by_distance;
+    if (lane == 0) bulk_wait_group_read<0>();
   }
 
   if (!ok) atomicCAS(status, 0, kStatusWaitTimeout);
@@ -534,9 +537,8 @@ cudaError_t launch_v(const ScoreArgs& s, const __half* qkv, const int32_t* vl, c
       !encode_operand_map(&td, dctx, (uint64_t)sh.head_num * D, sh.seq, sh.batch, 64, 128) ||
       !encode_operand_map(&to, dqkv, D, sh.seq, planes, 32, 32))
     return cudaErrorInvalidValue;
-  const long items = (long)sh.batch * sh.head_num, resident = (long)C::kCtasPerSm * num_sms;
-  return launch_kernel(kern, dim3((unsigned)(items < resident ? items : resident)), dim3(kThreads), C::kSmem, stream,
-                       nullptr, 0, s, tq, td, to, vl, qkv, ctx, lse, dctx, dqkv, partial, sh.batch, sh.seq, sh.head_num,
+  return launch_kernel(kern, dim3(scored_short_ctas(sh, num_sms)), dim3(kThreads), C::kSmem, stream,
+                       nullptr, 0, s, tq, td, to, vl, ctx, lse, dqkv, partial, sh.batch, sh.seq, sh.head_num,
                        status);
 }
 
@@ -552,6 +554,11 @@ cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, c
 
 }  // namespace
 }  // namespace scored_tc
+
+int scored_short_ctas(const ScoredShape& sh, int num_sms) {
+  const long items = (long)sh.batch * sh.head_num, resident = (sh.size_per_head > 64 ? 1L : 2L) * num_sms;
+  return (int)(items < resident ? items : resident);
+}
 
 cudaError_t launch_scored_backward_tc_short(const ScoreArgs& s, const __half* qkv, const int32_t* valid_len,
                                             const __half* ctx, const float* lse, const __half* dctx, __half* dqkv,
