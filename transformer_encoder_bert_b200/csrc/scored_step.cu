@@ -14,7 +14,10 @@
 // each.  A lane group takes kU rows of K and the same rows of V at a time,
 // through a ring of kStages stages in shared memory that cp.async fills: every
 // thread reads back only what it asked for itself, so the ring needs no barrier
-// and the loads of two stages (32 KB each) stay in flight under the arithmetic.
+// and the next stage's loads stay in flight under the arithmetic, with three CTAs
+// of 256 threads (32 KB a stage) to an SM.  Measured at 16 heads of 64, 32
+// sequences, capacity 4096, caches half to wholly full: 85 us, 4.7 TB/s of the
+// measured 6.56 (93 us with a cap and a table); two CTAs with three stages 100 us.
 // The kU dot products are added up over the group by halving: each exchange
 // passes half of the rows on, so that a lane ends with the score of one row and
 // bias, cap and exponential are worked out once per row.  The group keeps a
@@ -26,17 +29,25 @@
 namespace enc {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kU = 4;                                      // rows of K and of V per lane group and stage
-constexpr int kStages = 3;
-constexpr int kStageBytes = 2 * kU * kThreads * 16;
+constexpr int kStages = 2;
+constexpr int kShortCache = 512;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 template <typename T>
 struct Vec;                                                // the 16 bytes of a lane as floats
 template <>
 struct Vec<__half> {
   static constexpr int N = 8;
+  // 1 - 2 / (1 + 2^(2 x log2 e)), off by about 2^-22: far below the rounding of the result to FP16.
+  static __device__ __forceinline__ float tanh_of(float x) {
+    return 1.f - __fdividef(2.f, 1.f + ex2(x * (2.f * kLog2e)));
+  }
   static __device__ __forceinline__ void widen(const uint4& w, float (&f)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -50,6 +61,7 @@ struct Vec<__half> {
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
+  static __device__ __forceinline__ float tanh_of(float x) { return tanhf(x); }
   static __device__ __forceinline__ void widen(const uint4& w, float (&f)[4]) {
     f[0] = __uint_as_float(w.x); f[1] = __uint_as_float(w.y);
     f[2] = __uint_as_float(w.z); f[3] = __uint_as_float(w.w);
@@ -58,11 +70,6 @@ struct Vec<float> {
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // 2^(m - to), 0 for a part that has seen nothing.
 __device__ __forceinline__ float weight2(float m, float to) { return m == -INFINITY ? 0.f : ex2(m - to); }
 
@@ -76,11 +83,12 @@ __device__ __forceinline__ uint4 shared16(uint32_t addr) {
   return v;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, int D, int kThreads>
+__global__ void __launch_bounds__(kThreads, 768 / kThreads)
     scored_step_kernel(const __grid_constant__ ScoreArgs s, const T* __restrict__ qkv, T* __restrict__ cache,
                        const int32_t* __restrict__ len, T* __restrict__ ctx, int B, int C, int NH) {
   constexpr int N = Vec<T>::N;
+  constexpr int kWarps = kThreads / 32, kStageBytes = 2 * kU * kThreads * 16;
   constexpr int kLanes = D / N;                            // lanes of a row
   constexpr int kGroups = kThreads / kLanes;
   static_assert(kU == 4 && kLanes >= kU && kLanes <= 32, "a lane of the group per row");
@@ -130,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int doc = s.docs && held ? s.docs[(size_t)b * C + p] : 0;
   __syncthreads();
 
+  const float inv_cap = s.cap > 0.f ? 1.f / s.cap : 0.f;
   float m = -INFINITY, l = 0.f, o[N] = {};                 // l: of the rows that this lane scored
   int stage = 0;
   for (int j0 = lo; j0 < hi; j0 += kStep) {
@@ -166,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     float t = (up1 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, up1 ? k0 : k1, 1);
 #pragma unroll
     for (int off = 4; off < kLanes; off <<= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-    if (s.cap > 0.f) t = s.cap * tanhf(t / s.cap);
+    if (s.cap > 0.f) t = s.cap * Vec<T>::tanh_of(t * inv_cap);
     // A row that is not seen has t = -inf, whatever its K and V hold.
     t = bias == -INFINITY ? -INFINITY : (t + bias) * kLog2e;
     float mx = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
@@ -235,31 +244,41 @@ __global__ void __launch_bounds__(kThreads, 2)
   sm100::cluster_sync();                                   // the parts stay until rank 0 has read them
 }
 
-template <typename T, int D>
-cudaError_t step_d(const ScoreArgs& s, const void* qkv, void* cache, const int32_t* len, void* ctx, int ranks,
+template <typename T, int D, int kThreads>
+cudaError_t step_t(const ScoreArgs& s, const void* qkv, void* cache, const int32_t* len, void* ctx, int ranks,
                    const ScoredShape& sh, cudaStream_t stream) {
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      scored_step_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStages * kStageBytes);
+  constexpr int kBytes = kStages * 2 * kU * kThreads * 16;
+  auto kern = scored_step_kernel<T, D, kThreads>;
+  static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (attr != cudaSuccess) return attr;
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;
   cluster.val.clusterDim.x = (unsigned)ranks;
   cluster.val.clusterDim.y = 1;
   cluster.val.clusterDim.z = 1;
-  return launch_kernel(scored_step_kernel<T, D>, dim3((unsigned)ranks, sh.head_num, sh.batch), dim3(kThreads),
-                       kStages * kStageBytes, stream, &cluster, 1, s, static_cast<const T*>(qkv), static_cast<T*>(cache), len,
+  return launch_kernel(kern, dim3((unsigned)ranks, sh.head_num, sh.batch), dim3(kThreads), kBytes, stream, &cluster, 1, s, static_cast<const T*>(qkv), static_cast<T*>(cache), len,
                        static_cast<T*>(ctx), sh.batch, sh.seq, sh.head_num);
+}
+
+// Short caches leave 256 threads few rows each: 128 threads a CTA, six CTAs an SM (12 heads of 64, 200 sequences,
+// capacity 128: 31 -> 23 us); long ones stream better with 256 (16 heads of 64, 32 sequences, 4096: 96 -> 85 us).
+template <typename T, int D>
+cudaError_t step_d(const ScoreArgs& s, const void* qkv, void* cache, const int32_t* len, void* ctx, int ranks,
+                   const ScoredShape& sh, cudaStream_t stream) {
+  return sh.seq <= kShortCache ? step_t<T, D, 128>(s, qkv, cache, len, ctx, ranks, sh, stream)
+                               : step_t<T, D, 256>(s, qkv, cache, len, ctx, ranks, sh, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_scored_step(const ScoreArgs& s, const void* qkv, void* cache, const int32_t* len, void* ctx,
                                const ScoredShape& sh, bool half, int num_sms, cudaStream_t stream) {
-  // Four waves of two CTAs per SM, so that sequences of different lengths even out, but at least 128 positions
-  // of a full cache to a CTA; 8 is the portable cluster size.
+  // About four CTAs per SM and more, so that sequences of different lengths even out (with one or two CTAs to an
+  // item, 512 items of 4096 took 106 us; with two to four, 85; with eight, 141), but at least 128 positions of a full
+  // cache to a CTA; 8 is the portable cluster size.
   const long items = (long)sh.batch * sh.head_num;
   int ranks = 1;
-  while (ranks < 8 && items * ranks < 8L * num_sms && sh.seq >= 256 * ranks) ranks *= 2;
+  while (ranks < 8 && items * ranks < 4L * num_sms && sh.seq >= 256 * ranks) ranks *= 2;
   switch (sh.size_per_head) {
     case 32:
       return half ? step_d<__half, 32>(s, qkv, cache, len, ctx, ranks, sh, stream)
