@@ -39,6 +39,18 @@ __host__ __device__ __forceinline__ int score_bucket(const ScoreArgs& s, int rel
   return c + (s.both && rel > 0 ? nb : 0);
 }
 
+// The relative positions [lo, hi] of bucket c, within +-reach (empty where lo > hi).
+__device__ __forceinline__ void bucket_range(const ScoreArgs& s, int c, int& lo, int& hi) {
+  const int nb = s.both ? s.buckets >> 1 : s.buckets, exact = nb >> 1;
+  const bool ahead = s.both && c >= nb;                    // positive relative positions
+  const int cc = ahead ? c - nb : c;
+  const int a0 = cc < exact ? cc : cc == exact ? exact : s.bounds[cc - exact - 1];
+  const int a1 = cc < exact ? cc : cc == nb - 1 ? s.reach : s.bounds[cc - exact] - 1;
+  lo = ahead ? max(a0, 1) : -a1;
+  hi = ahead ? a1 : -a0;
+  if (!s.both && cc == 0) hi = s.reach;                    // one direction: every key ahead
+}
+
 // The part of t2 that depends on the distance alone; column: the head's column of the table.
 __device__ __forceinline__ float score_bias2(const ScoreArgs& s, const float* column, float slope, int rel) {
   float b = -slope * fabsf(static_cast<float>(rel));

@@ -246,7 +246,10 @@ __global__ void __launch_bounds__(kThreads)
   float* Vs = Ks + kT * (D + 4);
   float* Ps = Vs + kT * (D + 4);
   TileInfo* ti = reinterpret_cast<TileInfo*>(Ps + kT * kPs);
-  __shared__ float diag[2 * kT], bucket_sum[kMaxScoreBuckets];
+  // Sums of dT by distance within +-reach (index distance + reach), and past it on either side.
+  float* by_distance = reinterpret_cast<float*>(ti + 1);
+  float far_left = 0.f, far_right = 0.f;
+  __shared__ float far[2][2 * kT];
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.z, h = blockIdx.y, qb = gridDim.x - 1 - blockIdx.x, q0 = qb * kT;
@@ -264,7 +267,8 @@ __global__ void __launch_bounds__(kThreads)
   fill_docs(ti->row_doc, s, b, S, q0);
   load_column(s, ti->column, NH, h, threadIdx.x, kThreads);
   __syncthreads();
-  if (partial && threadIdx.x < kMaxScoreBuckets) bucket_sum[threadIdx.x] = 0.f;
+  if (partial)
+    for (int k = threadIdx.x; k <= 2 * s.reach; k += kThreads) by_distance[k] = 0.f;
   float lse2[4], dsum[4];
 #pragma unroll
   for (int a = 0; a < 4; ++a) {
@@ -297,32 +301,23 @@ __global__ void __launch_bounds__(kThreads)
         acc[a][c] = dt * sl;
       }
     }
-    if (partial) {                       // sums of dT along the tile's 127 diagonals, then by bucket
+    if (partial) {                       // the tile's 127 diagonals, a thread each
       __syncthreads();
-      const int t = threadIdx.x, d0 = t - (kT - 1);
-      if (t < 2 * kT - 1) {
+      const int d0 = (int)threadIdx.x - (kT - 1), rel = j0 - q0 + d0;
+      if (d0 < kT) {
         float sum = 0.f;
+#pragma unroll 8
         for (int r = max(0, -d0); r < min(kT, kT - d0); ++r) sum += Ps[r * kPs + r + d0];
-        diag[t] = sum;
+        if (rel <= -s.reach)
+          far_left += sum;
+        else if (rel >= s.reach)
+          far_right += sum;
+        else
+          by_distance[rel + s.reach] += sum;
       }
-      __syncthreads();
-      // The distances of one bucket are consecutive, so each bucket of the tile
-      // has one first diagonal, whose thread adds the bucket's sum.
-      const int rel0 = j0 - q0;
-      if (t < 2 * kT - 1) {
-        const int c = score_bucket(s, rel0 + d0);
-        if (t == 0 || score_bucket(s, rel0 + d0 - 1) != c) {
-          float sum = 0.f;
-          for (int k = t; k < 2 * kT - 1 && (k == t || score_bucket(s, rel0 + k - (kT - 1)) == c); ++k) sum += diag[k];
-          bucket_sum[c] += sum;
-        }
-      }
-      if (s.cap > 0.f)
-#pragma unroll
-        for (int a = 0; a < 4; ++a)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) Ps[(4 * ty + a) * kPs + tx + 16 * c] = acc[a][c];
-    } else if (s.cap > 0.f) {
+      if (s.cap > 0.f) __syncthreads();
+    }
+    if (s.cap > 0.f) {
 #pragma unroll
       for (int a = 0; a < 4; ++a)
 #pragma unroll
@@ -340,8 +335,30 @@ __global__ void __launch_bounds__(kThreads)
     for (int e = 0; e < D / 16; ++e) put(dq + (bh * S + i) * D + out_col<D>(e), out[a][e] * s.scale);
   }
   if (partial) {
+    if (threadIdx.x < 2 * kT) {
+      far[0][threadIdx.x] = far_left;
+      far[1][threadIdx.x] = far_right;
+    }
     __syncthreads();
-    if (threadIdx.x < s.buckets) partial[(bh * gridDim.x + qb) * s.buckets + threadIdx.x] = bucket_sum[threadIdx.x];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp < 2) {                      // both ends
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2 * kT; k += 32) sum += far[warp][k + lane];
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      if (lane == 0) by_distance[warp * 2 * s.reach] = sum;
+    }
+    __syncthreads();
+    for (int c = warp; c < s.buckets; c += kThreads / 32) {
+      int lo, hi;
+      bucket_range(s, c, lo, hi);
+      float sum = 0.f;
+      for (int k = lo + lane; k <= hi; k += 32) sum += by_distance[k + s.reach];
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      if (lane == 0) partial[(bh * gridDim.x + qb) * s.buckets + c] = sum;
+    }
   }
 }
 
@@ -460,18 +477,15 @@ __global__ void __launch_bounds__(kThreads)
     scored_table_grad_kernel(const __grid_constant__ ScoreArgs s, const float* __restrict__ partial,
                              float* __restrict__ dtable, int B, int blocks, int short_ctas, int S, int NH) {
   __shared__ double sums[kThreads / 32];
-  __shared__ int range[2];
   const int h = blockIdx.x, c = blockIdx.y, t = threadIdx.x;
   double sum = 0.0;
   if (short_ctas) {
-    if (t < 2) range[t] = t == 0 ? 256 : 0;
-    __syncthreads();
-    if (t >= 128 - S && t <= 126 + S && score_bucket(s, t - 127) == c) {
-      atomicMin(&range[0], t);
-      atomicMax(&range[1], t + 1);
-    }
-    __syncthreads();
-    const int at = range[0], count = max(0, range[1] - at), items = B * NH;
+    int lo, hi;
+    bucket_range(s, c, lo, hi);
+    // (past +-reach the bias does not change: the bucket takes the rest)
+    lo = lo <= -s.reach ? 1 - S : max(lo, 1 - S);
+    hi = hi >= s.reach ? S - 1 : min(hi, S - 1);
+    const int at = lo + 127, count = max(0, hi - lo + 1), items = B * NH;
     const int first = cta_of_item(h * B, items, short_ctas), last = cta_of_item(h * B + B - 1, items, short_ctas);
     pdl_wait();
     pdl_trigger();
@@ -522,12 +536,14 @@ cudaError_t fwd_d(const ScoreArgs& s, const void* qkv, const int32_t* vl, void* 
 template <typename T, int D>
 cudaError_t bwd_d(const ScoreArgs& s, const void* qkv, const int32_t* vl, const void* dctx, const float* lse,
                   const float* rowsum, void* dqkv, float* partial, const ScoredShape& sh, cudaStream_t stream) {
-  static const cudaError_t attr1 = allow_smem(scored_dq_kernel<T, D>, smem_bytes<D>(4));
+  const size_t dq_smem = smem_bytes<D>(4) + (partial ? (2 * s.reach + 1) * sizeof(float) : 0);
+  static const cudaError_t attr1 =
+      allow_smem(scored_dq_kernel<T, D>, smem_bytes<D>(4) + (2 * kMaxScoreDistance + 1) * sizeof(float));
   static const cudaError_t attr2 = allow_smem(scored_dkv_kernel<T, D>, smem_bytes<D>(4));
   if (attr1 != cudaSuccess) return attr1;
   if (attr2 != cudaSuccess) return attr2;
   const dim3 grid((sh.seq + kT - 1) / kT, sh.head_num, sh.batch);
-  cudaError_t e = launch_kernel(scored_dq_kernel<T, D>, grid, dim3(kThreads), smem_bytes<D>(4), stream, nullptr, 0, s,
+  cudaError_t e = launch_kernel(scored_dq_kernel<T, D>, grid, dim3(kThreads), dq_smem, stream, nullptr, 0, s,
                                 static_cast<const T*>(qkv), vl, static_cast<const T*>(dctx), lse, rowsum,
                                 static_cast<T*>(dqkv), partial, sh.batch, sh.seq, sh.head_num);
   if (e != cudaSuccess) return e;
