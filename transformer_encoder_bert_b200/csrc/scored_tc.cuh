@@ -176,6 +176,13 @@ __device__ __forceinline__ uint64_t tanh_over_x2(uint64_t z) {
 // tanh(s in) of any size; in2 = 2 in log2 e.
 __device__ __forceinline__ float tanh_of(float s, float in2) { return fmaf(-2.f, rcp(1.f + ex2(s * in2)), 1.f); }
 
+// (Two predicated additions; a choice of addends costs two more instructions a score.)
+__device__ __forceinline__ void add_either(bool first, float v, float& a, float& b) {
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t@p add.f32 %0, %0, %3;\n\t@!p add.f32 %1, %1, %3;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "r"((int)first), "f"(v));
+}
+
 // Adds 32 lanes' values to the warp's bucket sums.  The lanes' distances are consecutive (up or down), so a
 // bucket's lanes are neighbours: a segmented scan, then the last lane of each run adds.
 __device__ __forceinline__ void add_by_bucket(float v, int bucket, float* sums, int lane) {

@@ -26,10 +26,10 @@
 // the FP32 results.
 //
 // The table's gradient (dQ mode) is the sum of dT over every diagonal of equal
-// distance, then over a bucket's distances.  A warp owns 32 rows: the partial
-// sum of a diagonal moves one lane up with each column, so a shuffle and an add
-// per column sum all diagonals of the block in a fixed order; a block whose
-// distances all share a bucket only adds its values up.
+// distance, then over a bucket's distances.  A warp owns 32 rows: with one
+// shuffle a column the 32 values of a column go to 32 lanes by diagonal (see
+// row_chunk), each of which adds up the diagonals of its number in a fixed order;
+// a block whose distances all share a bucket only adds its values up.
 #include "scored_tc.cuh"
 
 namespace enc {
@@ -58,8 +58,7 @@ struct BCfg {
   static constexpr int kNumBars = 2 + 2 * kStages + 3 * NB;
   static constexpr int kSlot = kBars + kNumBars * 8;
   static constexpr int kDocs = (kSlot + 16 + 15) / 16 * 16;   // per row warp: the block's documents
-  static constexpr int kDiag = kDocs + NB * 4 * kBN * 4;      // dQ: per row warp, finished diagonals
-  static constexpr int kSums = kDiag + (MODE == kDQ ? NB * 4 * kBN * 4 : 0);   // dQ: per row warp, bucket sums
+  static constexpr int kSums = kDocs + NB * 4 * kBN * 4;      // dQ: per row warp, bucket sums
   static constexpr int kColumn = kSums + (MODE == kDQ ? NB * 4 * kMaxScoreBuckets * 4 : 0);   // of the bias table
   static constexpr int kLut = kColumn + kMaxScoreBuckets * 4;
   static constexpr int kS = 0, kDP = NB * kBN, kAcc = 2 * NB * kBN;
@@ -81,14 +80,84 @@ struct RowBlock {
   int doc;
   float e, de;              // dU's scale, and D e (dQ mode)
   const float* col;         // dKV mode: lse2 [64], D [64] of the columns (shared memory)
-  float* diag;              // dQ mode: where lane 31 leaves finished diagonals
+  bool whole;               // no row or column of the block is past n
 };
 
-// NEAR 0: linear bias; 1: bias from the table in shared memory; 2: that, and the diagonals' sums.
-// sum: NEAR 2: the diagonal that this lane holds at the end; else += dT.
+// 32 columns of it.  NEAR 0: linear bias; 1: bias from the table in shared memory; 2: that, and the diagonals' sums:
+// for column k, lane t takes dT of row (k - t) mod 32, which lies on the diagonal whose column less row is t (pos) or
+// t - 32 (neg).  Else pos += dT.  POLY: the cap's polynomial.
+template <int MODE, bool CAP, int NEAR, bool MASK, bool POLY>
+__device__ __forceinline__ void row_chunk(const RowBlock& rb, const Cap& cap, float scale2, int lane, int c,
+                                          const uint32_t (&sv)[32], const uint32_t (&dp)[32], float& pos, float& neg) {
+  uint32_t pp[MODE == kDKV ? 16 : 1], pu[16];
+  const float* lut = MODE == kDQ ? rb.lut + c : rb.lut - c;
+  const float base = NEAR ? rb.base : fmaf((float)c, rb.step, rb.base);
+  const int lo = rb.lo - c, hi = rb.hi - c;
+#pragma unroll
+  for (int k = 0; k < 32; k += 4) {
+    float nl[4] = {}, dcol[4];
+    int4 dj = make_int4(0, 0, 0, 0);
+    if (MODE == kDKV) {
+      const float4 a = *reinterpret_cast<const float4*>(rb.col + c + k);
+      const float4 d = *reinterpret_cast<const float4*>(rb.col + kBN + c + k);
+      nl[0] = a.x; nl[1] = a.y; nl[2] = a.z; nl[3] = a.w;
+      dcol[0] = d.x * rb.e; dcol[1] = d.y * rb.e; dcol[2] = d.z * rb.e; dcol[3] = d.w * rb.e;
+    }
+    if (MASK && rb.docs) dj = *reinterpret_cast<const int4*>(rb.docs + c + k);
+    const int djs[4] = {dj.x, dj.y, dj.z, dj.w};
+    float th[4] = {};
+    if constexpr (CAP) {
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        const float s0 = __uint_as_float(sv[k + q]), s1 = __uint_as_float(sv[k + q + 1]);
+        if (POLY) {
+          const uint64_t y = f2_mul(f2_pack(s0, s1), f2_pack(cap.in, cap.in));
+          f2_unpack(f2_mul(y, tanh_over_x2(f2_mul(y, y))), th[q], th[q + 1]);
+        } else {
+          th[q] = tanh_of(s0, 2.f * kLog2e * cap.in);
+          th[q + 1] = tanh_of(s1, 2.f * kLog2e * cap.in);
+        }
+      }
+    }
+    float p[4], u[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float add = NEAR ? base + (MODE == kDQ ? lut[k + q] : lut[-(k + q)]) : fmaf((float)(k + q), rb.step, base);
+      float t = CAP ? fmaf(cap.cap2, th[q], add) : fmaf(__uint_as_float(sv[k + q]), scale2, add);
+      if (MODE == kDKV) t -= nl[q];
+      p[q] = ex2(t);
+      float dt = p[q] * fmaf(__uint_as_float(dp[k + q]), rb.e, MODE == kDKV ? -dcol[q] : -rb.de);
+      u[q] = CAP ? dt * fmaf(-th[q], th[q], 1.f) : dt;
+      if (MASK) {                                          // (hidden scores may be NaN)
+        const bool see = k + q >= lo && k + q < hi && (!rb.docs || djs[q] == rb.doc);
+        p[q] = see ? p[q] : 0.f;
+        dt = see ? dt : 0.f;
+        u[q] = see ? u[q] : 0.f;
+      }
+      if (MODE == kDQ) {
+        if (NEAR == 2)
+          add_either(k + q >= lane, __shfl_sync(0xffffffffu, dt, k + q - lane), pos, neg);
+        else
+          pos += dt;
+      }
+    }
+    if (MODE == kDKV) {
+      pp[k / 2] = half2_of(p[0], p[1]);
+      pp[k / 2 + 1] = half2_of(p[2], p[3]);
+    }
+    pu[k / 2] = half2_of(u[0], u[1]);
+    pu[k / 2 + 1] = half2_of(u[2], u[3]);
+  }
+  // Over columns that this lane has read.
+  if constexpr (MODE == kDKV) tmem_st_32x32b_x16_async(rb.t_s + c / 2, pp);
+  tmem_st_32x32b_x16_async(rb.t_dp + c / 2, pu);
+}
+
+// sums: NEAR 2: the lane's diagonals of the block, 0: columns less rows lane - 32, 1: lane, 2: lane + 32 (from the
+// block's first column and the warp's first row); else sums[1] += dT.
 template <int MODE, bool CAP, int NEAR, bool MASK>
-__device__ __forceinline__ void row_block(const RowBlock& rb, const Cap& cap, float scale2, int lane, float& sum) {
-  float run = 0.f;
+__device__ __forceinline__ void row_block(const RowBlock& rb, const Cap& cap, float scale2, int lane, float (&sums)[3]) {
+  float pos = 0.f, neg = 0.f;
 #pragma unroll 1
   for (int c = 0; c < kBN; c += 32) {
     uint32_t sv[32], dp[32];
@@ -96,75 +165,39 @@ __device__ __forceinline__ void row_block(const RowBlock& rb, const Cap& cap, fl
     tmem_ld_32x32b_x32_async(rb.t_dp + c, dp);
     tmem_wait_ld(sv);
     tmem_wait_ld(dp);
-    uint32_t pp[MODE == kDKV ? 16 : 1], pu[16];
-    const float* lut = MODE == kDQ ? rb.lut + c : rb.lut - c;
-    const float base = NEAR ? rb.base : fmaf((float)c, rb.step, rb.base);
-    const int lo = rb.lo - c, hi = rb.hi - c;
+    bool poly = false;
+    if constexpr (CAP) {
+      float top = 0.f;
 #pragma unroll
-    for (int k = 0; k < 32; k += 4) {
-      float nl[4] = {}, dcol[4];
-      int4 dj = make_int4(0, 0, 0, 0);
-      if (MODE == kDKV) {
-        const float4 a = *reinterpret_cast<const float4*>(rb.col + c + k);
-        const float4 d = *reinterpret_cast<const float4*>(rb.col + kBN + c + k);
-        nl[0] = a.x; nl[1] = a.y; nl[2] = a.z; nl[3] = a.w;
-        dcol[0] = d.x * rb.e; dcol[1] = d.y * rb.e; dcol[2] = d.z * rb.e; dcol[3] = d.w * rb.e;
-      }
-      if (MASK && rb.docs) dj = *reinterpret_cast<const int4*>(rb.docs + c + k);
-      const int djs[4] = {dj.x, dj.y, dj.z, dj.w};
-      float p[4], u[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float s = __uint_as_float(sv[k + q]);
-        const float add = NEAR ? base + (MODE == kDQ ? lut[k + q] : lut[-(k + q)]) : fmaf((float)(k + q), rb.step, base);
-        float t, r = 0.f;
-        if (CAP) {
-          r = tanh_of(s, 2.f * kLog2e * cap.in);
-          t = fmaf(cap.cap2, r, add);
-        } else {
-          t = fmaf(s, scale2, add);
-        }
-        if (MODE == kDKV) t -= nl[q];
-        p[q] = ex2(t);
-        float dt = p[q] * fmaf(__uint_as_float(dp[k + q]), rb.e, MODE == kDKV ? -dcol[q] : -rb.de);
-        u[q] = CAP ? dt * fmaf(-r, r, 1.f) : dt;
-        if (MASK) {                                        // (hidden scores may be NaN)
-          const bool see = k + q >= lo && k + q < hi && (!rb.docs || djs[q] == rb.doc);
-          p[q] = see ? p[q] : 0.f;
-          dt = see ? dt : 0.f;
-          u[q] = see ? u[q] : 0.f;
-        }
-        if (MODE == kDQ) {
-          if (NEAR == 2) {
-            const float up = __shfl_up_sync(0xffffffffu, run, 1);
-            run = lane == 0 ? dt : up + dt;
-            if (lane == 31) rb.diag[c + k + q] = run;
-          } else {
-            sum += dt;
-          }
-        }
-      }
-      if (MODE == kDKV) {
-        pp[k / 2] = half2_of(p[0], p[1]);
-        pp[k / 2 + 1] = half2_of(p[2], p[3]);
-      }
-      pu[k / 2] = half2_of(u[0], u[1]);
-      pu[k / 2 + 1] = half2_of(u[2], u[3]);
+      for (int k = 0; k < 32; k += 2)
+        top = fmaxf(fmaxf(top, fabsf(__uint_as_float(sv[k]))), fabsf(__uint_as_float(sv[k + 1])));
+      poly = rb.whole && !any_warp(top * fabsf(cap.in) > kCapPoly);
     }
-    // Over columns that this lane has read.
-    if constexpr (MODE == kDKV) tmem_st_32x32b_x16_async(rb.t_s + c / 2, pp);
-    tmem_st_32x32b_x16_async(rb.t_dp + c / 2, pu);
+    if (CAP && poly)
+      row_chunk<MODE, CAP, NEAR, MASK, CAP>(rb, cap, scale2, lane, c, sv, dp, pos, neg);
+    else
+      row_chunk<MODE, CAP, NEAR, MASK, false>(rb, cap, scale2, lane, c, sv, dp, pos, neg);
+    if (NEAR == 2 && c == 0) {
+      sums[0] = neg;
+      neg = pos;                                           // the first half's lane is the second's lane - 32
+      pos = 0.f;
+    }
   }
-  if (NEAR == 2) sum = run;
+  if (NEAR == 2) {
+    sums[1] = neg;
+    sums[2] = pos;
+  } else {
+    sums[1] += pos;
+  }
 }
 
 template <int MODE, bool CAP, int NEAR>
 __device__ __forceinline__ void row_block_m(bool mask, const RowBlock& rb, const Cap& cap, float scale2, int lane,
-                                            float& sum) {
+                                            float (&sums)[3]) {
   if (mask)
-    row_block<MODE, CAP, NEAR, true>(rb, cap, scale2, lane, sum);
+    row_block<MODE, CAP, NEAR, true>(rb, cap, scale2, lane, sums);
   else
-    row_block<MODE, CAP, NEAR, false>(rb, cap, scale2, lane, sum);
+    row_block<MODE, CAP, NEAR, false>(rb, cap, scale2, lane, sums);
 }
 
 template <int D, int MODE>
@@ -413,7 +446,6 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
     rb.de = dsum * e;
     rb.t_s = t_lane + C::kS + w * kBN;
     rb.t_dp = t_lane + C::kDP + w * kBN;
-    rb.diag = reinterpret_cast<float*>(smem + C::kDiag) + warp * kBN;
     int* wdocs = reinterpret_cast<int*>(smem + C::kDocs) + warp * kBN;
     float far_right = 0.f, far_left = 0.f;                 // sums of dT past the table's reach
     const bool biased = s.table || s.slopes;
@@ -424,6 +456,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
       const uint32_t ph = (it / C::NB) & 1;
       const bool cut = lo_all > c0 || c0 + kBN > hi_all || r_end >= n;
       const bool by_doc = docs && cls[jb] == 2;
+      rb.whole = r_end < n && c0 + kBN <= n;
       rb.lo = lo - c0;
       rb.hi = hi - c0;
       rb.docs = nullptr;
@@ -449,7 +482,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
       if (MODE == kDKV && !(ok = warp_wait(b_full(st), (it / C::kStages) & 1))) break;   // the columns' lse2 and D
       tc_fence_after();
       const bool mask = cut || by_doc;
-      float sum = 0.f;
+      float sum[3] = {};
       if (near) {
         if (MODE == kDQ && partial) {
           if (cap.on)
@@ -483,17 +516,14 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
       if (lane == 0) mbar_arrive(p_full(w));
       if (MODE == kDQ && partial) {
         if (near) {
-          // diag[k]: the diagonal that left lane 31 at column k; `sum`: the one that is in this lane now.
-          const int first = c0 - (r0 + quad * 32 + 31);    // distance of diag[0]
-          auto bucket_at = [&](int rel) { return (int)bucket_of[max(-s.reach, min(s.reach, rel)) + s.reach]; };
-          add_by_bucket(rb.diag[lane], bucket_at(first + lane), sums, lane);
-          add_by_bucket(rb.diag[lane + 32], bucket_at(first + lane + 32), sums, lane);
-          const float rest = lane == 31 ? 0.f : sum;       // lane 31's has just been added
-          add_by_bucket(rest, bucket_at(c0 + kBN - 1 - (r0 + quad * 32 + lane)), sums, lane);
+          const int rel = c0 - (r0 + quad * 32);           // of the block's first column to the warp's first row
+          auto bucket_at = [&](int x) { return (int)bucket_of[max(-s.reach, min(s.reach, x)) + s.reach]; };
+#pragma unroll
+          for (int k = 0; k < 3; ++k) add_by_bucket(sum[k], bucket_at(rel + lane + 32 * (k - 1)), sums, lane);
         } else if (ahead) {
-          far_right += sum;
+          far_right += sum[1];
         } else {
-          far_left += sum;
+          far_left += sum[1];
         }
       }
     }

@@ -98,24 +98,14 @@ struct BwdChunk {
   float e;                  // dU's scale
   uint8_t* du;              // the row of dU^T (64 queries), and the swizzle and 16-byte unit of the chunk
   int swizzle, unit;
+  bool whole;               // no row or column of the chunk is past n
 };
 
-// (Two predicated additions; a choice of addends costs two more instructions a score.)
-__device__ __forceinline__ void add_either(bool first, float v, float& a, float& b) {
-  asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t@p add.f32 %0, %0, %3;\n\t@!p add.f32 %1, %1, %3;\n\t}"
-      : "+f"(a), "+f"(b)
-      : "r"((int)first), "f"(v));
-}
-
 // DIAG: adds dT to the lane's two diagonals of the 32 x 32 block (k0: the chunk's first column in it).
-template <bool CAP, bool BIAS, bool DIAG, bool MASK>
-__device__ __forceinline__ void bwd_chunk(const BwdChunk& ch, const Cap& cap, float scale2, int lane, int k0, float& pos,
-                                          float& neg) {
-  uint32_t sv[16], dp[16];
-  tmem_ld_32x32b_x16_async(ch.t_s, sv);
-  tmem_ld_32x32b_x16_async(ch.t_dp, dp);
-  tmem_wait_ld16(sv);
-  tmem_wait_ld16(dp);
+// POLY: the cap's polynomial.
+template <bool CAP, bool BIAS, bool DIAG, bool MASK, bool POLY>
+__device__ __forceinline__ void bwd_scores(const BwdChunk& ch, const Cap& cap, float scale2, int lane, int k0,
+                                           const uint32_t (&sv)[16], const uint32_t (&dp)[16], float& pos, float& neg) {
   uint32_t pp[8], pu[8];
 #pragma unroll
   for (int k = 0; k < 16; k += 4) {
@@ -125,21 +115,27 @@ __device__ __forceinline__ void bwd_chunk(const BwdChunk& ch, const Cap& cap, fl
     int4 dj = make_int4(0, 0, 0, 0);
     if (MASK && ch.docs) dj = *reinterpret_cast<const int4*>(ch.docs + k);
     const int djs[4] = {dj.x, dj.y, dj.z, dj.w};
+    float th[4] = {};
+    if constexpr (CAP) {
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        const float s0 = __uint_as_float(sv[k + q]), s1 = __uint_as_float(sv[k + q + 1]);
+        if (POLY) {
+          const uint64_t y = f2_mul(f2_pack(s0, s1), f2_pack(cap.in, cap.in));
+          f2_unpack(f2_mul(y, tanh_over_x2(f2_mul(y, y))), th[q], th[q + 1]);
+        } else {
+          th[q] = tanh_of(s0, 2.f * kLog2e * cap.in);
+          th[q + 1] = tanh_of(s1, 2.f * kLog2e * cap.in);
+        }
+      }
+    }
     float p[4], u[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float s = __uint_as_float(sv[k + q]);
       const float add = BIAS ? ch.lut[-(k + q)] - nl[q] : -nl[q];
-      float t, th = 0.f;
-      if (CAP) {
-        th = tanh_of(s, 2.f * kLog2e * cap.in);
-        t = fmaf(cap.cap2, th, add);
-      } else {
-        t = fmaf(s, scale2, add);
-      }
-      p[q] = ex2(t);
+      p[q] = ex2(CAP ? fmaf(cap.cap2, th[q], add) : fmaf(__uint_as_float(sv[k + q]), scale2, add));
       float dt = p[q] * ((__uint_as_float(dp[k + q]) - dc[q]) * ch.e);
-      u[q] = CAP ? dt * fmaf(-th, th, 1.f) : dt;
+      u[q] = CAP ? dt * fmaf(-th[q], th[q], 1.f) : dt;
       if (MASK) {                                          // (hidden scores may be NaN)
         const bool see = k + q >= ch.lo && k + q < ch.hi && (!ch.docs || djs[q] == ch.doc);
         p[q] = see ? p[q] : 0.f;
@@ -159,6 +155,28 @@ __device__ __forceinline__ void bwd_chunk(const BwdChunk& ch, const Cap& cap, fl
   tmem_st_32x32b_x8_async(ch.t_p, pp);                     // over columns that this lane has read
   *reinterpret_cast<uint4*>(ch.du + 16 * (ch.unit ^ ch.swizzle)) = make_uint4(pu[0], pu[1], pu[2], pu[3]);
   *reinterpret_cast<uint4*>(ch.du + 16 * ((ch.unit + 1) ^ ch.swizzle)) = make_uint4(pu[4], pu[5], pu[6], pu[7]);
+}
+
+template <bool CAP, bool BIAS, bool DIAG, bool MASK>
+__device__ __forceinline__ void bwd_chunk(const BwdChunk& ch, const Cap& cap, float scale2, int lane, int k0, float& pos,
+                                          float& neg) {
+  uint32_t sv[16], dp[16];
+  tmem_ld_32x32b_x16_async(ch.t_s, sv);
+  tmem_ld_32x32b_x16_async(ch.t_dp, dp);
+  tmem_wait_ld16(sv);
+  tmem_wait_ld16(dp);
+  bool poly = false;
+  if constexpr (CAP) {
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; k += 2)
+      top = fmaxf(fmaxf(top, fabsf(__uint_as_float(sv[k]))), fabsf(__uint_as_float(sv[k + 1])));
+    poly = ch.whole && !any_warp(top * fabsf(cap.in) > kCapPoly);
+  }
+  if (CAP && poly)
+    bwd_scores<CAP, BIAS, DIAG, MASK, CAP>(ch, cap, scale2, lane, k0, sv, dp, pos, neg);
+  else
+    bwd_scores<CAP, BIAS, DIAG, MASK, false>(ch, cap, scale2, lane, k0, sv, dp, pos, neg);
 }
 
 template <int D, bool CAP, bool BIAS, bool DIAG>
@@ -429,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
           ch.docs = s.docs ? pos_docs + i : nullptr;
           ch.du = smem + C::kDU + g * 16384 + r * 128;
           ch.unit = 4 * w + c / 8;
+          ch.whole = w1 < n && i + 16 <= n;
           if (none) {
             const uint32_t zero[8] = {};
             tmem_st_32x32b_x8_async(ch.t_p, zero);
