@@ -155,11 +155,23 @@ def _check(status: int):
         raise EncError(status, load_library().enc_last_error().decode())
 
 
+_raw_stream = None
+
+
 def _current_stream(stream=None) -> Optional[int]:
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return getattr(stream, "cuda_stream", stream)
+    """CUDA stream handle of `stream`, or of PyTorch's current stream on the current device."""
+    if stream is not None:
+        return getattr(stream, "cuda_stream", stream)
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        # The handle without a Stream object around it, which takes longer to make than a kernel to launch.
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            _raw_stream = lambda: raw(torch.cuda.current_device())  # noqa: E731
+    return _raw_stream()
 
 
 def _dptr(t, dtype_np=None) -> int:
