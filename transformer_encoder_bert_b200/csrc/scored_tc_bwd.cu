@@ -13,11 +13,12 @@
 // atomics from the dKV mode: 7 products instead of 5, but no FP32 traffic of dQ
 // through memory and the same result on every run.
 //
-// Warps: NB warpgroups of threads that own rows, taking the blocks in turn
-// (each with its own S and dP columns in TMEM), one MMA warp, one TMA warp.
-// Heads up to 64 run one warpgroup and two CTAs per SM (256 TMEM columns), so
-// that one CTA's exponentials run under the other's products; heads of 128
-// fill the TMEM with one CTA, which has two warpgroups instead.
+// Warps: two warpgroups of threads that own rows, one MMA warp, one TMA warp.
+// Heads up to 64 run two CTAs per SM (256 TMEM columns each), so that one CTA's
+// exponentials run under the other's products, and the warpgroups share a
+// block's columns: its scores are the chain that the products wait for, and half
+// the columns to a thread shorten it.  Heads of 128 fill the TMEM with one CTA:
+// its warpgroups take the blocks in turn, each with S and dP columns of its own.
 //
 // P and dU are rounded to FP16 for the products.  P is at most 1.  dU is scaled
 // by a power of two e per (sequence, head): |dT| <= 2 max|dO_i| max|v_j|, and e
@@ -41,9 +42,10 @@ constexpr int kDQ = 0, kDKV = 1;
 
 template <int D, int MODE>
 struct BCfg {
-  static constexpr int NB = D > 64 ? 2 : 1;
-  static constexpr int kRowThreads = NB * 128;
-  static constexpr int kThreads = kRowThreads + 64;
+  static constexpr int NB = D > 64 ? 2 : 1;                // S and dP buffers
+  static constexpr int kShare = 2 / NB;                    // warpgroups that share a block
+  static constexpr int kRowWarps = 8, kRowThreads = 256, kThreads = kRowThreads + 64;
+  static constexpr int kChunk = D > 64 ? 32 : 16;          // columns in registers at a time (168 or 96 registers)
   static constexpr int kSub = D > 64 ? D / 64 : 1;
   static constexpr int kABytes = kSub * 128 * 128;         // one operand of the rows
   static constexpr int kBSub = kBN * 128;
@@ -51,15 +53,15 @@ struct BCfg {
   static constexpr int kStages = 3;
   static constexpr int kStage = 2 * kBBytes;
   static constexpr int kB = 2 * kABytes;
-  static constexpr int kCol = kB + kStages * kStage;       // dKV: lse2 and D of a block's queries, per stage
+  static constexpr int kCol = kB + kStages * kStage;       // dKV: -lse2 and D of a block's queries, per stage
   static constexpr int kColBytes = 2 * kBN * 4;
   static constexpr int kBars = kCol + (MODE == kDKV ? kStages * kColBytes : 0);
   // a_full, drain, b_full, b_empty (kStages each), s_full, p_full, done (NB each)
   static constexpr int kNumBars = 2 + 2 * kStages + 3 * NB;
   static constexpr int kSlot = kBars + kNumBars * 8;
   static constexpr int kDocs = (kSlot + 16 + 15) / 16 * 16;   // per row warp: the block's documents
-  static constexpr int kSums = kDocs + NB * 4 * kBN * 4;      // dQ: per row warp, bucket sums
-  static constexpr int kColumn = kSums + (MODE == kDQ ? NB * 4 * kMaxScoreBuckets * 4 : 0);   // of the bias table
+  static constexpr int kSums = kDocs + kRowWarps * kBN * 4;   // dQ: per row warp, bucket sums
+  static constexpr int kColumn = kSums + (MODE == kDQ ? kRowWarps * kMaxScoreBuckets * 4 : 0);   // of the bias table
   static constexpr int kLut = kColumn + kMaxScoreBuckets * 4;
   static constexpr int kS = 0, kDP = NB * kBN, kAcc = 2 * NB * kBN;
   static constexpr int kTmemUsed = kAcc + (MODE == kDKV ? 2 : 1) * D;
@@ -73,113 +75,145 @@ struct BCfg {
 // One row's block of 64 columns, 32 at a time: from S and dP to P and dU.
 struct RowBlock {
   uint32_t t_s, t_dp;       // TMEM addresses of the row warp's S and dP columns
-  float base, step;         // bias (less lse2 in dQ mode): base + step * column, or base + lut
+  float base, step;         // bias (less lse2 in dQ mode): base, base + step * column, or base + lut
   const float* lut;         // at column 0
   int lo, hi;               // visible columns, as far as length and causality go
   const int* docs;          // documents of the columns (shared memory), or nullptr
   int doc;
   float e, de;              // dU's scale, and D e (dQ mode)
-  const float* col;         // dKV mode: lse2 [64], D [64] of the columns (shared memory)
+  const float* col;         // dKV mode: -lse2 [64], D [64] of the columns (shared memory)
   bool whole;               // no row or column of the block is past n
+  int p_at;                 // P and dU of column c go to column p_at + c / 2 (of S, of dP)
 };
 
-// 32 columns of it.  NEAR 0: linear bias; 1: bias from the table in shared memory; 2: that, and the diagonals' sums:
-// for column k, lane t takes dT of row (k - t) mod 32, which lies on the diagonal whose column less row is t (pos) or
-// t - 32 (neg).  Else pos += dT.  POLY: the cap's polynomial.
-template <int MODE, bool CAP, int NEAR, bool MASK, bool POLY>
+// CH columns of it from column c, two at a time in packed FP32 arithmetic.  NEAR 0: constant bias; 1: bias from the
+// table in shared memory; 2: that, and the diagonals' sums: for column k, lane t takes dT of row (k - t) mod 32, which
+// lies on the diagonal whose column less row is t (pos) or t - 32 (neg); else pos += dT.  NEAR 3: linear bias.
+// POLY: the cap's polynomial.
+template <int MODE, int CH, bool CAP, int NEAR, bool MASK, bool POLY>
 __device__ __forceinline__ void row_chunk(const RowBlock& rb, const Cap& cap, float scale2, int lane, int c,
-                                          const uint32_t (&sv)[32], const uint32_t (&dp)[32], float& pos, float& neg) {
-  uint32_t pp[MODE == kDKV ? 16 : 1], pu[16];
+                                          const uint32_t (&sv)[CH], const uint32_t (&dp)[CH], float& pos, float& neg) {
+  uint32_t pp[CH / 2], pu[CH / 2];
+  const int k0 = c & 31;                                   // column of a 32 x 32 block
   const float* lut = MODE == kDQ ? rb.lut + c : rb.lut - c;
-  const float base = NEAR ? rb.base : fmaf((float)c, rb.step, rb.base);
+  const float base = NEAR == 3 ? fmaf((float)c, rb.step, rb.base) : rb.base;
+  const uint64_t base2 = f2_pack(base, base), e2 = f2_pack(rb.e, rb.e), neg_e2 = f2_pack(-rb.e, -rb.e);
+  const uint64_t mul = CAP ? f2_pack(cap.cap2, cap.cap2) : f2_pack(scale2, scale2), one2 = f2_pack(1.f, 1.f);
+  const uint64_t row_d2 = f2_pack(-rb.de, -rb.de);
   const int lo = rb.lo - c, hi = rb.hi - c;
+  uint64_t far2 = 0;                                       // two partial sums of dT (0.0f, 0.0f)
 #pragma unroll
-  for (int k = 0; k < 32; k += 4) {
-    float nl[4] = {}, dcol[4];
-    int4 dj = make_int4(0, 0, 0, 0);
+  for (int k = 0; k < CH; k += 4) {
+    ulonglong2 nl = make_ulonglong2(0, 0), dc = make_ulonglong2(0, 0);       // -lse2 and D of four columns
     if (MODE == kDKV) {
-      const float4 a = *reinterpret_cast<const float4*>(rb.col + c + k);
-      const float4 d = *reinterpret_cast<const float4*>(rb.col + kBN + c + k);
-      nl[0] = a.x; nl[1] = a.y; nl[2] = a.z; nl[3] = a.w;
-      dcol[0] = d.x * rb.e; dcol[1] = d.y * rb.e; dcol[2] = d.z * rb.e; dcol[3] = d.w * rb.e;
+      nl = *reinterpret_cast<const ulonglong2*>(rb.col + c + k);
+      dc = *reinterpret_cast<const ulonglong2*>(rb.col + kBN + c + k);
     }
+    int4 dj = make_int4(0, 0, 0, 0);
     if (MASK && rb.docs) dj = *reinterpret_cast<const int4*>(rb.docs + c + k);
     const int djs[4] = {dj.x, dj.y, dj.z, dj.w};
-    float th[4] = {};
-    if constexpr (CAP) {
 #pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        const float s0 = __uint_as_float(sv[k + q]), s1 = __uint_as_float(sv[k + q + 1]);
+    for (int q = 0; q < 4; q += 2) {
+      const int at = k + q;
+      uint64_t x = f2_pack(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), th = 0;
+      if constexpr (CAP) {
         if (POLY) {
-          const uint64_t y = f2_mul(f2_pack(s0, s1), f2_pack(cap.in, cap.in));
-          f2_unpack(f2_mul(y, tanh_over_x2(f2_mul(y, y))), th[q], th[q + 1]);
+          const uint64_t y = f2_mul(x, f2_pack(cap.in, cap.in));
+          th = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
         } else {
-          th[q] = tanh_of(s0, 2.f * kLog2e * cap.in);
-          th[q + 1] = tanh_of(s1, 2.f * kLog2e * cap.in);
+          const float in2 = 2.f * kLog2e * cap.in;
+          th = f2_pack(tanh_of(__uint_as_float(sv[at]), in2), tanh_of(__uint_as_float(sv[at + 1]), in2));
         }
+        x = th;
       }
-    }
-    float p[4], u[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float add = NEAR ? base + (MODE == kDQ ? lut[k + q] : lut[-(k + q)]) : fmaf((float)(k + q), rb.step, base);
-      float t = CAP ? fmaf(cap.cap2, th[q], add) : fmaf(__uint_as_float(sv[k + q]), scale2, add);
-      if (MODE == kDKV) t -= nl[q];
-      p[q] = ex2(t);
-      float dt = p[q] * fmaf(__uint_as_float(dp[k + q]), rb.e, MODE == kDKV ? -dcol[q] : -rb.de);
-      u[q] = CAP ? dt * fmaf(-th[q], th[q], 1.f) : dt;
+      uint64_t add = base2;
+      if (NEAR == 3) add = f2_pack(fmaf((float)at, rb.step, base), fmaf((float)(at + 1), rb.step, base));
+      if (NEAR == 1 || NEAR == 2) {
+        add = MODE == kDQ ? f2_pack(lut[at], lut[at + 1]) : f2_pack(lut[-at], lut[-(at + 1)]);
+        if (MODE == kDQ) add = f2_add(add, base2);
+      }
+      if (MODE == kDKV) add = f2_add(add, q ? nl.y : nl.x);
+      float t0, t1;
+      f2_unpack(f2_fma(x, mul, add), t0, t1);
+      float p0 = ex2(t0), p1 = ex2(t1);
+      const uint64_t d2 = MODE == kDKV ? f2_mul(q ? dc.y : dc.x, neg_e2) : row_d2;
+      const uint64_t dt2 =
+          f2_mul(f2_pack(p0, p1), f2_fma(f2_pack(__uint_as_float(dp[at]), __uint_as_float(dp[at + 1])), e2, d2));
+      uint64_t u2 = dt2;
+      if constexpr (CAP) u2 = f2_mul(dt2, f2_fma(f2_mul(th, f2_pack(-1.f, -1.f)), th, one2));
+      float u0, u1, a0, a1;
+      f2_unpack(u2, u0, u1);
+      f2_unpack(dt2, a0, a1);
       if (MASK) {                                          // (hidden scores may be NaN)
-        const bool see = k + q >= lo && k + q < hi && (!rb.docs || djs[q] == rb.doc);
-        p[q] = see ? p[q] : 0.f;
-        dt = see ? dt : 0.f;
-        u[q] = see ? u[q] : 0.f;
+        const bool see0 = at >= lo && at < hi && (!rb.docs || djs[q] == rb.doc);
+        const bool see1 = at + 1 >= lo && at + 1 < hi && (!rb.docs || djs[q + 1] == rb.doc);
+        p0 = see0 ? p0 : 0.f;
+        p1 = see1 ? p1 : 0.f;
+        a0 = see0 ? a0 : 0.f;
+        a1 = see1 ? a1 : 0.f;
+        u0 = see0 ? u0 : 0.f;
+        u1 = see1 ? u1 : 0.f;
       }
       if (MODE == kDQ) {
-        if (NEAR == 2)
-          add_either(k + q >= lane, __shfl_sync(0xffffffffu, dt, k + q - lane), pos, neg);
-        else
-          pos += dt;
+        if (NEAR == 2) {
+          add_either(k0 + at >= lane, __shfl_sync(0xffffffffu, a0, k0 + at - lane), pos, neg);
+          add_either(k0 + at + 1 >= lane, __shfl_sync(0xffffffffu, a1, k0 + at + 1 - lane), pos, neg);
+        } else {
+          far2 = f2_add(far2, f2_pack(a0, a1));
+        }
       }
+      if (MODE == kDKV) pp[at / 2] = half2_of(p0, p1);
+      pu[at / 2] = half2_of(u0, u1);
     }
-    if (MODE == kDKV) {
-      pp[k / 2] = half2_of(p[0], p[1]);
-      pp[k / 2 + 1] = half2_of(p[2], p[3]);
-    }
-    pu[k / 2] = half2_of(u[0], u[1]);
-    pu[k / 2 + 1] = half2_of(u[2], u[3]);
+  }
+  if (MODE == kDQ && NEAR != 2) {
+    float a0, a1;
+    f2_unpack(far2, a0, a1);
+    pos += a0 + a1;
   }
   // Over columns that this lane has read.
-  if constexpr (MODE == kDKV) tmem_st_32x32b_x16_async(rb.t_s + c / 2, pp);
-  tmem_st_32x32b_x16_async(rb.t_dp + c / 2, pu);
+  if constexpr (CH == 32) {
+    if constexpr (MODE == kDKV) tmem_st_32x32b_x16_async(rb.t_s + rb.p_at + c / 2, pp);
+    tmem_st_32x32b_x16_async(rb.t_dp + rb.p_at + c / 2, pu);
+  } else {
+    if constexpr (MODE == kDKV) tmem_st_32x32b_x8_async(rb.t_s + rb.p_at + c / 2, pp);
+    tmem_st_32x32b_x8_async(rb.t_dp + rb.p_at + c / 2, pu);
+  }
 }
 
-// sums: NEAR 2: the lane's diagonals of the block, 0: columns less rows lane - 32, 1: lane, 2: lane + 32 (from the
-// block's first column and the warp's first row); else sums[1] += dT.
-template <int MODE, bool CAP, int NEAR, bool MASK>
-__device__ __forceinline__ void row_block(const RowBlock& rb, const Cap& cap, float scale2, int lane, float (&sums)[3]) {
+// Columns [first, last).  sums: NEAR 2: the lane's diagonals, k: columns less rows lane + 32 (k - 1), from the first
+// column and the warp's first row; else sums[1] += dT.
+template <int MODE, int CH, bool CAP, int NEAR, bool MASK>
+__device__ __forceinline__ void row_block(const RowBlock& rb, int first, int last, const Cap& cap, float scale2, int lane,
+                                          float (&sums)[3]) {
   float pos = 0.f, neg = 0.f;
 #pragma unroll 1
-  for (int c = 0; c < kBN; c += 32) {
-    uint32_t sv[32], dp[32];
-    tmem_ld_32x32b_x32_async(rb.t_s + c, sv);
-    tmem_ld_32x32b_x32_async(rb.t_dp + c, dp);
+  for (int c = first; c < last; c += CH) {
+    uint32_t sv[CH], dp[CH];
+    if constexpr (CH == 32) {
+      tmem_ld_32x32b_x32_async(rb.t_s + c, sv);
+      tmem_ld_32x32b_x32_async(rb.t_dp + c, dp);
+    } else {
+      tmem_ld_32x32b_x16_async(rb.t_s + c, sv);
+      tmem_ld_32x32b_x16_async(rb.t_dp + c, dp);
+    }
     tmem_wait_ld(sv);
     tmem_wait_ld(dp);
     bool poly = false;
     if constexpr (CAP) {
       float top = 0.f;
 #pragma unroll
-      for (int k = 0; k < 32; k += 2)
+      for (int k = 0; k < CH; k += 2)
         top = fmaxf(fmaxf(top, fabsf(__uint_as_float(sv[k]))), fabsf(__uint_as_float(sv[k + 1])));
       poly = rb.whole && !any_warp(top * fabsf(cap.in) > kCapPoly);
     }
     if (CAP && poly)
-      row_chunk<MODE, CAP, NEAR, MASK, CAP>(rb, cap, scale2, lane, c, sv, dp, pos, neg);
+      row_chunk<MODE, CH, CAP, NEAR, MASK, CAP>(rb, cap, scale2, lane, c, sv, dp, pos, neg);
     else
-      row_chunk<MODE, CAP, NEAR, MASK, false>(rb, cap, scale2, lane, c, sv, dp, pos, neg);
-    if (NEAR == 2 && c == 0) {
+      row_chunk<MODE, CH, CAP, NEAR, MASK, false>(rb, cap, scale2, lane, c, sv, dp, pos, neg);
+    if (NEAR == 2 && c + CH == first + 32) {
       sums[0] = neg;
-      neg = pos;                                           // the first half's lane is the second's lane - 32
+      neg = pos;                                           // the first 32 columns' lane is the next ones' lane - 32
       pos = 0.f;
     }
   }
@@ -191,13 +225,13 @@ __device__ __forceinline__ void row_block(const RowBlock& rb, const Cap& cap, fl
   }
 }
 
-template <int MODE, bool CAP, int NEAR>
-__device__ __forceinline__ void row_block_m(bool mask, const RowBlock& rb, const Cap& cap, float scale2, int lane,
-                                            float (&sums)[3]) {
+template <int MODE, int CH, bool CAP, int NEAR>
+__device__ __forceinline__ void row_block_m(bool mask, const RowBlock& rb, int first, int last, const Cap& cap,
+                                            float scale2, int lane, float (&sums)[3]) {
   if (mask)
-    row_block<MODE, CAP, NEAR, true>(rb, cap, scale2, lane, sums);
+    row_block<MODE, CH, CAP, NEAR, true>(rb, first, last, cap, scale2, lane, sums);
   else
-    row_block<MODE, CAP, NEAR, false>(rb, cap, scale2, lane, sums);
+    row_block<MODE, CH, CAP, NEAR, false>(rb, first, last, cap, scale2, lane, sums);
 }
 
 template <int D, int MODE>
@@ -251,10 +285,10 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
 
   if (tid == 0) {
     for (int k = 0; k < C::kNumBars; ++k) mbar_init(bar0 + 8 * k, 1);
-    for (int w = 0; w < C::NB; ++w) mbar_init(p_full(w), 4);
+    for (int w = 0; w < C::NB; ++w) mbar_init(p_full(w), 4 * C::kShare);
     fence_barrier_init();
   }
-  if (warp == C::NB * 4) {
+  if (warp == C::kRowWarps) {
     tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     tmem_relinquish();
   }
@@ -296,7 +330,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
   };
 
   bool ok = true;
-  if (warp == C::NB * 4 + 1) {
+  if (warp == C::kRowWarps + 1) {
     if (lane == 0) {                                       // TMA
       const int a0 = MODE == kDQ ? (int)bh : planes + (int)bh;               // plane of Q or K
       const int b0 = MODE == kDQ ? planes + (int)bh : (int)bh;               // plane of K or Q
@@ -330,11 +364,12 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
       for (int k = it > C::kStages ? it - C::kStages : 0; k < it; ++k)
         one_wait(b_full(k % C::kStages), (k / C::kStages) & 1);
     }
-  } else if (warp == C::NB * 4) {                          // MMA
+  } else if (warp == C::kRowWarps) {                       // MMA
     constexpr uint32_t idesc_s = idesc_f16_f32(128, kBN);
     constexpr uint32_t idesc_o = idesc_bmn(128, D);
     const uint64_t a_desc = smem_desc_sw128(sbase), b_desc = smem_desc_sw128(sbase + C::kB);
     const uint64_t bt_desc = desc_mn_sw128(sbase + C::kB, C::kBSub);           // the columns' operands, transposed
+    auto p_of = [](int kk) { return 8 * kk + (C::kShare == 2 ? 16 * (kk >> 1) : 0); };   // columns of 16 of P or dU
     auto issue_scores = [&](int w, int st) {               // S and dP of the block in stage st, for warpgroup w
       tc_fence_after();
       if (elect_one()) {
@@ -369,13 +404,13 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
           if (16 * kk < columns)
-            mma_f16_ts(tmem + C::kAcc, tmem + C::kDP + w * kBN + 8 * kk, desc_at(bt, kk * 2048), idesc_o,
+            mma_f16_ts(tmem + C::kAcc, tmem + C::kDP + w * kBN + p_of(kk), desc_at(bt, kk * 2048), idesc_o,
                        it > 0 || kk > 0 ? 1u : 0u);
         if (MODE == kDKV) {
 #pragma unroll
           for (int kk = 0; kk < kBN / 16; ++kk)
             if (16 * kk < columns)
-              mma_f16_ts(tmem + C::kAcc + D, tmem + C::kS + w * kBN + 8 * kk, desc_at(bt, C::kBBytes + kk * 2048),
+              mma_f16_ts(tmem + C::kAcc + D, tmem + C::kS + w * kBN + p_of(kk), desc_at(bt, C::kBBytes + kk * 2048),
                          idesc_o, it > 0 || kk > 0 ? 1u : 0u);
         }
         mma_commit(done(w));
@@ -429,9 +464,9 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
     const Cap cap = make_cap(s);
     const float scale2 = s.scale * kLog2e;
     const bool mine = pos < n;
-    float lse2 = 0.f, dsum = 0.f;
-    if (MODE == kDQ) {                                     // (+inf where the row sees nothing)
-      lse2 = rows2[bh * Sp + pos];
+    float neg_lse2 = 0.f, dsum = 0.f;
+    if (MODE == kDQ) {                                     // (-inf where the row sees nothing)
+      neg_lse2 = rows2[bh * Sp + pos];
       dsum = rows2[((size_t)planes + bh) * Sp + pos];
     }
     const int r_end = r0 + 127;
@@ -444,14 +479,16 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
     rb.doc = docs && mine ? docs[pos] : 0;
     rb.e = e;
     rb.de = dsum * e;
-    rb.t_s = t_lane + C::kS + w * kBN;
-    rb.t_dp = t_lane + C::kDP + w * kBN;
+    const int buf = C::NB == 2 ? w : 0, first = C::kShare == 2 ? 32 * w : 0, last = C::kShare == 2 ? first + 32 : kBN;
+    rb.t_s = t_lane + C::kS + buf * kBN;
+    rb.t_dp = t_lane + C::kDP + buf * kBN;
+    rb.p_at = C::kShare == 2 ? 16 * w : 0;                 // within the columns that the warpgroup reads itself
     int* wdocs = reinterpret_cast<int*>(smem + C::kDocs) + warp * kBN;
     float far_right = 0.f, far_left = 0.f;                 // sums of dT past the table's reach
     const bool biased = s.table || s.slopes;
     int it = 0;
     for (int jb = next_block(jb0); jb < jb1; jb = next_block(jb + 1), ++it) {
-      if (it % C::NB != w) continue;
+      if (it % C::NB != buf) continue;
       const int c0 = jb * kBN, st = it % C::kStages;
       const uint32_t ph = (it / C::NB) & 1;
       const bool cut = lo_all > c0 || c0 + kBN > hi_all || r_end >= n;
@@ -475,10 +512,10 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
       const bool near = biased && !ahead && rel_max > -bias.reach;
       const float sl = ahead ? -bias.slope2 : bias.slope2;
       rb.step = MODE == kDQ ? sl : -sl;
-      rb.base = near ? -lse2 : (biased ? (ahead ? bias.right : bias.left) + sl * (float)rel0 : 0.f) - lse2;
+      rb.base = near ? neg_lse2 : (biased ? (ahead ? bias.right : bias.left) + sl * (float)rel0 : 0.f) + neg_lse2;
       rb.lut = bias.lut + bias.off + rel0;
       rb.col = reinterpret_cast<const float*>(smem + C::kCol + st * C::kColBytes);
-      if (!(ok = warp_wait(s_full(w), ph))) break;
+      if (!(ok = warp_wait(s_full(buf), ph))) break;
       if (MODE == kDKV && !(ok = warp_wait(b_full(st), (it / C::kStages) & 1))) break;   // the columns' lse2 and D
       tc_fence_after();
       const bool mask = cut || by_doc;
@@ -486,22 +523,27 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
       if (near) {
         if (MODE == kDQ && partial) {
           if (cap.on)
-            row_block_m<MODE, true, MODE == kDQ ? 2 : 1>(mask, rb, cap, scale2, lane, sum);
+            row_block_m<MODE, C::kChunk, true, MODE == kDQ ? 2 : 1>(mask, rb, first, last, cap, scale2, lane, sum);
           else
-            row_block_m<MODE, false, MODE == kDQ ? 2 : 1>(mask, rb, cap, scale2, lane, sum);
+            row_block_m<MODE, C::kChunk, false, MODE == kDQ ? 2 : 1>(mask, rb, first, last, cap, scale2, lane, sum);
         } else if (cap.on) {
-          row_block_m<MODE, true, 1>(mask, rb, cap, scale2, lane, sum);
+          row_block_m<MODE, C::kChunk, true, 1>(mask, rb, first, last, cap, scale2, lane, sum);
         } else {
-          row_block_m<MODE, false, 1>(mask, rb, cap, scale2, lane, sum);
+          row_block_m<MODE, C::kChunk, false, 1>(mask, rb, first, last, cap, scale2, lane, sum);
         }
+      } else if (s.slopes) {
+        if (cap.on)
+          row_block_m<MODE, C::kChunk, true, 3>(mask, rb, first, last, cap, scale2, lane, sum);
+        else
+          row_block_m<MODE, C::kChunk, false, 3>(mask, rb, first, last, cap, scale2, lane, sum);
       } else if (cap.on) {
-        row_block_m<MODE, true, 0>(mask, rb, cap, scale2, lane, sum);
+        row_block_m<MODE, C::kChunk, true, 0>(mask, rb, first, last, cap, scale2, lane, sum);
       } else {
-        row_block_m<MODE, false, 0>(mask, rb, cap, scale2, lane, sum);
+        row_block_m<MODE, C::kChunk, false, 0>(mask, rb, first, last, cap, scale2, lane, sum);
       }
       // Rows of the columns' operands in [n, n rounded up to 16) are read by the products: zeros.
       const int lim = n - c0, lim16 = (min(kBN, lim) + 15) & ~15;
-      if (lim < lim16 && quad == 0) {
+      if (lim < lim16 && quad == 0 && (C::kShare == 1 || w == 0)) {
         const int units = (lim16 - lim) * 8;
         for (int k = lane; k < units * C::kSub * (MODE == kDKV ? 2 : 1); k += 32) {
           const int plane = k / units, rr = lim + k % units / 8;             // sub-tiles of B0, then of B1
@@ -513,13 +555,13 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(w));
+      if (lane == 0) mbar_arrive(p_full(buf));
       if (MODE == kDQ && partial) {
         if (near) {
-          const int rel = c0 - (r0 + quad * 32);           // of the block's first column to the warp's first row
+          const int rel = c0 + first - (r0 + quad * 32);   // of the first column to the warp's first row
           auto bucket_at = [&](int x) { return (int)bucket_of[max(-s.reach, min(s.reach, x)) + s.reach]; };
 #pragma unroll
-          for (int k = 0; k < 3; ++k) add_by_bucket(sum[k], bucket_at(rel + lane + 32 * (k - 1)), sums, lane);
+          for (int k = 0; k < (C::kShare == 2 ? 2 : 3); ++k) add_by_bucket(sum[k], bucket_at(rel + lane + 32 * (k - 1)), sums, lane);
         } else if (ahead) {
           far_right += sum[1];
         } else {
@@ -542,7 +584,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
       for (int k = tid; k < s.buckets; k += C::kRowThreads) {
         float total = 0.f;
 #pragma unroll
-        for (int v = 0; v < C::NB * 4; ++v) total += all[v * kMaxScoreBuckets + k];
+        for (int v = 0; v < C::kRowWarps; ++v) total += all[v * kMaxScoreBuckets + k];
         partial[(bh * gridDim.x + blk) * s.buckets + k] = total * inv_e;
       }
     }
@@ -556,7 +598,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
       constexpr int kCols = D < 64 ? D : 64, kRowBytes = 2 * kCols;
       constexpr int kParts = (MODE == kDKV ? 2 : 1) * C::kSub;               // pieces of up to 64 columns
 #pragma unroll 1
-      for (int part = w; part < kParts; part += C::NB) {
+      for (int part = w; part < kParts; part += 2) {
         const int acc = part / C::kSub, u = part % C::kSub;                  // acc 0: dQ or dK; 1: dV
         const float f = !mine ? 0.f : acc == 0 ? s.scale * inv_e : 1.f;
         uint8_t* tile = smem + part * 16384 + quad * 32 * kRowBytes;
@@ -591,13 +633,13 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
   if (!ok) atomicCAS(status, 0, kStatusWaitTimeout);
   tc_fence_before();
   __syncthreads();
-  if (warp == C::NB * 4) {
+  if (warp == C::kRowWarps) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
-// Per row i: lse in units of log2 (+inf where the row sees nothing or is past
+// Per row i: -lse in units of log2 (-inf where the row sees nothing or is past
 // n, which makes P zero) and D_i, in rows padded to Sp; per 128 rows, the
 // largest |dO_i|^2 and |v_j|^2.  D / 8 lanes read a row with 16-byte loads.
 constexpr int kStatThreads = 256;
@@ -651,8 +693,8 @@ __global__ void __launch_bounds__(kStatThreads)
     mo = fmaxf(mo, oo);
     mv = fmaxf(mv, vv);
     if (gl == 0) {
-      const float l = i < n ? lse[bh * S + i] * kLog2e : INFINITY;
-      rows2[bh * Sp + i] = l == -INFINITY ? INFINITY : l;
+      const float l = i < n ? lse[bh * S + i] * kLog2e : -INFINITY;
+      rows2[bh * Sp + i] = l == -INFINITY ? -INFINITY : -l;
       rows2[(planes + bh) * Sp + i] = dot;
     }
   }

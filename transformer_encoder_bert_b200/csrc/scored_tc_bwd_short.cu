@@ -51,7 +51,7 @@ struct SBCfg {
   // full, s_full, p_full, acc_full, free, group, drain
   static constexpr int kSlot = kBars + 64;
   static constexpr int kMax = kSlot + 16;                  // per row warp: norms of dO and V
-  static constexpr int kCol = kMax + 2 * kRowWarps * 4;    // lse2 [128], D [128]
+  static constexpr int kCol = kMax + 2 * kRowWarps * 4;    // -lse2 [128], D [128]
   static constexpr int kDocs = kCol + 256 * 4;
   static constexpr int kColumn = kDocs + 128 * 4;          // the head's column of the bias table
   static constexpr int kLut = kColumn + kMaxScoreBuckets * 4;   // bias of distance k - 127
@@ -64,34 +64,11 @@ struct SBCfg {
   static_assert(kCtasPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
-// Load 16 consecutive 32-bit columns without waiting; tmem_wait_ld16 names the registers.
-__device__ __forceinline__ void tmem_ld_32x32b_x16_async(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tmem_st_32x32b_x8_async(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 // 16 queries of a key row: from S^T and dP^T to P^T (TMEM) and dU^T (shared memory).
 struct BwdChunk {
   uint32_t t_s, t_dp, t_p;  // TMEM addresses
   const float* lut;         // the row's bias at the chunk's first query; falls with the query
-  const float* col;         // lse2 [128] and D [128] at the first query
+  const float* col;         // -lse2 [128] and D [128] at the first query
   int lo, hi;               // visible queries, as far as length and causality go
   const int* docs;          // documents of the queries, or nullptr
   int doc;
@@ -107,50 +84,60 @@ template <bool CAP, bool BIAS, bool DIAG, bool MASK, bool POLY>
 __device__ __forceinline__ void bwd_scores(const BwdChunk& ch, const Cap& cap, float scale2, int lane, int k0,
                                            const uint32_t (&sv)[16], const uint32_t (&dp)[16], float& pos, float& neg) {
   uint32_t pp[8], pu[8];
+  const uint64_t e2 = f2_pack(ch.e, ch.e), neg_e2 = f2_pack(-ch.e, -ch.e), one2 = f2_pack(1.f, 1.f);
+  const uint64_t mul = CAP ? f2_pack(cap.cap2, cap.cap2) : f2_pack(scale2, scale2);
 #pragma unroll
   for (int k = 0; k < 16; k += 4) {
-    const float4 l4 = *reinterpret_cast<const float4*>(ch.col + k);
-    const float4 d4 = *reinterpret_cast<const float4*>(ch.col + 128 + k);
-    const float nl[4] = {l4.x, l4.y, l4.z, l4.w}, dc[4] = {d4.x, d4.y, d4.z, d4.w};
+    const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(ch.col + k);
+    const ulonglong2 dc = *reinterpret_cast<const ulonglong2*>(ch.col + 128 + k);
     int4 dj = make_int4(0, 0, 0, 0);
     if (MASK && ch.docs) dj = *reinterpret_cast<const int4*>(ch.docs + k);
     const int djs[4] = {dj.x, dj.y, dj.z, dj.w};
-    float th[4] = {};
-    if constexpr (CAP) {
 #pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        const float s0 = __uint_as_float(sv[k + q]), s1 = __uint_as_float(sv[k + q + 1]);
+    for (int q = 0; q < 4; q += 2) {
+      const int at = k + q;
+      uint64_t x = f2_pack(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), th = 0;
+      if constexpr (CAP) {
         if (POLY) {
-          const uint64_t y = f2_mul(f2_pack(s0, s1), f2_pack(cap.in, cap.in));
-          f2_unpack(f2_mul(y, tanh_over_x2(f2_mul(y, y))), th[q], th[q + 1]);
+          const uint64_t y = f2_mul(x, f2_pack(cap.in, cap.in));
+          th = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
         } else {
-          th[q] = tanh_of(s0, 2.f * kLog2e * cap.in);
-          th[q + 1] = tanh_of(s1, 2.f * kLog2e * cap.in);
+          const float in2 = 2.f * kLog2e * cap.in;
+          th = f2_pack(tanh_of(__uint_as_float(sv[at]), in2), tanh_of(__uint_as_float(sv[at + 1]), in2));
         }
+        x = th;
       }
-    }
-    float p[4], u[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float add = BIAS ? ch.lut[-(k + q)] - nl[q] : -nl[q];
-      p[q] = ex2(CAP ? fmaf(cap.cap2, th[q], add) : fmaf(__uint_as_float(sv[k + q]), scale2, add));
-      float dt = p[q] * ((__uint_as_float(dp[k + q]) - dc[q]) * ch.e);
-      u[q] = CAP ? dt * fmaf(-th[q], th[q], 1.f) : dt;
+      uint64_t add = q ? nl.y : nl.x;
+      if (BIAS) add = f2_add(add, f2_pack(ch.lut[-at], ch.lut[-(at + 1)]));
+      float t0, t1;
+      f2_unpack(f2_fma(x, mul, add), t0, t1);
+      float p0 = ex2(t0), p1 = ex2(t1);
+      const uint64_t dt2 =
+          f2_mul(f2_pack(p0, p1), f2_fma(f2_pack(__uint_as_float(dp[at]), __uint_as_float(dp[at + 1])), e2,
+                                         f2_mul(q ? dc.y : dc.x, neg_e2)));
+      uint64_t u2 = dt2;
+      if constexpr (CAP) u2 = f2_mul(dt2, f2_fma(f2_mul(th, f2_pack(-1.f, -1.f)), th, one2));
+      float u0, u1, a0, a1;
+      f2_unpack(u2, u0, u1);
+      f2_unpack(dt2, a0, a1);
       if (MASK) {                                          // (hidden scores may be NaN)
-        const bool see = k + q >= ch.lo && k + q < ch.hi && (!ch.docs || djs[q] == ch.doc);
-        p[q] = see ? p[q] : 0.f;
-        dt = see ? dt : 0.f;
-        u[q] = see ? u[q] : 0.f;
+        const bool see0 = at >= ch.lo && at < ch.hi && (!ch.docs || djs[q] == ch.doc);
+        const bool see1 = at + 1 >= ch.lo && at + 1 < ch.hi && (!ch.docs || djs[q + 1] == ch.doc);
+        p0 = see0 ? p0 : 0.f;
+        p1 = see1 ? p1 : 0.f;
+        a0 = see0 ? a0 : 0.f;
+        a1 = see1 ? a1 : 0.f;
+        u0 = see0 ? u0 : 0.f;
+        u1 = see1 ? u1 : 0.f;
       }
       if (DIAG) {
-        const int row = lane + k0 + k + q;                 // (mod 32)
-        add_either(row < 32, __shfl_sync(0xffffffffu, dt, row), pos, neg);
+        const int row = lane + k0 + at;                    // (mod 32)
+        add_either(row < 32, __shfl_sync(0xffffffffu, a0, row), pos, neg);
+        add_either(row + 1 < 32, __shfl_sync(0xffffffffu, a1, row + 1), pos, neg);
       }
+      pp[at / 2] = half2_of(p0, p1);
+      pu[at / 2] = half2_of(u0, u1);
     }
-    pp[k / 2] = half2_of(p[0], p[1]);
-    pp[k / 2 + 1] = half2_of(p[2], p[3]);
-    pu[k / 2] = half2_of(u[0], u[1]);
-    pu[k / 2 + 1] = half2_of(u[2], u[3]);
   }
   tmem_st_32x32b_x8_async(ch.t_p, pp);                     // over columns that this lane has read
   *reinterpret_cast<uint4*>(ch.du + 16 * (ch.unit ^ ch.swizzle)) = make_uint4(pu[0], pu[1], pu[2], pu[3]);
@@ -163,8 +150,8 @@ __device__ __forceinline__ void bwd_chunk(const BwdChunk& ch, const Cap& cap, fl
   uint32_t sv[16], dp[16];
   tmem_ld_32x32b_x16_async(ch.t_s, sv);
   tmem_ld_32x32b_x16_async(ch.t_dp, dp);
-  tmem_wait_ld16(sv);
-  tmem_wait_ld16(dp);
+  tmem_wait_ld(sv);
+  tmem_wait_ld(dp);
   bool poly = false;
   if constexpr (CAP) {
     float top = 0.f;
@@ -365,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
       ++it;
       // Row statistics: two threads to a row.
       {
-        const float l = srow < n ? lse_row * kLog2e : INFINITY;
+        const float l = srow < n ? lse_row * kLog2e : -INFINITY;
         if (s.docs && shalf == 0) pos_docs[srow] = srow < n ? s.docs[(size_t)b * S + srow] : 0;
         if (!(ok = warp_wait(full, ph))) break;
         float dot = 0.f, oo = 0.f, vv = 0.f;
@@ -391,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
         dot += __shfl_xor_sync(0xffffffffu, dot, 1);
         float mo = oo + __shfl_xor_sync(0xffffffffu, oo, 1), mv = vv + __shfl_xor_sync(0xffffffffu, vv, 1);
         if (shalf == 0) {
-          col[srow] = l == -INFINITY ? INFINITY : l;
+          col[srow] = l == -INFINITY ? -INFINITY : -l;
           col[128 + srow] = dot;
         }
 #pragma unroll
