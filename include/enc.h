@@ -454,7 +454,7 @@ ENC_API enc_status enc_op_ffn2_ln(enc_t h, int layer, const void* u, const void*
  * ---------------------------------------------------------------------------- */
 typedef struct {
   float scale;                /* of q . k; 0 = 1/sqrt(size_per_head) */
-  float cap;                  /* 0 = none; else > 0 */
+  float cap;                  /* 0 = none; else in [1e-3, 1e4] */
   const float* slopes;        /* device [head_num], or NULL */
   const float* bias_table;    /* device [num_buckets, head_num], FP32 in both modes, or NULL */
   int num_buckets;            /* with a table: 2..128; bidirectional: even, >= 4 */
@@ -492,7 +492,8 @@ ENC_API enc_status enc_reserve_scored(enc_t h, int batch, int seq);
  *   int32 [batch]; ctx [batch * seq, H]; lse device FP32 [batch, head_num, seq]
  *   (natural logarithm), or NULL.  seq <= 65536.  qkv and ctx 16-byte aligned.
  * Accumulation, softmax and lse in FP32; FP16 mode rounds the unnormalised
- * probabilities to FP16 before the product with V, as enc_op_attention does.
+ * probabilities to FP16 before the product with V, as enc_op_attention does, and
+ * its tanh is an approximation that moves a capped score by up to cap 2^-21.
  * Asynchronous. */
 ENC_API enc_status enc_op_scored_attention(enc_t h, const enc_scores* scores, const void* qkv,
                                            const int32_t* valid_len, void* ctx, float* lse, int batch, int seq,

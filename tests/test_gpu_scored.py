@@ -410,6 +410,11 @@ def test_encoder_forward_with_scores(kind, s, mode):
     host = enc.forward_host(inp.x, np.asarray(inp.valid_len, np.int32))
     assert np.array_equal(host[mask], got.cpu().numpy()[mask])
     assert torch.equal(enc.forward_noalloc(x, vl, torch.empty_like(x)), got)
+    if c.spec.doc_ids is not None:                            # sized for another batch: refused, not read past its end
+        bigger = torch.cat([x, x])
+        for call in (lambda: enc.forward(bigger, torch.cat([vl, vl])), lambda: enc.forward(x[:, :-1].contiguous(), vl)):
+            with pytest.raises(ValueError, match="shape"):
+                call()
     out = torch.empty_like(x)
     rec = enc.record(x, vl, out)
     enc.set_scores(None)
@@ -452,6 +457,8 @@ def test_refusals():
     bad("max_distance", Scores(table=t, max_distance=2049))
     bad("cap", Scores(cap=-1.0))
     bad("cap", Scores(cap=float("nan")))
+    bad("cap", Scores(cap=1e-4))
+    bad("cap", Scores(cap=2e4))
     bad("scale", Scores(scale=float("inf")))
     bad("causal", Scores(prefix_len=vl))
     bad("overlaps", ctx=qkv[1].view(32, 128))

@@ -158,3 +158,46 @@ def test_scores_struct_matches_the_header_and_refuses_host_tensors():
         B.Scores(slopes=torch.zeros(4))
     with pytest.raises(TypeError):
         B.Scores(doc_ids=np.zeros((1, 4), np.int32))
+
+
+class _FakeTensor:
+    """What the binding looks at, of a CUDA tensor on another device."""
+
+    def __init__(self, shape, dtype, device):
+        self.shape, self.dtype, self._device = shape, dtype, device
+        self.is_cuda = True
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 1 << 20
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    def get_device(self):
+        return self._device
+
+
+def test_tensors_of_another_device_or_shape_are_refused():
+    ok = _FakeTensor((2, 4), torch.float32, 0)
+    assert B._shaped_ptr(ok, "float32", 8, 0) == 1 << 20
+    with pytest.raises(ValueError, match="cuda:1"):
+        B._shaped_ptr(_FakeTensor((2, 4), torch.float32, 1), "float32", 8, 0)
+    with pytest.raises(ValueError, match="float16"):
+        B._shaped_ptr(ok, "float16", 8, 0)
+    with pytest.raises(ValueError, match="elements"):
+        B._shaped_ptr(ok, "float32", 9, 0)
+    sc = B.Scores(table=_FakeTensor((8, 4), torch.float32, 1), causal=True,
+                  prefix_len=_FakeTensor((3,), torch.int32, 1), doc_ids=_FakeTensor((3, 5), torch.int32, 1))
+    sc.check(4, 1, 3, 5)
+    for args, match in (((4, 0, 3, 5), "device"), ((5, 1, 3, 5), "table"), ((4, 1, 2, 5), "prefix_len"),
+                        ((4, 1, 3, 6), "doc_ids")):
+        with pytest.raises(ValueError, match=match):
+            sc.check(*args)
+    with pytest.raises(ValueError, match="int32"):
+        B.Scores(doc_ids=_FakeTensor((3, 5), torch.int64, 0))

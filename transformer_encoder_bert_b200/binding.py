@@ -98,6 +98,8 @@ class Scores:
                  max_distance: int = 128, bidirectional: bool = True, causal: bool = False, prefix_len=None,
                  doc_ids=None):
         self.slopes, self.table, self.prefix_len, self.doc_ids = slopes, table, prefix_len, doc_ids
+        self.devices = {t.get_device() for t in (slopes, table, prefix_len, doc_ids) if t is not None
+                        and hasattr(t, "get_device")}
         self.c = EncScores(scale=0.0 if scale is None else scale, cap=cap, slopes=_typed_ptr(slopes, "float32", 1),
                            bias_table=_typed_ptr(table, "float32", 2),
                            num_buckets=0 if table is None else table.shape[0],
@@ -105,8 +107,10 @@ class Scores:
                            causal=int(causal), prefix_len=_typed_ptr(prefix_len, "int32", 1),
                            doc_ids=_typed_ptr(doc_ids, "int32", 2))
 
-    def check(self, head_num: int, batch: Optional[int] = None, seq: Optional[int] = None):
-        """Raise ValueError where a tensor does not fit head_num, batch or seq (the C ABI cannot see sizes)."""
+    def check(self, head_num: int, device: int, batch: Optional[int] = None, seq: Optional[int] = None):
+        """Raise ValueError where a tensor does not fit head_num, the device, batch or seq (the C ABI cannot see them)."""
+        if self.devices and self.devices != {device}:
+            raise ValueError(f"scores on devices {sorted(self.devices)}, expected the handle's device {device}")
         if self.slopes is not None and self.slopes.shape[0] != head_num:
             raise ValueError(f"slopes has shape {tuple(self.slopes.shape)}, expected {(head_num,)}")
         if self.table is not None and self.table.shape[1] != head_num:
@@ -193,11 +197,13 @@ def _typed_ptr(t, dtype: str, dim: int) -> Optional[int]:
     return p
 
 
-def _shaped_ptr(t, dtype: str, numel: int) -> int:
-    """Device pointer of a contiguous CUDA tensor of that dtype and element count."""
+def _shaped_ptr(t, dtype: str, numel: int, device: int) -> int:
+    """Device pointer of a contiguous CUDA tensor of that dtype, element count and device."""
     p = _dptr(t)
     if t.dtype is not _torch_dtype(dtype) or t.numel() != numel:
         raise ValueError(f"expected {numel} elements of {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"tensor on cuda:{t.get_device()}, expected the handle's device cuda:{device}")
     return p
 
 
@@ -226,6 +232,7 @@ class Encoder:
         self.num_layers = len(layers)
         self.dtype = dtype
         self.np_dtype = NP_DTYPES[dtype]
+        self._scores_keep: Optional[Scores] = None
         arr = (EncLayerWeights * max(1, len(layers)))()
         keep = []
         for i, lw in enumerate(layers):
@@ -293,6 +300,7 @@ class Encoder:
         """x: CUDA [B, S, H] tensor in the storage dtype; valid_len: CUDA int32 [B]."""
         import torch
         B, S, H = x.shape
+        self._check_scores(B, S)
         if out is None:
             out = torch.empty_like(x)
         _check(self.lib.enc_forward(self.handle, _dptr(x), _dptr(valid_len), _dptr(out), B, S,
@@ -303,6 +311,7 @@ class Encoder:
         """enc_forward_noalloc: the forward with its scratch in the library's fixed
         device array (no device allocation); out must be given."""
         B, S, H = x.shape
+        self._check_scores(B, S)
         _check(self.lib.enc_forward_noalloc(self.handle, _dptr(x), _dptr(valid_len), _dptr(out), B, S,
                                             _current_stream(stream)))
         return out
@@ -315,17 +324,20 @@ class Encoder:
         if out is None:
             out = np.empty_like(x)
         B, S, _ = x.shape
+        self._check_scores(B, S)
         _check(self.lib.enc_forward_host(self.handle, x.ctypes.data, vl.ctypes.data, out.ctypes.data,
                                          B, S, _current_stream(stream)))
         return out
 
     def forward_host_ptr(self, x_ptr: int, vl_ptr: int, out_ptr: int, batch: int, seq: int, stream=None):
         """enc_forward_host on raw host pointers (e.g. pinned torch tensors)."""
+        self._check_scores(batch, seq)
         _check(self.lib.enc_forward_host(self.handle, x_ptr, vl_ptr, out_ptr, batch, seq,
                                          _current_stream(stream)))
 
     def forward_host_async_ptr(self, x_ptr: int, vl_ptr: int, out_ptr: int, batch: int, seq: int, stream=None):
         """enc_forward_host_async on raw (pinned) host pointers; see host_join."""
+        self._check_scores(batch, seq)
         _check(self.lib.enc_forward_host_async(self.handle, x_ptr, vl_ptr, out_ptr, batch, seq,
                                                _current_stream(stream)))
 
@@ -336,10 +348,11 @@ class Encoder:
     def record(self, x, valid_len, out) -> "RecordedForward":
         """Record one forward on these CUDA tensors as a CUDA graph (see enc_graph_create)."""
         B, S, _ = x.shape
+        self._check_scores(B, S)
         g = ctypes.c_void_p()
         _check(self.lib.enc_graph_create(self.handle, _dptr(x), _dptr(valid_len), _dptr(out), B, S,
                                          ctypes.byref(g)))
-        return RecordedForward(self, g, (x, valid_len, out))
+        return RecordedForward(self, g, (x, valid_len, out, self._scores_keep))
 
     def kernels_per_forward(self, batch: int, seq: int) -> int:
         return int(self.lib.enc_kernels_per_forward(self.handle, batch, seq))
@@ -379,6 +392,7 @@ class Encoder:
         _check(self.lib.enc_op_qkv(self.handle, layer, _dptr(x), _dptr(qkv), batch, seq, _current_stream(stream)))
 
     def op_attention(self, qkv, valid_len, ctx, batch: int, seq: int, stream=None):
+        self._check_scores(batch, seq)
         _check(self.lib.enc_op_attention(self.handle, _dptr(qkv), _dptr(valid_len), _dptr(ctx), batch, seq,
                                          _current_stream(stream)))
 
@@ -399,10 +413,20 @@ class Encoder:
     def _act(self) -> str:
         return "float16" if self.dtype == "fp16" else "float32"
 
+    def _check_scores(self, batch: int, seq: int):
+        """The tensors of set_scores against the batch and seq of a forward."""
+        if self._scores_keep is not None:
+            self._scores_keep.check(self.head_num, self._device(), batch, seq)
+
+    def _device(self) -> int:
+        """The current device, which must be the handle's (the library checks that)."""
+        import torch
+        return torch.cuda.current_device()
+
     def set_scores(self, scores: Optional["Scores"]):
         """Run the attention of every later forward (and of op_attention) with these scores; None = plain."""
         if scores is not None:
-            scores.check(self.head_num)
+            scores.check(self.head_num, self._device())
         _check(self.lib.enc_set_scores(self.handle, None if scores is None else scores.pointer))
         self._scores_keep = scores
 
@@ -412,36 +436,39 @@ class Encoder:
 
     def op_scored_attention(self, scores: "Scores", qkv, valid_len, ctx, batch: int, seq: int, lse=None, stream=None):
         """ctx (and lse [batch, head_num, seq], float32) of qkv [3, batch, head_num, seq, d]."""
-        scores.check(self.head_num, batch, seq)
+        dev = self._device()
+        scores.check(self.head_num, dev, batch, seq)
         m = batch * seq * self.hidden
         _check(self.lib.enc_op_scored_attention(
-            self.handle, scores.pointer, _shaped_ptr(qkv, self._act(), 3 * m), _shaped_ptr(valid_len, "int32", batch),
-            _shaped_ptr(ctx, self._act(), m),
-            None if lse is None else _shaped_ptr(lse, "float32", batch * seq * self.head_num), batch, seq,
+            self.handle, scores.pointer, _shaped_ptr(qkv, self._act(), 3 * m, dev), _shaped_ptr(valid_len, "int32", batch, dev),
+            _shaped_ptr(ctx, self._act(), m, dev),
+            None if lse is None else _shaped_ptr(lse, "float32", batch * seq * self.head_num, dev), batch, seq,
             _current_stream(stream)))
 
     def op_scored_attention_backward(self, scores: "Scores", qkv, valid_len, ctx, lse, dctx, dqkv, batch: int, seq: int,
                                      dtable=None, stream=None):
         """dqkv (and dtable [num_buckets, head_num], float32) from the forward's ctx and lse and from dctx."""
-        scores.check(self.head_num, batch, seq)
+        dev = self._device()
+        scores.check(self.head_num, dev, batch, seq)
         m = batch * seq * self.hidden
         _check(self.lib.enc_op_scored_attention_backward(
-            self.handle, scores.pointer, _shaped_ptr(qkv, self._act(), 3 * m), _shaped_ptr(valid_len, "int32", batch),
-            _shaped_ptr(ctx, self._act(), m), _shaped_ptr(lse, "float32", batch * seq * self.head_num),
-            _shaped_ptr(dctx, self._act(), m), _shaped_ptr(dqkv, self._act(), 3 * m),
-            None if dtable is None else _shaped_ptr(dtable, "float32", scores.c.num_buckets * self.head_num), batch, seq,
+            self.handle, scores.pointer, _shaped_ptr(qkv, self._act(), 3 * m, dev), _shaped_ptr(valid_len, "int32", batch, dev),
+            _shaped_ptr(ctx, self._act(), m, dev), _shaped_ptr(lse, "float32", batch * seq * self.head_num, dev),
+            _shaped_ptr(dctx, self._act(), m, dev), _shaped_ptr(dqkv, self._act(), 3 * m, dev),
+            None if dtable is None else _shaped_ptr(dtable, "float32", scores.c.num_buckets * self.head_num, dev), batch, seq,
             _current_stream(stream)))
 
     def op_scored_attention_step(self, scores: "Scores", qkv, cache, length, ctx, batch: int, capacity: int,
                                  stream=None):
         """ctx [batch, hidden] of one new token per sequence; its key and value go into cache
         [2, batch, head_num, capacity, d] at position length[b]."""
-        scores.check(self.head_num, batch, capacity)
+        dev = self._device()
+        scores.check(self.head_num, dev, batch, capacity)
         m = batch * self.hidden
         _check(self.lib.enc_op_scored_attention_step(
-            self.handle, scores.pointer, _shaped_ptr(qkv, self._act(), 3 * m),
-            _shaped_ptr(cache, self._act(), 2 * m * capacity), _shaped_ptr(length, "int32", batch),
-            _shaped_ptr(ctx, self._act(), m), batch, capacity, _current_stream(stream)))
+            self.handle, scores.pointer, _shaped_ptr(qkv, self._act(), 3 * m, dev),
+            _shaped_ptr(cache, self._act(), 2 * m * capacity, dev), _shaped_ptr(length, "int32", batch, dev),
+            _shaped_ptr(ctx, self._act(), m, dev), batch, capacity, _current_stream(stream)))
 
 
 class Decoder:

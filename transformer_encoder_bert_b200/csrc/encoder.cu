@@ -514,7 +514,8 @@ bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
 enc_status make_scores(enc_handle* h, const enc_scores* p, enc::ScoreArgs& s) {
   if (!p) return fail(ENC_ERR_INVALID_ARG, "scores is null");
   if (!std::isfinite(p->scale)) return fail(ENC_ERR_INVALID_ARG, "scale is not finite");
-  if (!std::isfinite(p->cap) || p->cap < 0.f) return fail(ENC_ERR_INVALID_ARG, "cap must be finite and >= 0");
+  if (!std::isfinite(p->cap) || p->cap < 0.f || (p->cap > 0.f && (p->cap < 1e-3f || p->cap > 1e4f)))
+    return fail(ENC_ERR_INVALID_ARG, "cap must be 0 (none) or in [1e-3, 1e4]");
   s.scale = p->scale == 0.f ? 1.f / sqrtf((float)h->d) : p->scale;
   s.cap = p->cap;
   s.slopes = p->slopes;
