@@ -39,15 +39,29 @@ __device__ __forceinline__ float4 load4<__half>(const __half* p) {
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 
-// Rows [row0, row0 + 64) of a [rows, stride] operand into shared memory; rows at or past `rows` are zeros.
+// Rows [row0, row0 + 64) of a [rows, stride] operand into shared memory; rows at or past `rows` are zeros.  FP32
+// copies are asynchronous (one group; wait_copies), so that the next tile loads under this one's arithmetic.
 template <typename T, int D>
 __device__ __forceinline__ void load_tile(float* dst, const T* src, int row0, int rows, size_t stride) {
   for (int i = threadIdx.x; i < kT * (D / 4); i += kThreads) {
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row0 + r < rows) v = load4<T>(src + (size_t)(row0 + r) * stride + c);
-    *reinterpret_cast<float4*>(dst + r * (D + 4) + c) = v;
+    const bool read = row0 + r < rows;
+    if constexpr (sizeof(T) == 4) {
+      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst + r * (D + 4) + c));
+      const T* from = src + (read ? (size_t)(row0 + r) * stride + c : 0);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(read ? 16 : 0) : "memory");
+    } else {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (read) v = load4<T>(src + (size_t)(row0 + r) * stride + c);
+      *reinterpret_cast<float4*>(dst + r * (D + 4) + c) = v;
+    }
   }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the last N tiles asked for by this thread have arrived (a barrier makes the others' visible).
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // acc[a][c] = A[4 ty + a] . B[tx + 16 c]
@@ -153,8 +167,9 @@ __global__ void __launch_bounds__(kThreads)
                       int NH) {
   extern __shared__ __align__(16) float smem[];
   float* Qs = smem;
-  float* Ks = Qs + kT * (D + 4);         // K, then V
-  float* Ps = Ks + kT * (D + 4);
+  float* Ks = Qs + kT * (D + 4);
+  float* Vs = Ks + kT * (D + 4);
+  float* Ps = Vs + kT * (D + 4);
   TileInfo* ti = reinterpret_cast<TileInfo*>(Ps + kT * kPs);
   pdl_wait();
   pdl_trigger();
@@ -173,15 +188,17 @@ __global__ void __launch_bounds__(kThreads)
   fill_docs(ti->row_doc, s, b, S, q0);
   load_column(s, ti->column, NH, h, threadIdx.x, kThreads);
   __syncthreads();
+  load_tile<T, D>(Ks, Qg + part, 0, n, D);
+  load_tile<T, D>(Vs, Qg + 2 * part, 0, n, D);
   for (int j0 = 0; j0 < klim; j0 += kT) {
-    load_tile<T, D>(Ks, Qg + part, j0, n, D);
     fill_bias(ti, s, slope, j0 - q0);
     fill_docs(ti->col_doc, s, b, S, j0);
+    wait_copies<1>();
     __syncthreads();
     float acc[4][4];
     dot_tile<D>(Qs, Ks, acc);
     __syncthreads();
-    load_tile<T, D>(Ks, Qg + 2 * part, j0, n, D);
+    load_tile<T, D>(Ks, Qg + part, j0 + kT, n, D);         // the next tile's, under the softmax
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const int r = 4 * ty + a, i = q0 + r;
@@ -213,10 +230,13 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int e = 0; e < D / 16; ++e) out[a][e] *= alpha;
     }
+    wait_copies<1>();
     __syncthreads();
-    accumulate<D>(Ps, Ks, out);
+    accumulate<D>(Ps, Vs, out);
     __syncthreads();
+    load_tile<T, D>(Vs, Qg + 2 * part, j0 + kT, n, D);
   }
+  wait_copies<0>();
   const int H = NH * D;
 #pragma unroll
   for (int a = 0; a < 4; ++a) {
@@ -277,15 +297,18 @@ __global__ void __launch_bounds__(kThreads)
     if (lse2[a] == -INFINITY) lse2[a] = INFINITY;
     dsum[a] = i < n ? rowsum[bh * S + i] : 0.f;
   }
+  load_tile<T, D>(Ks, Qg + part, 0, n, D);
+  load_tile<T, D>(Vs, Qg + 2 * part, 0, n, D);
   for (int j0 = 0; j0 < klim; j0 += kT) {
-    load_tile<T, D>(Ks, Qg + part, j0, n, D);
-    load_tile<T, D>(Vs, Qg + 2 * part, j0, n, D);
     fill_bias(ti, s, slope, j0 - q0);
     fill_docs(ti->col_doc, s, b, S, j0);
+    wait_copies<0>();
     __syncthreads();
     float acc[4][4], dp[4][4];
     dot_tile<D>(Qs, Ks, acc);
     dot_tile<D>(dOs, Vs, dp);
+    __syncthreads();
+    load_tile<T, D>(Vs, Qg + 2 * part, j0 + kT, n, D);     // the next tile's
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const int r = 4 * ty + a, i = q0 + r;
@@ -326,7 +349,9 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     accumulate<D>(Ps, Ks, out);
     __syncthreads();
+    load_tile<T, D>(Ks, Qg + part, j0 + kT, n, D);
   }
+  wait_copies<0>();
 #pragma unroll
   for (int a = 0; a < 4; ++a) {
     const int i = q0 + 4 * ty + a;
@@ -391,9 +416,10 @@ __global__ void __launch_bounds__(kThreads)
   load_column(s, ti->column, NH, h, threadIdx.x, kThreads);
   __syncthreads();
   const int qfirst = j0 < n ? score_ilow(s, j0, prefix) / kT * kT : n;
+  const T* dOg = dctx + (size_t)b * S * H + h * D;
+  load_tile<T, D>(Qs, Qg, qfirst, n, D);
+  load_tile<T, D>(dOs, dOg, qfirst, n, H);
   for (int q0 = qfirst; q0 < n; q0 += kT) {
-    load_tile<T, D>(Qs, Qg, q0, n, D);
-    load_tile<T, D>(dOs, dctx + (size_t)b * S * H + h * D, q0, n, H);
     fill_bias(ti, s, slope, j0 - q0);
     fill_docs(ti->col_doc, s, b, S, q0);
     if (threadIdx.x < kT) {
@@ -402,6 +428,7 @@ __global__ void __launch_bounds__(kThreads)
       lse2[threadIdx.x] = v == -INFINITY ? INFINITY : v;
       dsum[threadIdx.x] = i < n ? rowsum[bh * S + i] : 0.f;
     }
+    wait_copies<0>();
     __syncthreads();
     float acc[4][4], dp[4][4];
     dot_tile<D>(Ks, Qs, acc);            // rows are keys, columns queries
@@ -424,6 +451,7 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     accumulate<D>(Ps, dOs, dv);
     __syncthreads();
+    load_tile<T, D>(dOs, dOg, q0 + kT, n, H);              // the next tile's
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
@@ -431,7 +459,9 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     accumulate<D>(Ps, Qs, dk);
     __syncthreads();
+    load_tile<T, D>(Qs, Qg, q0 + kT, n, D);
   }
+  wait_copies<0>();
 #pragma unroll
   for (int a = 0; a < 4; ++a) {
     const int j = j0 + 4 * ty + a;
@@ -526,10 +556,10 @@ cudaError_t allow_smem(K kern, size_t bytes) {
 template <typename T, int D>
 cudaError_t fwd_d(const ScoreArgs& s, const void* qkv, const int32_t* vl, void* ctx, float* lse,
                   const ScoredShape& sh, cudaStream_t stream) {
-  static const cudaError_t attr = allow_smem(scored_fwd_kernel<T, D>, smem_bytes<D>(2));
+  static const cudaError_t attr = allow_smem(scored_fwd_kernel<T, D>, smem_bytes<D>(3));
   if (attr != cudaSuccess) return attr;
   const dim3 grid((sh.seq + kT - 1) / kT, sh.head_num, sh.batch);
-  return launch_kernel(scored_fwd_kernel<T, D>, grid, dim3(kThreads), smem_bytes<D>(2), stream, nullptr, 0, s,
+  return launch_kernel(scored_fwd_kernel<T, D>, grid, dim3(kThreads), smem_bytes<D>(3), stream, nullptr, 0, s,
                        static_cast<const T*>(qkv), vl, static_cast<T*>(ctx), lse, sh.batch, sh.seq, sh.head_num);
 }
 
