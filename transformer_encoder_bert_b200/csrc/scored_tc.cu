@@ -18,15 +18,17 @@
 // What bounds a block is the softmax, not the products: 8 cycles of the
 // special-function unit a score and warp, and a chain of waits and dependent
 // steps around them.  So as many tiles share an SM as TMEM holds: three CTAs of
-// one tile for heads up to 64, one CTA of two tiles (which share K and V) or
-// two of one for heads of 128.
+// one tile for heads up to 64, one CTA of two tiles (which share K and V) for
+// heads of 128.
 //
 // Keys hidden by length, causal or prefix masks are a suffix of the row, so a
 // block past every row's limit is not visited and only blocks that a row's limit
 // cuts are masked per element.  With documents the CTA first takes the least and
 // largest id of every block: blocks whose range does not meet the rows' range
 // are not visited, and blocks that hold only the rows' one document are not
-// masked.
+// masked.  In a masked block each row's visible keys are a bit set that its
+// thread has before S arrives; a warp whose rows see none of the block writes
+// P = 0 and leaves it.
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -72,7 +74,7 @@ constexpr int BN = 64;                             // keys of a block
 
 template <int D, int TILES>
 struct Cfg {
-  static constexpr int kCtasPerSm = D > 64 ? 2 / TILES : 3;
+  static constexpr int kCtasPerSm = D > 64 ? 1 : 3;
   static constexpr int kSoftmaxThreads = TILES * 128;
   static constexpr int kMmaWarp = TILES * 4, kTmaWarp = TILES * 5;
   // The MMA and TMA warps are filled up to a warpgroup, whose registers the softmax warps take.
@@ -87,15 +89,14 @@ struct Cfg {
   static constexpr int kQBytes = kSub * 128 * 128;
   static constexpr int kKVSub = BN * 128;
   static constexpr int kKVBytes = kSub * kKVSub;
-  static constexpr int kStages = D > 64 && TILES == 1 ? 2 : 3;      // two CTAs' shared memory
+  static constexpr int kStages = 3;
   static constexpr int kK = TILES * kQBytes;
   static constexpr int kV = kK + kStages * kKVBytes;
   static constexpr int kBars = kV + kStages * kKVBytes;
   // q_full, k_full, k_empty, v_full, v_empty (kStages each), s_full, s_free, p_full, o_done, drain (TILES each)
   static constexpr int kNumBars = 1 + 4 * kStages + 5 * TILES;
   static constexpr int kSlot = kBars + kNumBars * 8;
-  static constexpr int kDocs = (kSlot + 16 + 15) / 16 * 16;            // per softmax warp: the block's documents
-  static constexpr int kColumn = kDocs + TILES * 4 * BN * 4;           // the head's column of the bias table
+  static constexpr int kColumn = (kSlot + 16 + 15) / 16 * 16;          // the head's column of the bias table
   static constexpr int kLut = kColumn + kMaxScoreBuckets * 4;
   // TMEM columns of tile t: S at t * BN, O at kO + t * D, P at kP + t * BN / 2; for heads of 64 P is an allocation
   // of its own, as 128 + 32 columns fit an SM three times where 160 would be rounded up to 256.
@@ -124,59 +125,30 @@ struct SoftmaxBlock {
   float cap_in;
   float base, step;
   const float* lut;         // at column 0
-  int lim;                  // visible columns, as far as length and causality go
-  const int* docs;          // documents of the columns (shared memory), or nullptr
-  int doc;
+  uint32_t see[BN / 32];    // bits: visible columns
   int keys;                 // columns that are valid keys (any number)
   bool mine;                // the row is a valid query
 };
 
-template <int D, bool CAP, int BIAS, bool MASK>
-__device__ __forceinline__ bool softmax_block(const SoftmaxBlock& sb, int lane, float& m_ref, uint64_t& sum2) {
-  uint64_t x[BN / 2];                                      // the row, two scores to a register pair
-  {
-    uint32_t sv[BN / 32][32];
-#pragma unroll
-    for (int c = 0; c < BN / 32; ++c) tmem_ld_32x32b_x32_async(sb.t_s + 32 * c, sv[c]);
-#pragma unroll
-    for (int c = 0; c < BN / 32; ++c) tmem_wait_ld(sv[c]);
-#pragma unroll
-    for (int k = 0; k < BN; k += 2)
-      x[k / 2] = f2_pack(__uint_as_float(sv[k / 32][k % 32]), __uint_as_float(sv[k / 32][k % 32 + 1]));
-  }
-  tc_fence_before();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(sb.s_free);
-
+// CAP 0: none; 1: by polynomial; 2: of any size.  x: the row, two scores to a register pair.
+template <int D, int CAP, int BIAS, bool MASK>
+__device__ __forceinline__ bool softmax_row(const SoftmaxBlock& sb, uint64_t (&x)[BN / 2], float& m_ref,
+                                            uint64_t& sum2) {
   // t2 of the row: x * mul + bias.
-  if constexpr (CAP) {
-    float top = 0.f;                                       // (of valid rows and keys, so that no other decides)
+  if constexpr (CAP == 1) {
+    const uint64_t in = f2_pack(sb.cap_in, sb.cap_in);
+#pragma unroll
+    for (int k = 0; k < BN / 2; ++k) {
+      const uint64_t y = f2_mul(x[k], in);
+      x[k] = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
+    }
+  } else if constexpr (CAP == 2) {
+    const float in2 = 2.f * kLog2e * sb.cap_in;
 #pragma unroll
     for (int k = 0; k < BN / 2; ++k) {
       float a, c;
       f2_unpack(x[k], a, c);
-      if (MASK) {
-        a = 2 * k < sb.keys ? a : 0.f;
-        c = 2 * k + 1 < sb.keys ? c : 0.f;
-      }
-      top = fmaxf(fmaxf(top, fabsf(a)), fabsf(c));
-    }
-    const uint64_t in = f2_pack(sb.cap_in, sb.cap_in);
-    const bool small = !any_warp(sb.mine && top * fabsf(sb.cap_in) > kCapPoly);
-    if (small) {
-#pragma unroll
-      for (int k = 0; k < BN / 2; ++k) {
-        const uint64_t y = f2_mul(x[k], in);
-        x[k] = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
-      }
-    } else {
-      const float in2 = 2.f * kLog2e * sb.cap_in;
-#pragma unroll
-      for (int k = 0; k < BN / 2; ++k) {
-        float a, c;
-        f2_unpack(x[k], a, c);
-        x[k] = f2_pack(tanh_of(a, in2), tanh_of(c, in2));
-      }
+      x[k] = f2_pack(tanh_of(a, in2), tanh_of(c, in2));
     }
   }
   const uint64_t mul = CAP ? sb.cap2 : sb.scale2;
@@ -193,18 +165,12 @@ __device__ __forceinline__ bool softmax_block(const SoftmaxBlock& sb, int lane, 
   }
   if constexpr (MASK) {
 #pragma unroll
-    for (int k = 0; k < BN; k += 4) {
-      int4 dj = make_int4(sb.doc, sb.doc, sb.doc, sb.doc);
-      if (sb.docs) dj = *reinterpret_cast<const int4*>(sb.docs + k);
-      float a, c, e, f;
+    for (int k = 0; k < BN; k += 2) {
+      float a, c;
       f2_unpack(x[k / 2], a, c);
-      f2_unpack(x[k / 2 + 1], e, f);
-      a = k < sb.lim && dj.x == sb.doc ? a : -INFINITY;
-      c = k + 1 < sb.lim && dj.y == sb.doc ? c : -INFINITY;
-      e = k + 2 < sb.lim && dj.z == sb.doc ? e : -INFINITY;
-      f = k + 3 < sb.lim && dj.w == sb.doc ? f : -INFINITY;
+      a = sb.see[k / 32] & (1u << k % 32) ? a : -INFINITY;
+      c = sb.see[k / 32] & (2u << k % 32) ? c : -INFINITY;
       x[k / 2] = f2_pack(a, c);
-      x[k / 2 + 1] = f2_pack(e, f);
     }
   }
   float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -251,6 +217,60 @@ __device__ __forceinline__ bool softmax_block(const SoftmaxBlock& sb, int lane, 
     }
     tmem_st_32x32b_x16_async(sb.t_p + c / 2, pk);
   }
+  return true;
+}
+
+template <int D, bool CAP, int BIAS, bool MASK>
+__device__ __forceinline__ bool softmax_block(const SoftmaxBlock& sb, int lane, float& m_ref, uint64_t& sum2) {
+  uint64_t x[BN / 2];
+  {
+    uint32_t sv[BN / 32][32];
+#pragma unroll
+    for (int c = 0; c < BN / 32; ++c) tmem_ld_32x32b_x32_async(sb.t_s + 32 * c, sv[c]);
+#pragma unroll
+    for (int c = 0; c < BN / 32; ++c) tmem_wait_ld(sv[c]);
+#pragma unroll
+    for (int k = 0; k < BN; k += 2)
+      x[k / 2] = f2_pack(__uint_as_float(sv[k / 32][k % 32]), __uint_as_float(sv[k / 32][k % 32 + 1]));
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(sb.s_free);
+  if constexpr (!CAP) {
+    return softmax_row<D, 0, BIAS, MASK>(sb, x, m_ref, sum2);
+  } else {
+    float top = 0.f;                                       // (of valid rows and keys, so that no other decides)
+    if (MASK && sb.keys < BN) {
+#pragma unroll
+      for (int k = 0; k < BN / 2; ++k) {
+        float a, c;
+        f2_unpack(x[k], a, c);
+        top = fmaxf(fmaxf(top, 2 * k < sb.keys ? fabsf(a) : 0.f), 2 * k + 1 < sb.keys ? fabsf(c) : 0.f);
+      }
+    } else {
+      float t4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < BN / 2; ++k) {
+        float a, c;
+        f2_unpack(x[k], a, c);
+        t4[k & 3] = fmaxf(fmaxf(t4[k & 3], fabsf(a)), fabsf(c));
+      }
+      top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+    }
+    return any_warp(sb.mine && top * fabsf(sb.cap_in) > kCapPoly) ? softmax_row<D, 2, BIAS, MASK>(sb, x, m_ref, sum2)
+                                                                  : softmax_row<D, 1, BIAS, MASK>(sb, x, m_ref, sum2);
+  }
+}
+
+// The same for a warp none of whose rows sees the block: P = 0, and nothing else changes.
+__device__ __forceinline__ bool hidden_block(const SoftmaxBlock& sb, int lane) {
+  if (lane == 0) mbar_arrive(sb.s_free);
+  if (sb.it > 0 && !warp_wait(sb.o_done, (sb.it - 1) & 1)) return false;
+  uint32_t zero[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) zero[k] = 0;
+#pragma unroll
+  for (int c = 0; c < BN; c += 32) tmem_st_32x32b_x16_async(sb.t_p + c / 2, zero);
   return true;
 }
 
@@ -480,37 +500,58 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasP
     sb.scale2 = f2_pack(s.scale * kLog2e, s.scale * kLog2e);
     sb.cap2 = f2_pack(cap.cap2, cap.cap2);
     sb.cap_in = cap.in;
-    sb.doc = docs && i < n ? docs[i] : 0;
     sb.mine = i < n;
-    int* wdocs = reinterpret_cast<int*>(smem + C::kDocs) + warp * BN;
+    const int doc = docs && i < n ? docs[i] : 0;
     float m_ref = -INFINITY;
     uint64_t sum2 = 0;                                     // two partial row sums (0.0f, 0.0f)
     const int nb_mine = TILES == 2 && t == 1 ? nb[TILES - 1] : nb[0];
     int it = 0;
     for (int jb = next_block(0); jb < nb_mine; jb = next_block(jb + 1), ++it) {
       const int j0 = jb * BN;
+      // The row's visible keys.  Documents: each id that the warp's rows hold, against the block's keys.
+      const bool by_doc = docs && cls[jb] == 2;
+      bool mask = j0 + BN > jall || by_doc, hidden = false;
+      if (mask) {
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) {
+          const int lim = jlim - j0 - 32 * c;
+          sb.see[c] = lim >= 32 ? ~0u : lim <= 0 ? 0u : (1u << lim) - 1;
+        }
+        if (by_doc) {
+          int dj[BN / 32];
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) {
+            const int j = j0 + 32 * c + lane;
+            dj[c] = j < n ? docs[j] : 0;
+          }
+          uint32_t left = __ballot_sync(0xffffffffu, sb.mine);
+          while (left) {
+            const int d = __shfl_sync(0xffffffffu, doc, __ffs(left) - 1);
+            const bool same = doc == d;
+            left &= ~__ballot_sync(0xffffffffu, same);
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c) {
+              const uint32_t eq = __ballot_sync(0xffffffffu, dj[c] == d);
+              if (same) sb.see[c] &= eq;
+            }
+          }
+        }
+        hidden = !any_warp(sb.mine && (sb.see[0] | sb.see[BN / 32 - 1]) != 0);
+        mask = any_warp(sb.mine && (sb.see[0] & sb.see[BN / 32 - 1]) != ~0u);
+      }
       if (!(ok = warp_wait(s_full(t), it & 1))) break;
       tc_fence_after();
-      // How the block is biased and masked.
+      // How the block is biased.
       sb.it = it;
       const bool near = BIAS && j0 - i_last < bias.reach && j0 + BN - 1 - i_first > -bias.reach;
       const bool ahead = j0 - i_last >= bias.reach;
       sb.step = ahead ? -bias.slope2 : bias.slope2;
       sb.base = (ahead ? bias.right : bias.left) + sb.step * (float)(j0 - i);
       sb.lut = bias.lut + bias.off + (j0 - i);
-      sb.lim = jlim - j0;
       sb.keys = n - j0;
-      const bool by_doc = docs && cls[jb] == 2;
-      sb.docs = nullptr;
-      if (by_doc) {
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < BN; c += 32) wdocs[c + lane] = j0 + c + lane < n ? docs[j0 + c + lane] : 0;
-        __syncwarp();
-        sb.docs = wdocs;
-      }
-      const bool mask = j0 + BN > jall || by_doc;
-      if (BIAS && near)
+      if (hidden)
+        ok = hidden_block(sb, lane);
+      else if (BIAS && near)
         ok = mask ? softmax_block<D, CAP, BIAS ? 3 : 0, true>(sb, lane, m_ref, sum2)
                   : softmax_block<D, CAP, BIAS ? 3 : 0, false>(sb, lane, m_ref, sum2);
       else
@@ -626,9 +667,7 @@ cudaError_t launch_scored_tc(const ScoreArgs& s, const __half* qkv, const int32_
   switch (sh.size_per_head) {
     case 32: return launch_d<32, 1>(s, qkv, valid_len, ctx, lse, sh, status, stream);
     case 64: return launch_d<64, 1>(s, qkv, valid_len, ctx, lse, sh, status, stream);
-    case 128:
-      return sh.seq > 128 ? launch_d<128, 2>(s, qkv, valid_len, ctx, lse, sh, status, stream)
-                          : launch_d<128, 1>(s, qkv, valid_len, ctx, lse, sh, status, stream);
+    case 128: return launch_d<128, 2>(s, qkv, valid_len, ctx, lse, sh, status, stream);
   }
   return cudaErrorInvalidValue;
 }
