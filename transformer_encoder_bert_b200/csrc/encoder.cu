@@ -518,6 +518,7 @@ enc_status make_scores(enc_handle* h, const enc_scores* p, enc::ScoreArgs& s) {
     return fail(ENC_ERR_INVALID_ARG, "cap must be 0 (none) or in [1e-3, 1e4]");
   s.scale = p->scale == 0.f ? 1.f / sqrtf((float)h->d) : p->scale;
   s.cap = p->cap;
+  enc::fold_cap(&s);
   s.slopes = p->slopes;
   s.table = p->bias_table;
   s.causal = p->causal != 0;

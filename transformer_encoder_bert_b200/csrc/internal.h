@@ -216,6 +216,8 @@ constexpr int kMaxScoreSeq = 65536;
 struct ScoreArgs {
   float scale = 0.f;                // of q . k
   float cap = 0.f;                  // 0: no cap
+  // cap log2 e tanh(scale q.k / cap) = q.k P((q.k)^2) while |q.k| <= cap_small_top (fold_cap in scored_tc.cu).
+  float cap_small_top = -1.f, cap_small[4] = {};
   const float* slopes = nullptr;    // [nh] or nullptr
   const float* table = nullptr;     // [buckets, nh] or nullptr
   int buckets = 0, both = 0;
@@ -230,6 +232,7 @@ struct ScoreArgs {
 struct ScoredShape {
   int batch, seq, head_num, size_per_head;
 };
+void fold_cap(ScoreArgs* s);        // fills cap_small of s.scale and s.cap
 // Forward: qkv [3, B, nh, S, d] -> ctx [B*S, nh*d], and lse [B, nh, S] unless nullptr.
 // Rows that see no key (rows i >= n among them): ctx = 0, lse = -inf.
 cudaError_t launch_scored_simt(const ScoreArgs& s, const void* qkv, const int32_t* valid_len, void* ctx, float* lse,

@@ -29,6 +29,7 @@
 // masked.  In a masked block each row's visible keys are a bit set that its
 // thread has before S arrives; a warp whose rows see none of the block writes
 // P = 0 and leaves it.
+#include <cmath>
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -130,19 +131,22 @@ struct SoftmaxBlock {
   bool mine;                // the row is a valid query
 };
 
-// CAP 0: none; 1: by polynomial; 2: of any size.  x: the row, two scores to a register pair.
+// CAP 0: none; 1: small scores; 2: by polynomial; 3: of any size.  x: the row, two scores to a register pair.
 template <int D, int CAP, int BIAS, bool MASK>
-__device__ __forceinline__ bool softmax_row(const SoftmaxBlock& sb, uint64_t (&x)[BN / 2], float& m_ref,
+__device__ __forceinline__ bool softmax_row(const ScoreArgs& s, const SoftmaxBlock& sb, uint64_t (&x)[BN / 2], float& m_ref,
                                             uint64_t& sum2) {
   // t2 of the row: x * mul + bias.
   if constexpr (CAP == 1) {
+#pragma unroll
+    for (int k = 0; k < BN / 2; ++k) x[k] = small_cap2(s, x[k]);
+  } else if constexpr (CAP == 2) {
     const uint64_t in = f2_pack(sb.cap_in, sb.cap_in);
 #pragma unroll
     for (int k = 0; k < BN / 2; ++k) {
       const uint64_t y = f2_mul(x[k], in);
       x[k] = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
     }
-  } else if constexpr (CAP == 2) {
+  } else if constexpr (CAP == 3) {
     const float in2 = 2.f * kLog2e * sb.cap_in;
 #pragma unroll
     for (int k = 0; k < BN / 2; ++k) {
@@ -154,14 +158,15 @@ __device__ __forceinline__ bool softmax_row(const SoftmaxBlock& sb, uint64_t (&x
   const uint64_t mul = CAP ? sb.cap2 : sb.scale2;
 #pragma unroll
   for (int k = 0; k < BN / 2; ++k) {
-    if (BIAS == 0)
-      x[k] = f2_mul(x[k], mul);
-    else if (BIAS == 1)
-      x[k] = f2_fma(x[k], mul, f2_pack(sb.base, sb.base));
-    else if (BIAS == 2)
-      x[k] = f2_fma(x[k], mul, f2_pack(fmaf((float)(2 * k), sb.step, sb.base), fmaf((float)(2 * k + 1), sb.step, sb.base)));
-    else
-      x[k] = f2_fma(x[k], mul, f2_pack(sb.lut[2 * k], sb.lut[2 * k + 1]));
+    if (BIAS == 0) {
+      if (CAP != 1) x[k] = f2_mul(x[k], mul);
+      continue;
+    }
+    const uint64_t add =
+        BIAS == 1   ? f2_pack(sb.base, sb.base)
+        : BIAS == 2 ? f2_pack(fmaf((float)(2 * k), sb.step, sb.base), fmaf((float)(2 * k + 1), sb.step, sb.base))
+                    : f2_pack(sb.lut[2 * k], sb.lut[2 * k + 1]);
+    x[k] = CAP == 1 ? f2_add(x[k], add) : f2_fma(x[k], mul, add);
   }
   if constexpr (MASK) {
 #pragma unroll
@@ -221,7 +226,7 @@ __device__ __forceinline__ bool softmax_row(const SoftmaxBlock& sb, uint64_t (&x
 }
 
 template <int D, bool CAP, int BIAS, bool MASK>
-__device__ __forceinline__ bool softmax_block(const SoftmaxBlock& sb, int lane, float& m_ref, uint64_t& sum2) {
+__device__ __forceinline__ bool softmax_block(const ScoreArgs& s, const SoftmaxBlock& sb, int lane, float& m_ref, uint64_t& sum2) {
   uint64_t x[BN / 2];
   {
     uint32_t sv[BN / 32][32];
@@ -237,7 +242,7 @@ __device__ __forceinline__ bool softmax_block(const SoftmaxBlock& sb, int lane, 
   __syncwarp();
   if (lane == 0) mbar_arrive(sb.s_free);
   if constexpr (!CAP) {
-    return softmax_row<D, 0, BIAS, MASK>(sb, x, m_ref, sum2);
+    return softmax_row<D, 0, BIAS, MASK>(s, sb, x, m_ref, sum2);
   } else {
     float top = 0.f;                                       // (of valid rows and keys, so that no other decides)
     if (MASK && sb.keys < BN) {
@@ -257,8 +262,10 @@ __device__ __forceinline__ bool softmax_block(const SoftmaxBlock& sb, int lane, 
       }
       top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
     }
-    return any_warp(sb.mine && top * fabsf(sb.cap_in) > kCapPoly) ? softmax_row<D, 2, BIAS, MASK>(sb, x, m_ref, sum2)
-                                                                  : softmax_row<D, 1, BIAS, MASK>(sb, x, m_ref, sum2);
+    if (!any_warp(sb.mine && top > s.cap_small_top)) return softmax_row<D, 1, BIAS, MASK>(s, sb, x, m_ref, sum2);
+    if (!any_warp(sb.mine && top * fabsf(sb.cap_in) > kCapPoly))
+      return softmax_row<D, 2, BIAS, MASK>(s, sb, x, m_ref, sum2);
+    return softmax_row<D, 3, BIAS, MASK>(s, sb, x, m_ref, sum2);
   }
 }
 
@@ -552,11 +559,11 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasP
       if (hidden)
         ok = hidden_block(sb, lane);
       else if (BIAS && near)
-        ok = mask ? softmax_block<D, CAP, BIAS ? 3 : 0, true>(sb, lane, m_ref, sum2)
-                  : softmax_block<D, CAP, BIAS ? 3 : 0, false>(sb, lane, m_ref, sum2);
+        ok = mask ? softmax_block<D, CAP, BIAS ? 3 : 0, true>(s, sb, lane, m_ref, sum2)
+                  : softmax_block<D, CAP, BIAS ? 3 : 0, false>(s, sb, lane, m_ref, sum2);
       else
-        ok = mask ? softmax_block<D, CAP, BIAS, true>(sb, lane, m_ref, sum2)
-                  : softmax_block<D, CAP, BIAS, false>(sb, lane, m_ref, sum2);
+        ok = mask ? softmax_block<D, CAP, BIAS, true>(s, sb, lane, m_ref, sum2)
+                  : softmax_block<D, CAP, BIAS, false>(s, sb, lane, m_ref, sum2);
       if (!ok) break;
       // V rows of keys in [n, n rounded up to 16) are read by P V: zeros, whatever memory holds there.
       const int lim = n - j0, lim16 = (min(BN, klim[t] - j0) + 15) & ~15;
@@ -660,6 +667,18 @@ cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, _
 
 }  // namespace
 }  // namespace scored_tc
+
+// Coefficients of tanh(x) / x on |x| <= kCapSmall in powers of x^2, with x = in q.k: multiplied by in^(2k + 1) cap2.
+// Beyond the factors here a coefficient could leave FP32's range, and no score takes this form.
+void fold_cap(ScoreArgs* s) {
+  constexpr double c[4] = {0.9999976754188538, -0.33320656418800354, 0.13145145773887634, -0.04337247461080551};
+  const double in = (double)s->scale / s->cap;
+  s->cap_small_top = -1.f;
+  if (!(s->cap > 0.f) || !(fabs(in) >= 1e-4 && fabs(in) <= 1e4)) return;
+  double f = in * s->cap * 1.4426950408889634;
+  for (int k = 0; k < 4; ++k, f *= in * in) s->cap_small[k] = (float)(c[k] * f);
+  s->cap_small_top = (float)(scored_tc::kCapSmall / fabs(in));
+}
 
 cudaError_t launch_scored_tc(const ScoreArgs& s, const __half* qkv, const int32_t* valid_len, __half* ctx, float* lse,
                              const ScoredShape& sh, int* status, cudaStream_t stream) {

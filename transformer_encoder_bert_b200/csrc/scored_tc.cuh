@@ -147,12 +147,14 @@ __device__ __forceinline__ Bias make_bias(const ScoreArgs& s, float* column, flo
 
 // The cap, t2 = cap2 tanh(x) with x = s * in = u / cap.  The exact form,
 // tanh(x) = 1 - 2 / (1 + 2^(2 x log2 e)), costs two special-function operations
-// a score (a quarter of the FMA rate each, besides the softmax's own); where
-// every |x| of a warp's block is at most kCapPoly, a polynomial x P(x^2) does it
-// on the FMA pipe.  P is a least-maximum fit of degree 7, found by reweighted
-// least squares: |x P(x^2) - tanh(x)| <= 3.5e-8, 1.3e-7 with FP32 rounding.  The
-// exact form is off by about 2^-22.
-constexpr float kCapPoly = 1.25f;
+// a score (a quarter of the FMA rate each, besides the softmax's own).  Where
+// every |x| of a warp's block is at most kCapPoly, a polynomial x P(x^2) of degree 7
+// in x^2 does it on the FMA pipe, and where every one is at most kCapSmall, one of
+// degree 3 with in and cap2 taken into its coefficients (s.cap_small), 5 operations
+// a score where the other costs 11.  Both are least-maximum fits found by reweighted
+// least squares: |x P(x^2) - tanh(x)| <= 3.5e-8 and 1.3e-7, with FP32 rounding
+// 1.4e-7 and 1.6e-7.  The exact form is off by about 2^-22.
+constexpr float kCapPoly = 1.25f, kCapSmall = 0.5f;
 struct Cap {
   float in, cap2;
   bool on;
@@ -172,6 +174,14 @@ __device__ __forceinline__ uint64_t tanh_over_x2(uint64_t z) {
 #pragma unroll
   for (int k = 6; k >= 0; --k) p = f2_fma(p, z, f2_pack(c[k], c[k]));
   return p;
+}
+// t2 of two scores by s.cap_small.
+__device__ __forceinline__ uint64_t small_cap2(const ScoreArgs& s, uint64_t x) {
+  const uint64_t z = f2_mul(x, x);
+  uint64_t p = f2_pack(s.cap_small[3], s.cap_small[3]);
+#pragma unroll
+  for (int k = 2; k >= 0; --k) p = f2_fma(p, z, f2_pack(s.cap_small[k], s.cap_small[k]));
+  return f2_mul(x, p);
 }
 // tanh(s in) of any size; in2 = 2 in log2 e.
 __device__ __forceinline__ float tanh_of(float s, float in2) { return fmaf(-2.f, rcp(1.f + ex2(s * in2)), 1.f); }

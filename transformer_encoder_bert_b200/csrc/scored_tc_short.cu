@@ -58,12 +58,13 @@ struct ShortChunk {
   bool mine;                // the row is a valid query
 };
 template <bool CAP, bool BIAS, bool MASK>
-__device__ __forceinline__ float first_pass(const ShortChunk& ch, float mx) {
+__device__ __forceinline__ float first_pass(const ScoreArgs& s, const ShortChunk& ch, float mx) {
   uint32_t sv[32];
   tmem_ld_32x32b_x32(ch.t_s, sv);
   uint64_t x[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) x[k] = f2_pack(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1]));
+  uint64_t mul = CAP ? ch.cap2 : ch.scale2;
   if constexpr (CAP) {
     float top = 0.f;                                       // (of valid rows and keys, so that no other decides)
 #pragma unroll
@@ -76,7 +77,11 @@ __device__ __forceinline__ float first_pass(const ShortChunk& ch, float mx) {
       }
       top = fmaxf(fmaxf(top, fabsf(a)), fabsf(c));
     }
-    if (!any_warp(ch.mine && top * fabsf(ch.cap_in) > kCapPoly)) {
+    if (!any_warp(ch.mine && top > s.cap_small_top)) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = small_cap2(s, x[k]);
+      mul = f2_pack(1.f, 1.f);
+    } else if (!any_warp(ch.mine && top * fabsf(ch.cap_in) > kCapPoly)) {
       const uint64_t in = f2_pack(ch.cap_in, ch.cap_in);
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
@@ -93,7 +98,6 @@ __device__ __forceinline__ float first_pass(const ShortChunk& ch, float mx) {
       }
     }
   }
-  const uint64_t mul = CAP ? ch.cap2 : ch.scale2;
   float m2[2] = {mx, mx};
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
@@ -291,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, SCfg<D>::kCtasPerSm)
         ch.lim = jlim - 32 * c;
         ch.docs = s.docs ? key_docs + 32 * c : nullptr;
         ch.keys = n - 32 * c;
-        mx = 32 * c + 32 <= jall ? first_pass<CAP, BIAS, false>(ch, mx) : first_pass<CAP, BIAS, true>(ch, mx);
+        mx = 32 * c + 32 <= jall ? first_pass<CAP, BIAS, false>(s, ch, mx) : first_pass<CAP, BIAS, true>(s, ch, mx);
       }
       const float mu = mx == -INFINITY ? 0.f : mx;
       const uint64_t neg_m2 = f2_pack(-mu, -mu);
