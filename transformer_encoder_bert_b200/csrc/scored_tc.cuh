@@ -157,6 +157,7 @@ __device__ __forceinline__ Bias make_bias(const ScoreArgs& s, float* column, flo
 constexpr float kCapPoly = 1.25f, kCapSmall = 0.5f;
 struct Cap {
   float in, cap2;
+  float neg_inv2;           // -1 / cap2^2: 1 - tanh^2 of a capped score
   bool on;
 };
 __device__ __forceinline__ Cap make_cap(const ScoreArgs& s) {
@@ -164,6 +165,7 @@ __device__ __forceinline__ Cap make_cap(const ScoreArgs& s) {
   c.on = s.cap > 0.f;
   c.in = c.on ? s.scale / s.cap : 0.f;
   c.cap2 = s.cap * kLog2e;
+  c.neg_inv2 = c.on ? -1.f / (c.cap2 * c.cap2) : 0.f;
   return c;
 }
 // tanh(x) / x of two scores from x^2, |x| <= kCapPoly.
@@ -183,6 +185,8 @@ __device__ __forceinline__ uint64_t small_cap2(const ScoreArgs& s, uint64_t x) {
   for (int k = 2; k >= 0; --k) p = f2_fma(p, z, f2_pack(s.cap_small[k], s.cap_small[k]));
   return f2_mul(x, p);
 }
+// The forms of the cap; any: also when there is none.
+constexpr int kAny = 0, kPoly = 1, kSmall = 2;
 // tanh(s in) of any size; in2 = 2 in log2 e.
 __device__ __forceinline__ float tanh_of(float s, float in2) { return fmaf(-2.f, rcp(1.f + ex2(s * in2)), 1.f); }
 

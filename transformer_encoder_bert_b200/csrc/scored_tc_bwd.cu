@@ -59,8 +59,7 @@ struct BCfg {
   // a_full, drain, b_full, b_empty (kStages each), s_full, p_full, done (NB each)
   static constexpr int kNumBars = 2 + 2 * kStages + 3 * NB;
   static constexpr int kSlot = kBars + kNumBars * 8;
-  static constexpr int kDocs = (kSlot + 16 + 15) / 16 * 16;   // per row warp: the block's documents
-  static constexpr int kSums = kDocs + kRowWarps * kBN * 4;   // dQ: per row warp, bucket sums
+  static constexpr int kSums = (kSlot + 16 + 15) / 16 * 16;   // dQ: per row warp, bucket sums
   static constexpr int kColumn = kSums + (MODE == kDQ ? kRowWarps * kMaxScoreBuckets * 4 : 0);   // of the bias table
   static constexpr int kLut = kColumn + kMaxScoreBuckets * 4;
   static constexpr int kS = 0, kDP = NB * kBN, kAcc = 2 * NB * kBN;
@@ -77,9 +76,7 @@ struct RowBlock {
   uint32_t t_s, t_dp;       // TMEM addresses of the row warp's S and dP columns
   float base, step;         // bias (less lse2 in dQ mode): base, base + step * column, or base + lut
   const float* lut;         // at column 0
-  int lo, hi;               // visible columns, as far as length and causality go
-  const int* docs;          // documents of the columns (shared memory), or nullptr
-  int doc;
+  uint32_t see[2];          // bits: visible columns
   float e, de;              // dU's scale, and D e (dQ mode)
   const float* col;         // dKV mode: -lse2 [64], D [64] of the columns (shared memory)
   bool whole;               // no row or column of the block is past n
@@ -89,9 +86,9 @@ struct RowBlock {
 // CH columns of it from column c, two at a time in packed FP32 arithmetic.  NEAR 0: constant bias; 1: bias from the
 // table in shared memory; 2: that, and the diagonals' sums: for column k, lane t takes dT of row (k - t) mod 32, which
 // lies on the diagonal whose column less row is t (pos) or t - 32 (neg); else pos += dT.  NEAR 3: linear bias.
-// POLY: the cap's polynomial.
-template <int MODE, int CH, bool CAP, int NEAR, bool MASK, bool POLY>
-__device__ __forceinline__ void row_chunk(const RowBlock& rb, const Cap& cap, float scale2, int lane, int c,
+// FORM: of the cap.
+template <int MODE, int CH, bool CAP, int NEAR, bool MASK, int FORM>
+__device__ __forceinline__ void row_chunk(const ScoreArgs& s, const RowBlock& rb, const Cap& cap, float scale2, int lane, int c,
                                           const uint32_t (&sv)[CH], const uint32_t (&dp)[CH], float& pos, float& neg) {
   uint32_t pp[CH / 2], pu[CH / 2];
   const int k0 = c & 31;                                   // column of a 32 x 32 block
@@ -100,7 +97,7 @@ __device__ __forceinline__ void row_chunk(const RowBlock& rb, const Cap& cap, fl
   const uint64_t base2 = f2_pack(base, base), e2 = f2_pack(rb.e, rb.e), neg_e2 = f2_pack(-rb.e, -rb.e);
   const uint64_t mul = CAP ? f2_pack(cap.cap2, cap.cap2) : f2_pack(scale2, scale2), one2 = f2_pack(1.f, 1.f);
   const uint64_t row_d2 = f2_pack(-rb.de, -rb.de);
-  const int lo = rb.lo - c, hi = rb.hi - c;
+  const uint32_t see = (c < 32 ? rb.see[0] : rb.see[1]) >> (c & 31);
   uint64_t far2 = 0;                                       // two partial sums of dT (0.0f, 0.0f)
 #pragma unroll
   for (int k = 0; k < CH; k += 4) {
@@ -109,22 +106,20 @@ __device__ __forceinline__ void row_chunk(const RowBlock& rb, const Cap& cap, fl
       nl = *reinterpret_cast<const ulonglong2*>(rb.col + c + k);
       dc = *reinterpret_cast<const ulonglong2*>(rb.col + kBN + c + k);
     }
-    int4 dj = make_int4(0, 0, 0, 0);
-    if (MASK && rb.docs) dj = *reinterpret_cast<const int4*>(rb.docs + c + k);
-    const int djs[4] = {dj.x, dj.y, dj.z, dj.w};
 #pragma unroll
     for (int q = 0; q < 4; q += 2) {
       const int at = k + q;
-      uint64_t x = f2_pack(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), th = 0;
+      uint64_t x = f2_pack(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1]));
       if constexpr (CAP) {
-        if (POLY) {
+        if (FORM == kSmall) {
+          x = small_cap2(s, x);
+        } else if (FORM == kPoly) {
           const uint64_t y = f2_mul(x, f2_pack(cap.in, cap.in));
-          th = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
+          x = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
         } else {
           const float in2 = 2.f * kLog2e * cap.in;
-          th = f2_pack(tanh_of(__uint_as_float(sv[at]), in2), tanh_of(__uint_as_float(sv[at + 1]), in2));
+          x = f2_pack(tanh_of(__uint_as_float(sv[at]), in2), tanh_of(__uint_as_float(sv[at + 1]), in2));
         }
-        x = th;
       }
       uint64_t add = base2;
       if (NEAR == 3) add = f2_pack(fmaf((float)at, rb.step, base), fmaf((float)(at + 1), rb.step, base));
@@ -134,19 +129,21 @@ __device__ __forceinline__ void row_chunk(const RowBlock& rb, const Cap& cap, fl
       }
       if (MODE == kDKV) add = f2_add(add, q ? nl.y : nl.x);
       float t0, t1;
-      f2_unpack(f2_fma(x, mul, add), t0, t1);
+      f2_unpack(CAP && FORM == kSmall ? f2_add(x, add) : f2_fma(x, mul, add), t0, t1);
       float p0 = ex2(t0), p1 = ex2(t1);
       const uint64_t d2 = MODE == kDKV ? f2_mul(q ? dc.y : dc.x, neg_e2) : row_d2;
       const uint64_t dt2 =
           f2_mul(f2_pack(p0, p1), f2_fma(f2_pack(__uint_as_float(dp[at]), __uint_as_float(dp[at + 1])), e2, d2));
       uint64_t u2 = dt2;
-      if constexpr (CAP) u2 = f2_mul(dt2, f2_fma(f2_mul(th, f2_pack(-1.f, -1.f)), th, one2));
+      if constexpr (CAP) {                                 // dU = dT (1 - tanh^2)
+        const float f = FORM == kSmall ? cap.neg_inv2 : -1.f;
+        u2 = f2_mul(dt2, f2_fma(f2_mul(x, f2_pack(f, f)), x, one2));
+      }
       float u0, u1, a0, a1;
       f2_unpack(u2, u0, u1);
       f2_unpack(dt2, a0, a1);
       if (MASK) {                                          // (hidden scores may be NaN)
-        const bool see0 = at >= lo && at < hi && (!rb.docs || djs[q] == rb.doc);
-        const bool see1 = at + 1 >= lo && at + 1 < hi && (!rb.docs || djs[q + 1] == rb.doc);
+        const bool see0 = see & (1u << at), see1 = see & (2u << at);
         p0 = see0 ? p0 : 0.f;
         p1 = see1 ? p1 : 0.f;
         a0 = see0 ? a0 : 0.f;
@@ -184,8 +181,8 @@ __device__ __forceinline__ void row_chunk(const RowBlock& rb, const Cap& cap, fl
 // Columns [first, last).  sums: NEAR 2: the lane's diagonals, k: columns less rows lane + 32 (k - 1), from the first
 // column and the warp's first row; else sums[1] += dT.
 template <int MODE, int CH, bool CAP, int NEAR, bool MASK>
-__device__ __forceinline__ void row_block(const RowBlock& rb, int first, int last, const Cap& cap, float scale2, int lane,
-                                          float (&sums)[3]) {
+__device__ __forceinline__ void row_block(const ScoreArgs& s, const RowBlock& rb, int first, int last, const Cap& cap, float scale2,
+                                          int lane, float (&sums)[3]) {
   float pos = 0.f, neg = 0.f;
 #pragma unroll 1
   for (int c = first; c < last; c += CH) {
@@ -199,18 +196,20 @@ __device__ __forceinline__ void row_block(const RowBlock& rb, int first, int las
     }
     tmem_wait_ld(sv);
     tmem_wait_ld(dp);
-    bool poly = false;
+    int form = kAny;
     if constexpr (CAP) {
       float top = 0.f;
 #pragma unroll
       for (int k = 0; k < CH; k += 2)
         top = fmaxf(fmaxf(top, fabsf(__uint_as_float(sv[k]))), fabsf(__uint_as_float(sv[k + 1])));
-      poly = rb.whole && !any_warp(top * fabsf(cap.in) > kCapPoly);
+      if (rb.whole) form = !any_warp(top > s.cap_small_top) ? kSmall : !any_warp(top * fabsf(cap.in) > kCapPoly) ? kPoly : kAny;
     }
-    if (CAP && poly)
-      row_chunk<MODE, CH, CAP, NEAR, MASK, CAP>(rb, cap, scale2, lane, c, sv, dp, pos, neg);
+    if (CAP && form == kSmall)
+      row_chunk<MODE, CH, CAP, NEAR, MASK, CAP ? kSmall : kAny>(s, rb, cap, scale2, lane, c, sv, dp, pos, neg);
+    else if (CAP && form == kPoly)
+      row_chunk<MODE, CH, CAP, NEAR, MASK, CAP ? kPoly : kAny>(s, rb, cap, scale2, lane, c, sv, dp, pos, neg);
     else
-      row_chunk<MODE, CH, CAP, NEAR, MASK, false>(rb, cap, scale2, lane, c, sv, dp, pos, neg);
+      row_chunk<MODE, CH, CAP, NEAR, MASK, kAny>(s, rb, cap, scale2, lane, c, sv, dp, pos, neg);
     if (NEAR == 2 && c + CH == first + 32) {
       sums[0] = neg;
       neg = pos;                                           // the first 32 columns' lane is the next ones' lane - 32
@@ -225,13 +224,25 @@ __device__ __forceinline__ void row_block(const RowBlock& rb, int first, int las
   }
 }
 
+// Columns [first, last) of a warp none of whose rows sees them: P = dU = 0, nothing to sum.
+template <int MODE>
+__device__ __forceinline__ void hidden_rows(const RowBlock& rb, int first, int last) {
+  uint32_t zero[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) zero[k] = 0;
+  for (int c = first; c < last; c += 32) {
+    if constexpr (MODE == kDKV) tmem_st_32x32b_x16_async(rb.t_s + rb.p_at + c / 2, zero);
+    tmem_st_32x32b_x16_async(rb.t_dp + rb.p_at + c / 2, zero);
+  }
+}
+
 template <int MODE, int CH, bool CAP, int NEAR>
-__device__ __forceinline__ void row_block_m(bool mask, const RowBlock& rb, int first, int last, const Cap& cap,
+__device__ __forceinline__ void row_block_m(const ScoreArgs& s, bool mask, const RowBlock& rb, int first, int last, const Cap& cap,
                                             float scale2, int lane, float (&sums)[3]) {
   if (mask)
-    row_block<MODE, CH, CAP, NEAR, true>(rb, first, last, cap, scale2, lane, sums);
+    row_block<MODE, CH, CAP, NEAR, true>(s, rb, first, last, cap, scale2, lane, sums);
   else
-    row_block<MODE, CH, CAP, NEAR, false>(rb, first, last, cap, scale2, lane, sums);
+    row_block<MODE, CH, CAP, NEAR, false>(s, rb, first, last, cap, scale2, lane, sums);
 }
 
 template <int D, int MODE>
@@ -476,14 +487,13 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
     const int lo_all = MODE == kDQ ? 0 : score_ilow(s, r_end, prefix);
     const int hi_all = MODE == kDQ ? score_jlim(s, r0, n, prefix) : n;
     RowBlock rb;
-    rb.doc = docs && mine ? docs[pos] : 0;
+    const int doc = docs && mine ? docs[pos] : 0;
     rb.e = e;
     rb.de = dsum * e;
     const int buf = C::NB == 2 ? w : 0, first = C::kShare == 2 ? 32 * w : 0, last = C::kShare == 2 ? first + 32 : kBN;
     rb.t_s = t_lane + C::kS + buf * kBN;
     rb.t_dp = t_lane + C::kDP + buf * kBN;
     rb.p_at = C::kShare == 2 ? 16 * w : 0;                 // within the columns that the warpgroup reads itself
-    int* wdocs = reinterpret_cast<int*>(smem + C::kDocs) + warp * kBN;
     float far_right = 0.f, far_left = 0.f;                 // sums of dT past the table's reach
     const bool biased = s.table || s.slopes;
     int it = 0;
@@ -494,15 +504,34 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
       const bool cut = lo_all > c0 || c0 + kBN > hi_all || r_end >= n;
       const bool by_doc = docs && cls[jb] == 2;
       rb.whole = r_end < n && c0 + kBN <= n;
-      rb.lo = lo - c0;
-      rb.hi = hi - c0;
-      rb.docs = nullptr;
-      if (by_doc) {
-        __syncwarp();
+      // The row's visible columns among those that its warpgroup takes.  Documents: each id that the warp's rows
+      // hold, against the columns'.
+      bool mask = cut || by_doc, hidden = false;
+      if (mask) {
+        uint32_t some = 0, all = ~0u;
 #pragma unroll
-        for (int c = 0; c < kBN; c += 32) wdocs[c + lane] = c0 + c + lane < n ? docs[c0 + c + lane] : 0;
-        __syncwarp();
-        rb.docs = wdocs;
+        for (int c = 0; c < kBN / 32; ++c) {
+          if (C::kShare == 2 && c != w) continue;
+          auto below = [](int x) { return x >= 32 ? ~0u : x <= 0 ? 0u : (1u << x) - 1; };
+          uint32_t see = below(hi - c0 - 32 * c) & ~below(lo - c0 - 32 * c);
+          if (by_doc) {
+            const int j = c0 + 32 * c + lane, dj = j < n ? docs[j] : 0;
+            uint32_t left = __ballot_sync(0xffffffffu, mine), eq = 0;
+            while (left) {
+              const int d = __shfl_sync(0xffffffffu, doc, __ffs(left) - 1);
+              const bool same = doc == d;
+              const uint32_t here = __ballot_sync(0xffffffffu, dj == d);
+              left &= ~__ballot_sync(0xffffffffu, same);
+              if (same) eq = here;
+            }
+            see &= eq;
+          }
+          rb.see[c] = see;
+          some |= see;
+          all &= see;
+        }
+        hidden = !any_warp(some != 0);                     // (rows past n see nothing)
+        mask = any_warp(all != ~0u);
       }
       // Distances key - query of the block, and its bias.
       const int rel0 = MODE == kDQ ? c0 - pos : pos - c0;  // at column 0
@@ -518,28 +547,29 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
       if (!(ok = warp_wait(s_full(buf), ph))) break;
       if (MODE == kDKV && !(ok = warp_wait(b_full(st), (it / C::kStages) & 1))) break;   // the columns' lse2 and D
       tc_fence_after();
-      const bool mask = cut || by_doc;
       float sum[3] = {};
-      if (near) {
+      if (hidden) {
+        hidden_rows<MODE>(rb, first, last);
+      } else if (near) {
         if (MODE == kDQ && partial) {
           if (cap.on)
-            row_block_m<MODE, C::kChunk, true, MODE == kDQ ? 2 : 1>(mask, rb, first, last, cap, scale2, lane, sum);
+            row_block_m<MODE, C::kChunk, true, MODE == kDQ ? 2 : 1>(s, mask, rb, first, last, cap, scale2, lane, sum);
           else
-            row_block_m<MODE, C::kChunk, false, MODE == kDQ ? 2 : 1>(mask, rb, first, last, cap, scale2, lane, sum);
+            row_block_m<MODE, C::kChunk, false, MODE == kDQ ? 2 : 1>(s, mask, rb, first, last, cap, scale2, lane, sum);
         } else if (cap.on) {
-          row_block_m<MODE, C::kChunk, true, 1>(mask, rb, first, last, cap, scale2, lane, sum);
+          row_block_m<MODE, C::kChunk, true, 1>(s, mask, rb, first, last, cap, scale2, lane, sum);
         } else {
-          row_block_m<MODE, C::kChunk, false, 1>(mask, rb, first, last, cap, scale2, lane, sum);
+          row_block_m<MODE, C::kChunk, false, 1>(s, mask, rb, first, last, cap, scale2, lane, sum);
         }
       } else if (s.slopes) {
         if (cap.on)
-          row_block_m<MODE, C::kChunk, true, 3>(mask, rb, first, last, cap, scale2, lane, sum);
+          row_block_m<MODE, C::kChunk, true, 3>(s, mask, rb, first, last, cap, scale2, lane, sum);
         else
-          row_block_m<MODE, C::kChunk, false, 3>(mask, rb, first, last, cap, scale2, lane, sum);
+          row_block_m<MODE, C::kChunk, false, 3>(s, mask, rb, first, last, cap, scale2, lane, sum);
       } else if (cap.on) {
-        row_block_m<MODE, C::kChunk, true, 0>(mask, rb, first, last, cap, scale2, lane, sum);
+        row_block_m<MODE, C::kChunk, true, 0>(s, mask, rb, first, last, cap, scale2, lane, sum);
       } else {
-        row_block_m<MODE, C::kChunk, false, 0>(mask, rb, first, last, cap, scale2, lane, sum);
+        row_block_m<MODE, C::kChunk, false, 0>(s, mask, rb, first, last, cap, scale2, lane, sum);
       }
       // Rows of the columns' operands in [n, n rounded up to 16) are read by the products: zeros.
       const int lim = n - c0, lim16 = (min(kBN, lim) + 15) & ~15;

@@ -79,9 +79,9 @@ struct BwdChunk {
 };
 
 // DIAG: adds dT to the lane's two diagonals of the 32 x 32 block (k0: the chunk's first column in it).
-// POLY: the cap's polynomial.
-template <bool CAP, bool BIAS, bool DIAG, bool MASK, bool POLY>
-__device__ __forceinline__ void bwd_scores(const BwdChunk& ch, const Cap& cap, float scale2, int lane, int k0,
+// FORM: of the cap.
+template <bool CAP, bool BIAS, bool DIAG, bool MASK, int FORM>
+__device__ __forceinline__ void bwd_scores(const ScoreArgs& s, const BwdChunk& ch, const Cap& cap, float scale2, int lane, int k0,
                                            const uint32_t (&sv)[16], const uint32_t (&dp)[16], float& pos, float& neg) {
   uint32_t pp[8], pu[8];
   const uint64_t e2 = f2_pack(ch.e, ch.e), neg_e2 = f2_pack(-ch.e, -ch.e), one2 = f2_pack(1.f, 1.f);
@@ -96,27 +96,31 @@ __device__ __forceinline__ void bwd_scores(const BwdChunk& ch, const Cap& cap, f
 #pragma unroll
     for (int q = 0; q < 4; q += 2) {
       const int at = k + q;
-      uint64_t x = f2_pack(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), th = 0;
+      uint64_t x = f2_pack(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1]));
       if constexpr (CAP) {
-        if (POLY) {
+        if (FORM == kSmall) {
+          x = small_cap2(s, x);
+        } else if (FORM == kPoly) {
           const uint64_t y = f2_mul(x, f2_pack(cap.in, cap.in));
-          th = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
+          x = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
         } else {
           const float in2 = 2.f * kLog2e * cap.in;
-          th = f2_pack(tanh_of(__uint_as_float(sv[at]), in2), tanh_of(__uint_as_float(sv[at + 1]), in2));
+          x = f2_pack(tanh_of(__uint_as_float(sv[at]), in2), tanh_of(__uint_as_float(sv[at + 1]), in2));
         }
-        x = th;
       }
       uint64_t add = q ? nl.y : nl.x;
       if (BIAS) add = f2_add(add, f2_pack(ch.lut[-at], ch.lut[-(at + 1)]));
       float t0, t1;
-      f2_unpack(f2_fma(x, mul, add), t0, t1);
+      f2_unpack(CAP && FORM == kSmall ? f2_add(x, add) : f2_fma(x, mul, add), t0, t1);
       float p0 = ex2(t0), p1 = ex2(t1);
       const uint64_t dt2 =
           f2_mul(f2_pack(p0, p1), f2_fma(f2_pack(__uint_as_float(dp[at]), __uint_as_float(dp[at + 1])), e2,
                                          f2_mul(q ? dc.y : dc.x, neg_e2)));
       uint64_t u2 = dt2;
-      if constexpr (CAP) u2 = f2_mul(dt2, f2_fma(f2_mul(th, f2_pack(-1.f, -1.f)), th, one2));
+      if constexpr (CAP) {                                 // dU = dT (1 - tanh^2)
+        const float f = FORM == kSmall ? cap.neg_inv2 : -1.f;
+        u2 = f2_mul(dt2, f2_fma(f2_mul(x, f2_pack(f, f)), x, one2));
+      }
       float u0, u1, a0, a1;
       f2_unpack(u2, u0, u1);
       f2_unpack(dt2, a0, a1);
@@ -145,25 +149,27 @@ __device__ __forceinline__ void bwd_scores(const BwdChunk& ch, const Cap& cap, f
 }
 
 template <bool CAP, bool BIAS, bool DIAG, bool MASK>
-__device__ __forceinline__ void bwd_chunk(const BwdChunk& ch, const Cap& cap, float scale2, int lane, int k0, float& pos,
-                                          float& neg) {
+__device__ __forceinline__ void bwd_chunk(const ScoreArgs& s, const BwdChunk& ch, const Cap& cap, float scale2, int lane,
+                                          int k0, float& pos, float& neg) {
   uint32_t sv[16], dp[16];
   tmem_ld_32x32b_x16_async(ch.t_s, sv);
   tmem_ld_32x32b_x16_async(ch.t_dp, dp);
   tmem_wait_ld(sv);
   tmem_wait_ld(dp);
-  bool poly = false;
+  int form = kAny;
   if constexpr (CAP) {
     float top = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; k += 2)
       top = fmaxf(fmaxf(top, fabsf(__uint_as_float(sv[k]))), fabsf(__uint_as_float(sv[k + 1])));
-    poly = ch.whole && !any_warp(top * fabsf(cap.in) > kCapPoly);
+    if (ch.whole) form = !any_warp(top > s.cap_small_top) ? kSmall : !any_warp(top * fabsf(cap.in) > kCapPoly) ? kPoly : kAny;
   }
-  if (CAP && poly)
-    bwd_scores<CAP, BIAS, DIAG, MASK, CAP>(ch, cap, scale2, lane, k0, sv, dp, pos, neg);
+  if (CAP && form == kSmall)
+    bwd_scores<CAP, BIAS, DIAG, MASK, CAP ? kSmall : kAny>(s, ch, cap, scale2, lane, k0, sv, dp, pos, neg);
+  else if (CAP && form == kPoly)
+    bwd_scores<CAP, BIAS, DIAG, MASK, CAP ? kPoly : kAny>(s, ch, cap, scale2, lane, k0, sv, dp, pos, neg);
   else
-    bwd_scores<CAP, BIAS, DIAG, MASK, false>(ch, cap, scale2, lane, k0, sv, dp, pos, neg);
+    bwd_scores<CAP, BIAS, DIAG, MASK, kAny>(s, ch, cap, scale2, lane, k0, sv, dp, pos, neg);
 }
 
 template <int D, bool CAP, bool BIAS, bool DIAG>
@@ -441,9 +447,9 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
             *reinterpret_cast<uint4*>(ch.du + 16 * (ch.unit ^ ch.swizzle)) = make_uint4(0, 0, 0, 0);
             *reinterpret_cast<uint4*>(ch.du + 16 * ((ch.unit + 1) ^ ch.swizzle)) = make_uint4(0, 0, 0, 0);
           } else if (s.docs || w1 >= n || i + 16 > n || i < ilow_all) {
-            bwd_chunk<CAP, BIAS, DIAG, true>(ch, cap, scale2, lane, c, pos, neg);
+            bwd_chunk<CAP, BIAS, DIAG, true>(s, ch, cap, scale2, lane, c, pos, neg);
           } else {
-            bwd_chunk<CAP, BIAS, DIAG, false>(ch, cap, scale2, lane, c, pos, neg);
+            bwd_chunk<CAP, BIAS, DIAG, false>(s, ch, cap, scale2, lane, c, pos, neg);
           }
         }
         if (DIAG) {
