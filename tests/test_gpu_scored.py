@@ -105,9 +105,10 @@ class Case:
 
 def _t_error(c):
     """Bound on the error of any t of the case: the dot product, its scaling, the cap, the bias, and the
-    rounding of t in units of log2 (at most 4 roundings of |t| by 2^-24, twice counted)."""
+    rounding of t in units of log2 (at most 4 roundings of |t| by 2^-24, twice counted).  The bounds take |scale|:
+    errors of a product are relative to its magnitude, whatever the scale's sign."""
     q, k = (SO._clean(c.qkv[i], c.valid, 2) for i in range(2))
-    dots = c.spec.scale * (np.abs(q) @ np.swapaxes(np.abs(k), -1, -2)).max()
+    dots = abs(c.spec.scale) * (np.abs(q) @ np.swapaxes(np.abs(k), -1, -2)).max()
     pos = np.arange(c.s)
     t, _ = SO.scores(c.spec, q, k, pos, pos)
     top = np.abs(t).max() + np.abs(SO.bias(c.spec, c.nh, pos, pos)).max() + c.spec.cap
@@ -152,7 +153,8 @@ def check_backward(c, ctx, lse, dqkv, dtable):
     err_p = (eps_p + 2 * rel) * p + tiny
     seen = p > 0
     err_du, err_p = np.where(seen, err_du, 0), np.where(seen, err_p, 0)
-    bound = np.stack((c.spec.scale * (err_du @ k), c.spec.scale * (np.swapaxes(err_du, -1, -2) @ q),
+    scale = abs(c.spec.scale)
+    bound = np.stack((scale * (err_du @ k), scale * (np.swapaxes(err_du, -1, -2) @ q),
                       np.swapaxes(err_p, -1, -2) @ do)) + eps_out * np.abs(ref) + tiny
     got = dqkv.cpu().numpy().astype(np.float64)
     assert np.isfinite(got).all()
