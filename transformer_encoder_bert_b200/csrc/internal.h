@@ -217,7 +217,7 @@ struct ScoreArgs {
   float scale = 0.f;                // of q . k
   float cap = 0.f;                  // 0: no cap
   // cap log2 e tanh(scale q.k / cap) = q.k P((q.k)^2) while |q.k| <= cap_small_top (fold_cap in scored_tc.cu).
-  float cap_small_top = -1.f, cap_small[4] = {};
+  float cap_small_top = -1.f, cap_small[5] = {};
   const float* slopes = nullptr;    // [nh] or nullptr
   const float* table = nullptr;     // [buckets, nh] or nullptr
   int buckets = 0, both = 0;

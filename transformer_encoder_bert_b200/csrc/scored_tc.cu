@@ -671,12 +671,12 @@ cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, _
 // Coefficients of tanh(x) / x on |x| <= kCapSmall in powers of x^2, with x = in q.k: multiplied by in^(2k + 1) cap2.
 // Beyond the factors here a coefficient could leave FP32's range, and no score takes this form.
 void fold_cap(ScoreArgs* s) {
-  constexpr double c[4] = {0.9999976754188538, -0.33320656418800354, 0.13145145773887634, -0.04337247461080551};
+  constexpr double c[5] = {1.0, -0.33333075046539307, 0.13324907422065735, -0.0529942512512207, 0.017151331529021263};
   const double in = (double)s->scale / s->cap;
   s->cap_small_top = -1.f;
   if (!(s->cap > 0.f) || !(fabs(in) >= 1e-4 && fabs(in) <= 1e4)) return;
   double f = in * s->cap * 1.4426950408889634;
-  for (int k = 0; k < 4; ++k, f *= in * in) s->cap_small[k] = (float)(c[k] * f);
+  for (int k = 0; k < 5; ++k, f *= in * in) s->cap_small[k] = (float)(c[k] * f);
   s->cap_small_top = (float)(scored_tc::kCapSmall / fabs(in));
 }
 

@@ -148,12 +148,14 @@ __device__ __forceinline__ Bias make_bias(const ScoreArgs& s, float* column, flo
 // The cap, t2 = cap2 tanh(x) with x = s * in = u / cap.  The exact form,
 // tanh(x) = 1 - 2 / (1 + 2^(2 x log2 e)), costs two special-function operations
 // a score (a quarter of the FMA rate each, besides the softmax's own).  Where
-// every |x| of a warp's block is at most kCapPoly, a polynomial x P(x^2) of degree 7
+// every |x| of a warp's block is at most kCapPoly, a polynomial x P(x^2) of degree 8
 // in x^2 does it on the FMA pipe, and where every one is at most kCapSmall, one of
-// degree 3 with in and cap2 taken into its coefficients (s.cap_small), 5 operations
-// a score where the other costs 11.  Both are least-maximum fits found by reweighted
-// least squares: |x P(x^2) - tanh(x)| <= 3.5e-8 and 1.3e-7, with FP32 rounding
-// 1.4e-7 and 1.6e-7.  The exact form is off by about 2^-22.
+// degree 4 with in and cap2 taken into its coefficients (s.cap_small), 6 operations
+// a score where the other costs 12.  Both are least-maximum fits of the relative
+// error, found by reweighted least squares: 7.7e-9 and 1.3e-8, with FP32 rounding
+// 1.1e-7 and 1e-7 (fits of the absolute error take a term less, but are off by 2e-6 of
+// a small score, which the table's gradient shows).  The exact form is off by about
+// 2^-22 of the cap.
 constexpr float kCapPoly = 1.25f, kCapSmall = 0.5f;
 struct Cap {
   float in, cap2;
@@ -170,19 +172,26 @@ __device__ __forceinline__ Cap make_cap(const ScoreArgs& s) {
 }
 // tanh(x) / x of two scores from x^2, |x| <= kCapPoly.
 __device__ __forceinline__ uint64_t tanh_over_x2(uint64_t z) {
-  constexpr float c[8] = {0.9999995231628418f,  -0.3333173394203186f,  0.13317924737930298f,  -0.0532919205725193f,
-                          0.02024945616722107f, -0.006540181580930948f, 0.0014795474708080292f, -0.0001641625858610496f};
-  uint64_t p = f2_pack(c[7], c[7]);
+  constexpr float c[9] = {1.f,
+                          -0.33333247900009155f,
+                          0.13331784307956696f,
+                          -0.053858835250139236f,
+                          0.021475467830896378f,
+                          -0.00804087147116661f,
+                          0.002523908857256174f,
+                          -0.0005492825293913484f,
+                          5.841381425852887e-05f};
+  uint64_t p = f2_pack(c[8], c[8]);
 #pragma unroll
-  for (int k = 6; k >= 0; --k) p = f2_fma(p, z, f2_pack(c[k], c[k]));
+  for (int k = 7; k >= 0; --k) p = f2_fma(p, z, f2_pack(c[k], c[k]));
   return p;
 }
 // t2 of two scores by s.cap_small.
 __device__ __forceinline__ uint64_t small_cap2(const ScoreArgs& s, uint64_t x) {
   const uint64_t z = f2_mul(x, x);
-  uint64_t p = f2_pack(s.cap_small[3], s.cap_small[3]);
+  uint64_t p = f2_pack(s.cap_small[4], s.cap_small[4]);
 #pragma unroll
-  for (int k = 2; k >= 0; --k) p = f2_fma(p, z, f2_pack(s.cap_small[k], s.cap_small[k]));
+  for (int k = 3; k >= 0; --k) p = f2_fma(p, z, f2_pack(s.cap_small[k], s.cap_small[k]));
   return f2_mul(x, p);
 }
 // The forms of the cap; any: also when there is none.
