@@ -277,7 +277,11 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
   const int r0 = blk * 128;
   const size_t bh = (size_t)b * NH + h;
   const int planes = B * NH;
-  pdl_wait();
+  // The dKV grid needs nothing of the dQ grid before it, and what both need is complete once the dQ grid's blocks have
+  // passed this wait, as they all have before they let the dKV grid start.  So its blocks fill the SMs that the dQ
+  // grid's last ones leave idle, and wait for the end of that grid at their own end, so that what follows finds both
+  // complete (8 heads of 128, 4093 tokens, causal: 222 -> 200 us; 8 sequences of 512 and 16 heads of 64: 80 -> 71 us).
+  if (MODE == kDQ) pdl_wait();
   const int n = score_len(valid_len, b, S), prefix = score_prefix(s, b);
   if (r0 >= n) {                                           // padding: zero gradients
     const int rows = min(128, S - r0);
@@ -287,6 +291,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
             make_uint4(0, 0, 0, 0);
     if (MODE == kDQ && partial)
       for (int k = tid; k < s.buckets; k += C::kThreads) partial[(bh * gridDim.x + blk) * s.buckets + k] = 0.f;
+    if (MODE == kDKV) pdl_wait();
     return;
   }
   // Blocks of columns that some row sees, as far as length and causality go.
@@ -667,6 +672,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
+  if (MODE == kDKV) pdl_wait();
 }
 
 // Per row i: -lse in units of log2 (-inf where the row sees nothing or is past
