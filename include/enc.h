@@ -121,7 +121,9 @@ typedef enum {
    * LayerNorm fusions, which need TMA). */
   ENC_OPT_TMA_STORE = 1,
   /* 1 (default): tcgen05 attention for size-64 heads on sequences longer than
-   * 64; 0: the mma.sync attention kernels for every length. */
+   * 64; 0: the mma.sync attention kernels for every length.  With modified
+   * scores (enc_scores) in FP16 mode, 0 takes the CUDA-core kernels of FP32 mode
+   * on FP16 tensors (the single-token step has one kernel only). */
   ENC_OPT_TC_ATTENTION = 2,
   /* 1 (default): split-K thread-block clusters for GEMMs whose tiles would
    * leave more than half the SMs idle; 0: never split K. */
