@@ -14,6 +14,13 @@
 //
 // The backward pass computes the scores twice instead of adding to dQ with
 // atomics, so that its results do not depend on the order of the blocks.
+//
+// Bound by shared memory: a step of 64 FMAs reads 8 float4 (and the second
+// products as many).  Measured, FP32, 12 heads of 64, 8 sequences of 512: forward
+// 169 us, 22 TF/s of the visible pairs' products (table 193 us), backward 509 us,
+// 18 TF/s (table 662 us).  Tiles are copied under the arithmetic of the ones
+// before (forward 186, backward 549 us without); for heads of 128 the forward's
+// third tile leaves one block to an SM (226 -> 234 us at 8 heads, 8 of 512).
 #include "scored.cuh"
 
 namespace enc {

@@ -29,6 +29,12 @@
 // masked.  In a masked block each row's visible keys are a bit set that its
 // thread has before S arrives; a warp whose rows see none of the block writes
 // P = 0 and leaves it.
+//
+// Measured, full lengths: 8 heads of 128, 37 sequences of 2048: 736 us, 864 TF/s
+// (slopes 887, table 812, cap 972 us); 16 heads of 64, 37 of 1024: 300 us, 529
+// TF/s (slopes 383, table 415, cap 442 us), where a block of 64 keys takes the three
+// tiles of an SM 2,570 cycles against 1,536 of exponentials alone: the rest is
+// loads from and stores to TMEM, the arithmetic of t and P, and waits.
 #include <cmath>
 #include <mutex>
 

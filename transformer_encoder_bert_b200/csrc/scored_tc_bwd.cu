@@ -31,6 +31,13 @@
 // shuffle a column the 32 values of a column go to 32 lanes by diagonal (see
 // row_chunk), each of which adds up the diagonals of its number in a fixed order;
 // a block whose distances all share a bucket only adds its values up.
+//
+// Measured, full lengths, counted as five products: 8 heads of 128, 37 sequences
+// of 2048: 2.66 ms, 598 TF/s (837 as the seven that run; table 2.83, cap 2.98
+// ms); 16 heads of 64, 37 of 1024: 1.13 ms, 353 TF/s (table 1.29, cap 1.37 ms).
+// What bounds a block is the chain S and dP -> a row's arithmetic -> the products
+// -> the next S and dP in the same columns; TMEM holds no third pair of buffers
+// beside the accumulators.
 #include "scored_tc.cuh"
 
 namespace enc {

@@ -31,6 +31,11 @@
 // shuffle that waits for the one before (a partial sum passed from lane to lane
 // along the diagonal took 64 dependent steps a row: 8,400 cycles an item against
 // 2,400 without the sums).
+//
+// Measured, 12 heads of 64: 64 sequences of 64 to 128 with a table 50 us against
+// 13 us of bytes; 148 full sequences of 128 58 us, 319 TF/s (table 78, cap 63 us).
+// Bound by an item's chain of latencies: with two items to an SM, 5,000 cycles
+// each with the table's sums, of which 630 are loads and stores at full bandwidth.
 #include "scored_tc.cuh"
 
 namespace enc {
