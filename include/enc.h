@@ -446,7 +446,9 @@ ENC_API enc_status enc_op_ffn2_ln(enc_t h, int layer, const void* u, const void*
  *   lse_i = log(sum over the visible keys of exp(t)).
  * A row that sees no key, and every row i >= n, has ctx = 0 and lse = -infinity.
  * (enc_op_attention without enc_set_scores computes rows i >= n like the others.)
- * What q, k, v and dctx hold in rows i >= n is never used.
+ * What q, k, v and dctx hold in rows i >= n is never used.  Rows below n hold
+ * finite values: a key that a mask hides from a query has the weight zero there,
+ * and zero times an infinity or a NaN is not zero.
  *
  * bucket(r) of a relative position r = j - i, with num_buckets and max_distance:
  *   bidirectional: m = num_buckets / 2, a = |r|, and m is added for r > 0;

@@ -32,9 +32,12 @@ __host__ __device__ __forceinline__ int score_bucket(const ScoreArgs& s, int rel
   const int exact = nb >> 1;
   int c = a;
   if (a >= exact) {
-    c = exact;                              // and how many bounds are <= a (the same ones for every lane)
+    c = nb - 1;                             // from the last bound on
+    if (a < s.reach) {
+      c = exact;                            // and how many bounds are <= a (the same ones for every lane)
 #pragma unroll 8
-    for (int k = 0; k < s.num_bounds; ++k) c += s.bounds[k] <= a;
+      for (int k = 0; k < s.num_bounds; ++k) c += s.bounds[k] <= a;
+    }
   }
   return c + (s.both && rel > 0 ? nb : 0);
 }

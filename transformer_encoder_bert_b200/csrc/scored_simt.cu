@@ -16,11 +16,13 @@
 // atomics, so that its results do not depend on the order of the blocks.
 //
 // Bound by shared memory: a step of 64 FMAs reads 8 float4 (and the second
-// products as many).  Measured, FP32, 12 heads of 64, 8 sequences of 512: forward
-// 169 us, 22 TF/s of the visible pairs' products (table 193 us), backward 509 us,
-// 18 TF/s (table 662 us).  Tiles are copied under the arithmetic of the ones
-// before (forward 186, backward 549 us without); for heads of 128 the forward's
-// third tile leaves one block to an SM (226 -> 234 us at 8 heads, 8 of 512).
+// products as many), and short sequences by the latency of a block's few tiles.
+// Measured, FP32, 12 heads of 64, 8 sequences of 512: forward 162 us, 23 TF/s of
+// the visible pairs' products (table 191 us), backward 441 us, 21 TF/s (table 582
+// us).  Tiles are copied under the arithmetic of the ones before (forward 186,
+// backward 549 us without), a last tile of at most 16 columns forms those alone (4
+// heads of 32, 16 sequences of 131: forward 22.6 -> 19.9 us), and the dK/dV grid
+// runs beside the dQ grid (the same sequences' backward 63.5 -> 43.1 us).
 #include "scored.cuh"
 
 namespace enc {
@@ -71,9 +73,9 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// acc[a][c] = A[4 ty + a] . B[tx + 16 c]
-template <int D>
-__device__ __forceinline__ void dot_tile(const float* A, const float* B, float (&acc)[4][4]) {
+// acc[a][c] = A[4 ty + a] . B[tx + 16 c] for c < N; zeros past that.
+template <int D, int N>
+__device__ __forceinline__ void dot_columns(const float* A, const float* B, float (&acc)[4][4]) {
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
 #pragma unroll
   for (int a = 0; a < 4; ++a)
@@ -81,21 +83,29 @@ __device__ __forceinline__ void dot_tile(const float* A, const float* B, float (
     for (int c = 0; c < 4; ++c) acc[a][c] = 0.f;
 #pragma unroll 4
   for (int k = 0; k < D; k += 4) {
-    float4 x[4], y[4];
+    float4 x[4], y[N];
 #pragma unroll
     for (int a = 0; a < 4; ++a) x[a] = *reinterpret_cast<const float4*>(A + (4 * ty + a) * (D + 4) + k);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const float4*>(B + (tx + 16 * c) * (D + 4) + k);
+    for (int c = 0; c < N; ++c) y[c] = *reinterpret_cast<const float4*>(B + (tx + 16 * c) * (D + 4) + k);
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < N; ++c) {
         acc[a][c] = fmaf(x[a].x, y[c].x, acc[a][c]);
         acc[a][c] = fmaf(x[a].y, y[c].y, acc[a][c]);
         acc[a][c] = fmaf(x[a].z, y[c].z, acc[a][c]);
         acc[a][c] = fmaf(x[a].w, y[c].w, acc[a][c]);
       }
   }
+}
+// The same for the first `live` columns of a tile (the others are hidden; a last tile of at most 16 is common).
+template <int D>
+__device__ __forceinline__ void dot_tile(const float* A, const float* B, int live, float (&acc)[4][4]) {
+  if (live <= 16)
+    dot_columns<D, 1>(A, B, acc);
+  else
+    dot_columns<D, 4>(A, B, acc);
 }
 
 // Column of a thread's e-th output element (D / 16 of them).
@@ -105,12 +115,12 @@ __device__ __forceinline__ int out_col(int e) {
   return D == 32 ? tx * 2 + e : (e / 4) * 64 + tx * 4 + e % 4;
 }
 
-// out[a][e] += sum_k P[4 ty + a][k] B[k][out_col(e)]
+// out[a][e] += sum over k < live of P[4 ty + a][k] B[k][out_col(e)] (P = 0 from there to a multiple of 4)
 template <int D>
-__device__ __forceinline__ void accumulate(const float* P, const float* B, float (&out)[4][D / 16]) {
+__device__ __forceinline__ void accumulate(const float* P, const float* B, int live, float (&out)[4][D / 16]) {
   const int ty = threadIdx.x >> 4;
 #pragma unroll 2
-  for (int k = 0; k < kT; k += 4) {
+  for (int k = 0; k < live; k += 4) {
     float p[4][4];
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
@@ -158,11 +168,11 @@ __device__ __forceinline__ void fill_docs(int* dst, const ScoreArgs& s, int b, i
 }
 
 // u in units of log2, and 1 - tanh^2 (1 without a cap).
-__device__ __forceinline__ float capped2(const ScoreArgs& s, float dot, float& slope) {
+__device__ __forceinline__ float capped2(const ScoreArgs& s, float inv_cap, float dot, float& slope) {
   const float u = dot * s.scale;
   slope = 1.f;
   if (s.cap <= 0.f) return u * kLog2e;
-  const float th = tanhf(u / s.cap);
+  const float th = tanhf(u * inv_cap);
   slope = fmaf(-th, th, 1.f);
   return s.cap * th * kLog2e;
 }
@@ -185,25 +195,26 @@ __global__ void __launch_bounds__(kThreads)
   const int n = score_len(valid_len, b, S), prefix = score_prefix(s, b);
   const size_t head = (size_t)S * D, part = (size_t)B * NH * head;
   const T* Qg = qkv + ((size_t)b * NH + h) * head;
-  const float slope = s.slopes ? s.slopes[h] : 0.f;
+  const float slope = s.slopes ? s.slopes[h] : 0.f, inv_cap = s.cap > 0.f ? 1.f / s.cap : 0.f;
   float out[4][D / 16] = {};
   float m[4], l[4] = {};
   for (int a = 0; a < 4; ++a) m[a] = -INFINITY;
   const int rows = min(kT, n - q0);      // valid queries of the tile
   const int klim = rows > 0 ? score_jlim(s, q0 + rows - 1, n, prefix) : 0;
   load_tile<T, D>(Qs, Qg, q0, n, D);
+  load_tile<T, D>(Ks, Qg + part, 0, n, D);
+  load_tile<T, D>(Vs, Qg + 2 * part, 0, n, D);
   fill_docs(ti->row_doc, s, b, S, q0);
   load_column(s, ti->column, NH, h, threadIdx.x, kThreads);
   __syncthreads();
-  load_tile<T, D>(Ks, Qg + part, 0, n, D);
-  load_tile<T, D>(Vs, Qg + 2 * part, 0, n, D);
   for (int j0 = 0; j0 < klim; j0 += kT) {
     fill_bias(ti, s, slope, j0 - q0);
     fill_docs(ti->col_doc, s, b, S, j0);
     wait_copies<1>();
     __syncthreads();
+    const int live = min(kT, klim - j0);
     float acc[4][4];
-    dot_tile<D>(Qs, Ks, acc);
+    dot_tile<D>(Qs, Ks, live, acc);
     __syncthreads();
     load_tile<T, D>(Ks, Qg + part, j0 + kT, n, D);         // the next tile's, under the softmax
 #pragma unroll
@@ -215,7 +226,7 @@ __global__ void __launch_bounds__(kThreads)
       for (int c = 0; c < 4; ++c) {
         const int col = tx + 16 * c, j = j0 + col;
         float unused;
-        const float t = capped2(s, acc[a][c], unused) + ti->bias2[col - r + kT - 1];
+        const float t = capped2(s, inv_cap, acc[a][c], unused) + ti->bias2[col - r + kT - 1];
         acc[a][c] = j < jlim && (!s.docs || ti->row_doc[r] == ti->col_doc[col]) ? t : -INFINITY;
         mx = fmaxf(mx, acc[a][c]);
       }
@@ -239,7 +250,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     wait_copies<1>();
     __syncthreads();
-    accumulate<D>(Ps, Vs, out);
+    accumulate<D>(Ps, Vs, live, out);
     __syncthreads();
     load_tile<T, D>(Vs, Qg + 2 * part, j0 + kT, n, D);
   }
@@ -285,12 +296,15 @@ __global__ void __launch_bounds__(kThreads)
   const size_t head = (size_t)S * D, part = (size_t)B * NH * head, bh = (size_t)b * NH + h;
   const T* Qg = qkv + bh * head;
   const int H = NH * D;
-  const float slope = s.slopes ? s.slopes[h] : 0.f;
+  const float slope = s.slopes ? s.slopes[h] : 0.f, inv_cap = s.cap > 0.f ? 1.f / s.cap : 0.f;
   float out[4][D / 16] = {};
+  const bool busy = q0 + 8 * (ty >> 1) < n;                // some row of the warp's eight is valid
   const int rows = min(kT, n - q0);
   const int klim = rows > 0 ? score_jlim(s, q0 + rows - 1, n, prefix) : 0;
   load_tile<T, D>(Qs, Qg, q0, n, D);
   load_tile<T, D>(dOs, dctx + (size_t)b * S * H + h * D, q0, n, H);
+  load_tile<T, D>(Ks, Qg + part, 0, n, D);
+  load_tile<T, D>(Vs, Qg + 2 * part, 0, n, D);
   fill_docs(ti->row_doc, s, b, S, q0);
   load_column(s, ti->column, NH, h, threadIdx.x, kThreads);
   __syncthreads();
@@ -304,16 +318,17 @@ __global__ void __launch_bounds__(kThreads)
     if (lse2[a] == -INFINITY) lse2[a] = INFINITY;
     dsum[a] = i < n ? rowsum[bh * S + i] : 0.f;
   }
-  load_tile<T, D>(Ks, Qg + part, 0, n, D);
-  load_tile<T, D>(Vs, Qg + 2 * part, 0, n, D);
   for (int j0 = 0; j0 < klim; j0 += kT) {
     fill_bias(ti, s, slope, j0 - q0);
     fill_docs(ti->col_doc, s, b, S, j0);
     wait_copies<0>();
     __syncthreads();
-    float acc[4][4], dp[4][4];
-    dot_tile<D>(Qs, Ks, acc);
-    dot_tile<D>(dOs, Vs, dp);
+    const int live = min(kT, klim - j0);
+    float acc[4][4] = {}, dp[4][4] = {};
+    if (busy) {
+      dot_tile<D>(Qs, Ks, live, acc);
+      dot_tile<D>(dOs, Vs, live, dp);
+    }
     __syncthreads();
     load_tile<T, D>(Vs, Qg + 2 * part, j0 + kT, n, D);     // the next tile's
 #pragma unroll
@@ -324,7 +339,7 @@ __global__ void __launch_bounds__(kThreads)
       for (int c = 0; c < 4; ++c) {
         const int col = tx + 16 * c, j = j0 + col;
         float sl;
-        const float t = capped2(s, acc[a][c], sl) + ti->bias2[col - r + kT - 1];
+        const float t = capped2(s, inv_cap, acc[a][c], sl) + ti->bias2[col - r + kT - 1];
         const bool see = j < jlim && (!s.docs || ti->row_doc[r] == ti->col_doc[col]);
         const float dt = see ? prob2(t, lse2[a]) * (dp[a][c] - dsum[a]) : 0.f;
         Ps[r * kPs + col] = dt;
@@ -354,7 +369,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int c = 0; c < 4; ++c) Ps[(4 * ty + a) * kPs + tx + 16 * c] = acc[a][c];
     }
     __syncthreads();
-    accumulate<D>(Ps, Ks, out);
+    if (busy) accumulate<D>(Ps, Ks, live, out);
     __syncthreads();
     load_tile<T, D>(Ks, Qg + part, j0 + kT, n, D);
   }
@@ -407,7 +422,8 @@ __global__ void __launch_bounds__(kThreads)
   float* Ps = dOs + kT * (D + 4);
   TileInfo* ti = reinterpret_cast<TileInfo*>(Ps + kT * kPs);
   __shared__ float lse2[kT], dsum[kT];
-  pdl_wait();
+  // The dQ grid before it makes nothing that this one reads, and its blocks have all passed their wait before they let
+  // this grid start: it runs beside that grid, and waits for it at the end so that what follows finds both complete.
   pdl_trigger();
   const int b = blockIdx.z, h = blockIdx.y, j0 = blockIdx.x * kT;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -415,17 +431,18 @@ __global__ void __launch_bounds__(kThreads)
   const size_t head = (size_t)S * D, part = (size_t)B * NH * head, bh = (size_t)b * NH + h;
   const T* Qg = qkv + bh * head;
   const int H = NH * D;
-  const float slope = s.slopes ? s.slopes[h] : 0.f;
+  const float slope = s.slopes ? s.slopes[h] : 0.f, inv_cap = s.cap > 0.f ? 1.f / s.cap : 0.f;
   float dk[4][D / 16] = {}, dv[4][D / 16] = {};
   load_tile<T, D>(Ks, Qg + part, j0, n, D);
   load_tile<T, D>(Vs, Qg + 2 * part, j0, n, D);
-  fill_docs(ti->row_doc, s, b, S, j0);
-  load_column(s, ti->column, NH, h, threadIdx.x, kThreads);
-  __syncthreads();
+  const bool busy = j0 + 8 * (ty >> 1) < n;                // some row of the warp's eight is valid
   const int qfirst = j0 < n ? score_ilow(s, j0, prefix) / kT * kT : n;
   const T* dOg = dctx + (size_t)b * S * H + h * D;
   load_tile<T, D>(Qs, Qg, qfirst, n, D);
   load_tile<T, D>(dOs, dOg, qfirst, n, H);
+  fill_docs(ti->row_doc, s, b, S, j0);
+  load_column(s, ti->column, NH, h, threadIdx.x, kThreads);
+  __syncthreads();
   for (int q0 = qfirst; q0 < n; q0 += kT) {
     fill_bias(ti, s, slope, j0 - q0);
     fill_docs(ti->col_doc, s, b, S, q0);
@@ -437,18 +454,21 @@ __global__ void __launch_bounds__(kThreads)
     }
     wait_copies<0>();
     __syncthreads();
+    const int live = min(kT, n - q0);
     float acc[4][4], dp[4][4];
-    dot_tile<D>(Ks, Qs, acc);            // rows are keys, columns queries
-    dot_tile<D>(Vs, dOs, dp);
+    if (busy) {
+      dot_tile<D>(Ks, Qs, live, acc);    // rows are keys, columns queries
+      dot_tile<D>(Vs, dOs, live, dp);
+    }
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
+    for (int a = 0; a < 4 && busy; ++a) {
       const int r = 4 * ty + a, j = j0 + r;
       const int ilow = score_ilow(s, j, prefix);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int col = tx + 16 * c, i = q0 + col;
         float sl;
-        const float t = capped2(s, acc[a][c], sl) + ti->bias2[r - col + kT - 1];
+        const float t = capped2(s, inv_cap, acc[a][c], sl) + ti->bias2[r - col + kT - 1];
         const bool see = j < n && i >= ilow && i < n && (!s.docs || ti->row_doc[r] == ti->col_doc[col]);
         const float p = see ? prob2(t, lse2[col]) : 0.f;
         Ps[r * kPs + col] = p;
@@ -456,15 +476,15 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     __syncthreads();
-    accumulate<D>(Ps, dOs, dv);
+    if (busy) accumulate<D>(Ps, dOs, live, dv);
     __syncthreads();
     load_tile<T, D>(dOs, dOg, q0 + kT, n, H);              // the next tile's
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < 4 && busy; ++a)
 #pragma unroll
       for (int c = 0; c < 4; ++c) Ps[(4 * ty + a) * kPs + tx + 16 * c] = acc[a][c];
     __syncthreads();
-    accumulate<D>(Ps, Qs, dk);
+    if (busy) accumulate<D>(Ps, Qs, live, dk);
     __syncthreads();
     load_tile<T, D>(Qs, Qg, q0 + kT, n, D);
   }
@@ -479,6 +499,7 @@ __global__ void __launch_bounds__(kThreads)
       put(dqkv + 2 * part + (bh * S + j) * D + out_col<D>(e), dv[a][e]);
     }
   }
+  pdl_wait();
 }
 
 // One warp per (token, head).
