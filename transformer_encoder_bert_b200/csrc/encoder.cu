@@ -560,11 +560,11 @@ enc_status make_scores(enc_handle* h, const enc_scores* p, enc::ScoreArgs& s) {
   return ENC_OK;
 }
 
-// Scratch of the backward pass: the row statistics (of either kernels), then
+// Scratch of the backward pass: the row statistics and the counter (of either kernels), then
 // each query block's sums of the table's gradient (for the smallest block and
 // the largest table, or the sums by distance).
 size_t scored_rows_bytes(const enc_handle* h, int batch, int seq) {
-  return align_up(std::max((size_t)batch * seq * h->nh * 4,
+  return align_up(std::max(((size_t)batch * seq * h->nh + 1) * 4,
                            enc::scored_backward_tc_scratch(enc::ScoredShape{batch, seq, h->nh, h->d})), 256);
 }
 size_t scored_ws_bytes(const enc_handle* h, int batch, int seq) {
@@ -1628,10 +1628,11 @@ enc_status enc_op_scored_attention_backward(enc_t h, const enc_scores* scores, c
   } else {
     const bool half = h->dtype == ENC_FP16;
     float* rowsum = static_cast<float*>(h->scored_ws);
+    unsigned* counter = reinterpret_cast<unsigned*>(rowsum + (size_t)batch * seq * h->nh);
     rows = enc::kScoredSimtRows;
-    e = enc::launch_scored_rowsum(ctx, dctx, valid_len, rowsum, sh, half, st);
+    e = enc::launch_scored_rowsum(ctx, dctx, valid_len, rowsum, counter, sh, half, st);
     if (e == cudaSuccess)
-      e = enc::launch_scored_backward_simt(a, qkv, valid_len, dctx, lse, rowsum, dqkv, partial, sh, half, st);
+      e = enc::launch_scored_backward_simt(a, qkv, valid_len, dctx, lse, rowsum, counter, dqkv, partial, sh, half, st);
     if (e == cudaSuccess) h->launches += 3;
   }
   if (e != cudaSuccess) return cuda_fail(e, "scored attention backward launch");

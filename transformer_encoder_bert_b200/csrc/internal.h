@@ -244,15 +244,16 @@ cudaError_t launch_scored_tc(const ScoreArgs& s, const __half* qkv, const int32_
 constexpr int kScoredShort = 128;
 cudaError_t launch_scored_tc_short(const ScoreArgs& s, const __half* qkv, const int32_t* valid_len, __half* ctx,
                                    float* lse, const ScoredShape& sh, int* status, int num_sms, cudaStream_t stream);
-// Row sums D_i = dctx_i . ctx_i (0 for i >= n) -> rowsum [B, nh, S].
+// Row sums D_i = dctx_i . ctx_i (0 for i >= n) -> rowsum [B, nh, S]; sets the counter (count_block in scored.cuh) to 0.
 cudaError_t launch_scored_rowsum(const void* ctx, const void* dctx, const int32_t* valid_len, float* rowsum,
-                                 const ScoredShape& sh, bool half, cudaStream_t stream);
+                                 unsigned* counter, const ScoredShape& sh, bool half, cudaStream_t stream);
 // Backward: dqkv [3, B, nh, S, d]; partial [B, nh, ceil(S / rows of a block), buckets] gets each query
-// block's sums of the table's gradient (nullptr: no table gradient).
+// block's sums of the table's gradient (nullptr: no table gradient); counter: the one that launch_scored_rowsum set.
 constexpr int kScoredSimtRows = 64;
 cudaError_t launch_scored_backward_simt(const ScoreArgs& s, const void* qkv, const int32_t* valid_len,
-                                        const void* dctx, const float* lse, const float* rowsum, void* dqkv,
-                                        float* partial, const ScoredShape& sh, bool half, cudaStream_t stream);
+                                        const void* dctx, const float* lse, const float* rowsum, unsigned* counter,
+                                        void* dqkv, float* partial, const ScoredShape& sh, bool half,
+                                        cudaStream_t stream);
 // The same on the tensor cores, FP16 (scored_tc_bwd.cu), the row sums included; partial has query blocks of
 // kScoredTcRows; scratch: scored_backward_tc_scratch bytes.
 constexpr int kScoredTcRows = 128;

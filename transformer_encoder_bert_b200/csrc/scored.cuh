@@ -82,6 +82,24 @@ __device__ __forceinline__ int score_ilow(const ScoreArgs& s, int j, int prefix)
   return s.causal && j >= prefix ? j : 0;
 }
 
+// A grid that starts before the one ahead of it has ended (dK/dV beside dQ) reads what a still earlier grid wrote (the
+// row statistics).  Its own griddepcontrol.wait would make that visible, but would also wait for the whole dQ grid.  So
+// every dQ block, once past its wait, adds one to a counter with release order before it lets the next grid start, and
+// a dK/dV block that acquires the full count sees all that the dQ blocks saw.  One that does not (no block has to wait
+// for another one here) takes its griddepcontrol.wait at its start instead of its end.  The statistics grid, which
+// starts after every earlier reader has ended, sets the counter to zero.
+__device__ __forceinline__ void count_block(unsigned* counter) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
+}
+// Called by every thread of a block; a barrier.  The bulk copies that follow read through the asynchronous proxy.
+__device__ __forceinline__ bool all_blocks_counted(const unsigned* counter, unsigned blocks) {
+  unsigned v = 0;
+  if (threadIdx.x == 0) asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+  const bool all = __syncthreads_or(threadIdx.x == 0 && v == blocks);
+  asm volatile("fence.proxy.async;" ::: "memory");
+  return all;
+}
+
 // Persistent CTAs over `items`: CTA c of `ctas` takes [first_item(c), first_item(c + 1)).
 __host__ __device__ __forceinline__ int first_item(int c, int items, int ctas) {
   return static_cast<int>(static_cast<long long>(items) * c / ctas);

@@ -275,8 +275,8 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
     scored_dq_kernel(const __grid_constant__ ScoreArgs s, const T* __restrict__ qkv,
                      const int32_t* __restrict__ valid_len, const T* __restrict__ dctx, const float* __restrict__ lse,
-                     const float* __restrict__ rowsum, T* __restrict__ dq, float* __restrict__ partial, int B, int S,
-                     int NH) {
+                     const float* __restrict__ rowsum, unsigned* __restrict__ counter, T* __restrict__ dq,
+                     float* __restrict__ partial, int B, int S, int NH) {
   extern __shared__ __align__(16) float smem[];
   float* Qs = smem;
   float* dOs = Qs + kT * (D + 4);
@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kThreads)
   float far_left = 0.f, far_right = 0.f;
   __shared__ float far[2][2 * kT];
   pdl_wait();
+  if (threadIdx.x == 0) count_block(counter);
   pdl_trigger();
   const int b = blockIdx.z, h = blockIdx.y, qb = gridDim.x - 1 - blockIdx.x, q0 = qb * kT;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -411,9 +412,9 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-    scored_dkv_kernel(const __grid_constant__ ScoreArgs s, const T* __restrict__ qkv,
-                      const int32_t* __restrict__ valid_len, const T* __restrict__ dctx, const float* __restrict__ lse,
-                      const float* __restrict__ rowsum, T* __restrict__ dqkv, int B, int S, int NH) {
+    scored_dkv_kernel(const __grid_constant__ ScoreArgs s, const T* qkv, const int32_t* valid_len, const T* dctx,
+                      const float* lse, const float* rowsum, const unsigned* counter, T* dqkv, int B, int S, int NH) {
+  // (Pointers without __restrict__: no load may go through the read-only path, or move above the acquire.)
   extern __shared__ __align__(16) float smem[];
   float* Ks = smem;
   float* Vs = Ks + kT * (D + 4);
@@ -422,8 +423,9 @@ __global__ void __launch_bounds__(kThreads)
   float* Ps = dOs + kT * (D + 4);
   TileInfo* ti = reinterpret_cast<TileInfo*>(Ps + kT * kPs);
   __shared__ float lse2[kT], dsum[kT];
-  // The dQ grid before it makes nothing that this one reads, and its blocks have all passed their wait before they let
-  // this grid start: it runs beside that grid, and waits for it at the end so that what follows finds both complete.
+  // The dQ grid before it makes nothing that this one reads: it runs beside that grid (all_blocks_counted has how it
+  // sees what both read), and waits for it at the end so that what follows finds both complete.
+  if (!all_blocks_counted(counter, gridDim.x * gridDim.y * gridDim.z)) pdl_wait();
   pdl_trigger();
   const int b = blockIdx.z, h = blockIdx.y, j0 = blockIdx.x * kT;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -506,9 +508,10 @@ __global__ void __launch_bounds__(kThreads)
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
     scored_rowsum_kernel(const T* __restrict__ ctx, const T* __restrict__ dctx, const int32_t* __restrict__ valid_len,
-                         float* __restrict__ rowsum, int B, int S, int NH) {
+                         float* __restrict__ rowsum, unsigned* __restrict__ counter, int B, int S, int NH) {
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
   const size_t item = (size_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (item >= (size_t)B * S * NH) return;
@@ -593,7 +596,8 @@ cudaError_t fwd_d(const ScoreArgs& s, const void* qkv, const int32_t* vl, void* 
 
 template <typename T, int D>
 cudaError_t bwd_d(const ScoreArgs& s, const void* qkv, const int32_t* vl, const void* dctx, const float* lse,
-                  const float* rowsum, void* dqkv, float* partial, const ScoredShape& sh, cudaStream_t stream) {
+                  const float* rowsum, unsigned* counter, void* dqkv, float* partial, const ScoredShape& sh,
+                  cudaStream_t stream) {
   const size_t dq_smem = smem_bytes<D>(4) + (partial ? (2 * s.reach + 1) * sizeof(float) : 0);
   static const cudaError_t attr1 =
       allow_smem(scored_dq_kernel<T, D>, smem_bytes<D>(4) + (2 * kMaxScoreDistance + 1) * sizeof(float));
@@ -602,20 +606,20 @@ cudaError_t bwd_d(const ScoreArgs& s, const void* qkv, const int32_t* vl, const 
   if (attr2 != cudaSuccess) return attr2;
   const dim3 grid((sh.seq + kT - 1) / kT, sh.head_num, sh.batch);
   cudaError_t e = launch_kernel(scored_dq_kernel<T, D>, grid, dim3(kThreads), dq_smem, stream, nullptr, 0, s,
-                                static_cast<const T*>(qkv), vl, static_cast<const T*>(dctx), lse, rowsum,
+                                static_cast<const T*>(qkv), vl, static_cast<const T*>(dctx), lse, rowsum, counter,
                                 static_cast<T*>(dqkv), partial, sh.batch, sh.seq, sh.head_num);
   if (e != cudaSuccess) return e;
   return launch_kernel(scored_dkv_kernel<T, D>, grid, dim3(kThreads), smem_bytes<D>(4), stream, nullptr, 0, s,
-                       static_cast<const T*>(qkv), vl, static_cast<const T*>(dctx), lse, rowsum,
+                       static_cast<const T*>(qkv), vl, static_cast<const T*>(dctx), lse, rowsum, counter,
                        static_cast<T*>(dqkv), sh.batch, sh.seq, sh.head_num);
 }
 
 template <typename T, int D>
-cudaError_t rowsum_d(const void* ctx, const void* dctx, const int32_t* vl, float* rowsum, const ScoredShape& sh,
-                     cudaStream_t stream) {
+cudaError_t rowsum_d(const void* ctx, const void* dctx, const int32_t* vl, float* rowsum, unsigned* counter,
+                     const ScoredShape& sh, cudaStream_t stream) {
   const size_t items = (size_t)sh.batch * sh.seq * sh.head_num;
   return launch_kernel(scored_rowsum_kernel<T, D>, dim3((unsigned)((items + 7) / 8)), dim3(kThreads), 0, stream,
-                       nullptr, 0, static_cast<const T*>(ctx), static_cast<const T*>(dctx), vl, rowsum, sh.batch,
+                       nullptr, 0, static_cast<const T*>(ctx), static_cast<const T*>(dctx), vl, rowsum, counter, sh.batch,
                        sh.seq, sh.head_num);
 }
 
@@ -640,17 +644,19 @@ cudaError_t launch_scored_simt(const ScoreArgs& s, const void* qkv, const int32_
 }
 
 cudaError_t launch_scored_rowsum(const void* ctx, const void* dctx, const int32_t* valid_len, float* rowsum,
-                                 const ScoredShape& sh, bool half, cudaStream_t stream) {
+                                 unsigned* counter, const ScoredShape& sh, bool half, cudaStream_t stream) {
   return dispatch(half, sh.size_per_head, [&](auto t, auto d) {
-    return rowsum_d<decltype(t), decltype(d)::value>(ctx, dctx, valid_len, rowsum, sh, stream);
+    return rowsum_d<decltype(t), decltype(d)::value>(ctx, dctx, valid_len, rowsum, counter, sh, stream);
   });
 }
 
 cudaError_t launch_scored_backward_simt(const ScoreArgs& s, const void* qkv, const int32_t* valid_len,
-                                        const void* dctx, const float* lse, const float* rowsum, void* dqkv,
-                                        float* partial, const ScoredShape& sh, bool half, cudaStream_t stream) {
+                                        const void* dctx, const float* lse, const float* rowsum, unsigned* counter,
+                                        void* dqkv, float* partial, const ScoredShape& sh, bool half,
+                                        cudaStream_t stream) {
   return dispatch(half, sh.size_per_head, [&](auto t, auto d) {
-    return bwd_d<decltype(t), decltype(d)::value>(s, qkv, valid_len, dctx, lse, rowsum, dqkv, partial, sh, stream);
+    return bwd_d<decltype(t), decltype(d)::value>(s, qkv, valid_len, dctx, lse, rowsum, counter, dqkv, partial, sh,
+                                                        stream);
   });
 }
 

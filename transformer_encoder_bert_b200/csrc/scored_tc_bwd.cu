@@ -257,9 +257,9 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
     scored_tc_bwd_kernel(const __grid_constant__ ScoreArgs s, const __grid_constant__ CUtensorMap tm_a0,
                          const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b0,
                          const __grid_constant__ CUtensorMap tm_b1, const __grid_constant__ CUtensorMap tm_out,
-                         const int32_t* __restrict__ valid_len, const float* __restrict__ rows2, int Sp,
-                         const float* __restrict__ norms, float* __restrict__ partial, __half* __restrict__ dqkv, int B,
-                         int S, int NH, int* __restrict__ status) {
+                         const int32_t* valid_len, const float* rows2, int Sp, const float* norms, unsigned* counter,
+                         float* partial, __half* dqkv, int B, int S, int NH, int* status) {
+  // (Pointers without __restrict__: no load may go through the read-only path, or move above the acquire.)
   using C = BCfg<D, MODE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -284,11 +284,16 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
   const int r0 = blk * 128;
   const size_t bh = (size_t)b * NH + h;
   const int planes = B * NH;
-  // The dKV grid needs nothing of the dQ grid before it, and what both need is complete once the dQ grid's blocks have
-  // passed this wait, as they all have before they let the dKV grid start.  So its blocks fill the SMs that the dQ
-  // grid's last ones leave idle, and wait for the end of that grid at their own end, so that what follows finds both
-  // complete (8 heads of 128, 4093 tokens, causal: 222 -> 200 us; 8 sequences of 512 and 16 heads of 64: 80 -> 71 us).
-  if (MODE == kDQ) pdl_wait();
+  // The dKV grid needs nothing of the dQ grid before it (all_blocks_counted has how it sees what both read).  So its
+  // blocks fill the SMs that the dQ grid's last ones leave idle, and wait for the end of that grid at their own end, so
+  // that what follows finds both complete (8 heads of 128, 4093 tokens, causal: 222 -> 200 us; 8 sequences of 512 and
+  // 16 heads of 64: 80 -> 71 us).
+  if (MODE == kDQ) {
+    pdl_wait();
+    if (tid == 0) count_block(counter);
+  } else if (!all_blocks_counted(counter, gridDim.x * gridDim.y * gridDim.z)) {
+    pdl_wait();
+  }
   const int n = score_len(valid_len, b, S), prefix = score_prefix(s, b);
   if (r0 >= n) {                                           // padding: zero gradients
     const int rows = min(128, S - r0);
@@ -691,12 +696,13 @@ __global__ void __launch_bounds__(kStatThreads)
     scored_stats_kernel(const __half* __restrict__ qkv, const __half* __restrict__ ctx,
                         const __half* __restrict__ dctx, const float* __restrict__ lse,
                         const int32_t* __restrict__ valid_len, float* __restrict__ rows2, float* __restrict__ norms,
-                        int B, int S, int Sp, int NH) {
+                        unsigned* __restrict__ counter, int B, int S, int Sp, int NH) {
   constexpr int kLanes = D / 8, kRows = kStatThreads / kLanes;
   __shared__ float wo[kStatThreads / 32], wv[kStatThreads / 32];
   pdl_wait();
   pdl_trigger();
   const int h = blockIdx.y, b = blockIdx.z, r0 = blockIdx.x * 128;
+  if (blockIdx.x + h + b == 0 && threadIdx.x == 0) *counter = 0;
   const size_t bh = (size_t)b * NH + h, planes = (size_t)B * NH;
   const int n = score_len(valid_len, b, S);
   const int gl = threadIdx.x % kLanes;
@@ -764,15 +770,15 @@ __global__ void __launch_bounds__(kStatThreads)
 template <int D, int MODE>
 cudaError_t launch_mode(const ScoreArgs& s, const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0,
                         const CUtensorMap& b1, const CUtensorMap& out, const int32_t* vl, const float* rows2, int Sp,
-                        const float* norms, float* partial, __half* dqkv, const ScoredShape& sh, int* status,
-                        cudaStream_t stream) {
+                        const float* norms, unsigned* counter, float* partial, __half* dqkv, const ScoredShape& sh,
+                        int* status, cudaStream_t stream) {
   using C = BCfg<D, MODE>;
   static const cudaError_t attr = cudaFuncSetAttribute(scored_tc_bwd_kernel<D, MODE>,
                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (attr != cudaSuccess) return attr;
   const dim3 grid((sh.seq + 127) / 128, sh.head_num, sh.batch);
   return launch_kernel(scored_tc_bwd_kernel<D, MODE>, grid, dim3(C::kThreads), C::smem(s, sh.seq, partial != nullptr),
-                       stream, nullptr, 0, s, a0, a1, b0, b1, out, vl, rows2, Sp, norms, partial, dqkv, sh.batch,
+                       stream, nullptr, 0, s, a0, a1, b0, b1, out, vl, rows2, Sp, norms, counter, partial, dqkv, sh.batch,
                        sh.seq, sh.head_num, status);
 }
 
@@ -784,9 +790,10 @@ cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, c
   const int Sp = (sh.seq + 127) / 128 * 128;
   float* rows2 = static_cast<float*>(scratch);
   float* norms = rows2 + 2 * planes * Sp;
+  unsigned* counter = reinterpret_cast<unsigned*>(norms + 2 * planes * (Sp / 128));
   const dim3 grid(Sp / 128, sh.head_num, sh.batch);
   cudaError_t e = launch_kernel(scored_stats_kernel<D>, grid, dim3(kStatThreads), 0, stream, nullptr, 0, qkv, ctx, dctx,
-                                lse, vl, rows2, norms, sh.batch, sh.seq, Sp, sh.head_num);
+                                lse, vl, rows2, norms, counter, sh.batch, sh.seq, Sp, sh.head_num);
   if (e != cudaSuccess) return e;
   CUtensorMap rows, cols, drows, dcols, out;
   if (!encode_operand_map(&rows, qkv, D, sh.seq, 3 * planes, 64, 128) ||
@@ -795,9 +802,11 @@ cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, c
       !encode_operand_map(&dcols, dctx, H, sh.seq, sh.batch, 64, kBN) ||
       !encode_operand_map(&out, dqkv, D, sh.seq, 3 * planes, D < 64 ? D : 64, 32))
     return cudaErrorInvalidValue;
-  e = launch_mode<D, kDQ>(s, rows, drows, cols, cols, out, vl, rows2, Sp, norms, partial, dqkv, sh, status, stream);
+  e = launch_mode<D, kDQ>(s, rows, drows, cols, cols, out, vl, rows2, Sp, norms, counter, partial, dqkv, sh, status,
+                           stream);
   if (e != cudaSuccess) return e;
-  return launch_mode<D, kDKV>(s, rows, rows, cols, dcols, out, vl, rows2, Sp, norms, nullptr, dqkv, sh, status, stream);
+  return launch_mode<D, kDKV>(s, rows, rows, cols, dcols, out, vl, rows2, Sp, norms, counter, nullptr, dqkv, sh, status,
+                             stream);
 }
 
 }  // namespace
@@ -805,7 +814,7 @@ cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, c
 
 size_t scored_backward_tc_scratch(const ScoredShape& sh) {
   const size_t planes = (size_t)sh.batch * sh.head_num, blocks = ((size_t)sh.seq + 127) / 128;
-  return planes * blocks * (2 * 128 + 2) * 4;
+  return (planes * blocks * (2 * 128 + 2) + 1) * 4;
 }
 
 cudaError_t launch_scored_backward_tc(const ScoreArgs& s, const __half* qkv, const int32_t* valid_len,
