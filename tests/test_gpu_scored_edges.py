@@ -48,3 +48,41 @@ def test_inputs_that_alternate_through_one_handle(pdl, nh, d, s, mode):
     assert enc.device_status() == 0
     for i, x in zip(order, got):
         assert torch.equal(want[i][0], x[0]) and torch.equal(want[i][1], x[1])
+
+
+# ---------------------------------------------------------------- the cap
+def equal_scores(mode, s, cap, u, valid, outlier=False):
+    """A case whose every score is u (the products are exact), whose v grows along the keys and whose dctx is 1, so
+    that all of a far bucket's dT have one sign.  outlier: key 3's score is -2.5 caps instead."""
+    d, nh, b = 64, 2, len(valid)
+    c = Case("table", mode, b, nh, s, d, seed=30, valid=valid)
+    c.spec.cap, c.spec.scale, c.spec.max_distance = float(cap), 0.125, s - 10
+    c.spec.table = np.zeros((16, nh), np.float32)
+    c.qkv[:2] = 0
+    c.qkv[:2, ..., 0] = np.sqrt(u / c.spec.scale)
+    c.qkv[2] = (np.arange(1, s + 1) / s)[None, None, :, None]
+    if outlier:
+        c.qkv[0, ..., 1] = 100
+        c.qkv[1, :, :, 3, 1] = -2.5 * cap / c.spec.scale / 100
+    c.dctx[:] = 1
+    return c
+
+
+# A score of 0.4 steps (2^-23) of the cap: a tanh that is only good to such a step returns 0 for it, and moves the
+# score by 4.8e-4 at a cap of 1e4.  Without that, t, lse (below 8), their forms in log2 and the exponential are off by
+# a few 2^-24 of 8, below 2^-19 in all, and sums of s terms by s 2^-24 more.
+@pytest.mark.parametrize("mode", ["fp16", "fp16-simt", "fp32"])
+@pytest.mark.parametrize("cap", [30.0, 1e4])
+@pytest.mark.parametrize("s,valid", [(100, [100, 97, 70]), (150, [150, 129, 141]), (300, [300, 257, 290])], ids=str)
+def test_ragged_tiles_keep_small_scores(s, valid, cap, mode):
+    """The table's gradient where tiles end in padding: P is rebuilt from the scores that the forward had."""
+    c = equal_scores(mode, s, cap, 0.4 * 2.0 ** -23 * cap, valid)
+    ctx, lse = c.forward()
+    _, dtable = c.backward(ctx, lse)
+    _, ref, (p, size, _) = SO.backward(c.spec, c.qkv, c.valid, c.shaped(ctx), lse.cpu().numpy().astype(np.float64), c.dctx)
+    rel = 2.0 ** -19 + (s + c.d + 8) * 2.0 ** -24
+    bound = np.zeros(ref.shape)
+    pos = np.arange(s)
+    np.add.at(bound, SO.bucket_matrix(c.spec, pos, pos), np.moveaxis((2 * rel * size).sum(0), 0, -1))
+    err = np.abs(dtable.cpu().numpy() - ref)
+    assert (err <= bound + 2.0 ** -23 * np.abs(ref)).all(), (err / (bound + 1e-30)).max()

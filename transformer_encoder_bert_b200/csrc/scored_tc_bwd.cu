@@ -86,7 +86,8 @@ struct RowBlock {
   uint32_t see[2];          // bits: visible columns
   float e, de;              // dU's scale, and D e (dQ mode)
   const float* col;         // dKV mode: -lse2 [64], D [64] of the columns (shared memory)
-  bool whole;               // no row or column of the block is past n
+  int valid;                // columns that are valid positions (any number)
+  bool mine;                // the row is one
   int p_at;                 // P and dU of column c go to column p_at + c / 2 (of S, of dP)
 };
 
@@ -205,11 +206,17 @@ __device__ __forceinline__ void row_block(const ScoreArgs& s, const RowBlock& rb
     tmem_wait_ld(dp);
     int form = kAny;
     if constexpr (CAP) {
-      float top = 0.f;
+      float top = 0.f;                                     // (of valid rows and columns, so that no other decides)
+      if (MASK && c + CH > rb.valid) {
 #pragma unroll
-      for (int k = 0; k < CH; k += 2)
-        top = fmaxf(fmaxf(top, fabsf(__uint_as_float(sv[k]))), fabsf(__uint_as_float(sv[k + 1])));
-      if (rb.whole) form = !any_warp(top > s.cap_small_top) ? kSmall : !any_warp(top * fabsf(cap.in) > kCapPoly) ? kPoly : kAny;
+        for (int k = 0; k < CH; ++k) top = fmaxf(top, c + k < rb.valid ? fabsf(__uint_as_float(sv[k])) : 0.f);
+      } else {
+#pragma unroll
+        for (int k = 0; k < CH; k += 2)
+          top = fmaxf(fmaxf(top, fabsf(__uint_as_float(sv[k]))), fabsf(__uint_as_float(sv[k + 1])));
+      }
+      form = !any_warp(rb.mine && top > s.cap_small_top) ? kSmall
+             : !any_warp(rb.mine && top * fabsf(cap.in) > kCapPoly) ? kPoly : kAny;
     }
     if (CAP && form == kSmall)
       row_chunk<MODE, CH, CAP, NEAR, MASK, CAP ? kSmall : kAny>(s, rb, cap, scale2, lane, c, sv, dp, pos, neg);
@@ -505,6 +512,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
     const int hi_all = MODE == kDQ ? score_jlim(s, r0, n, prefix) : n;
     RowBlock rb;
     const int doc = docs && mine ? docs[pos] : 0;
+    rb.mine = mine;
     rb.e = e;
     rb.de = dsum * e;
     const int buf = C::NB == 2 ? w : 0, first = C::kShare == 2 ? 32 * w : 0, last = C::kShare == 2 ? first + 32 : kBN;
@@ -520,7 +528,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
       const uint32_t ph = (it / C::NB) & 1;
       const bool cut = lo_all > c0 || c0 + kBN > hi_all || r_end >= n;
       const bool by_doc = docs && cls[jb] == 2;
-      rb.whole = r_end < n && c0 + kBN <= n;
+      rb.valid = n - c0;
       // The row's visible columns among those that its warpgroup takes.  Documents: each id that the warp's rows
       // hold, against the columns'.
       bool mask = cut || by_doc, hidden = false;

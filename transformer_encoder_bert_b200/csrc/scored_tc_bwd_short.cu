@@ -80,7 +80,8 @@ struct BwdChunk {
   float e;                  // dU's scale
   uint8_t* du;              // the row of dU^T (64 queries), and the swizzle and 16-byte unit of the chunk
   int swizzle, unit;
-  bool whole;               // no row or column of the chunk is past n
+  int valid;                // queries that are valid positions (any number)
+  bool mine;                // the row is one
 };
 
 // DIAG: adds dT to the lane's two diagonals of the 32 x 32 block (k0: the chunk's first column in it).
@@ -163,11 +164,11 @@ __device__ __forceinline__ void bwd_chunk(const ScoreArgs& s, const BwdChunk& ch
   tmem_wait_ld(dp);
   int form = kAny;
   if constexpr (CAP) {
-    float top = 0.f;
+    float top = 0.f;                                       // (of valid rows and queries, so that no other decides)
 #pragma unroll
-    for (int k = 0; k < 16; k += 2)
-      top = fmaxf(fmaxf(top, fabsf(__uint_as_float(sv[k]))), fabsf(__uint_as_float(sv[k + 1])));
-    if (ch.whole) form = !any_warp(top > s.cap_small_top) ? kSmall : !any_warp(top * fabsf(cap.in) > kCapPoly) ? kPoly : kAny;
+    for (int k = 0; k < 16; ++k) top = fmaxf(top, !MASK || k < ch.valid ? fabsf(__uint_as_float(sv[k])) : 0.f);
+    form = !any_warp(ch.mine && top > s.cap_small_top) ? kSmall
+           : !any_warp(ch.mine && top * fabsf(cap.in) > kCapPoly) ? kPoly : kAny;
   }
   if (CAP && form == kSmall)
     bwd_scores<CAP, BIAS, DIAG, MASK, CAP ? kSmall : kAny>(s, ch, cap, scale2, lane, k0, sv, dp, pos, neg);
@@ -445,7 +446,8 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
           ch.docs = s.docs ? pos_docs + i : nullptr;
           ch.du = smem + C::kDU + g * 16384 + r * 128;
           ch.unit = 4 * w + c / 8;
-          ch.whole = w1 < n && i + 16 <= n;
+          ch.valid = n - i;
+          ch.mine = mine;
           if (none) {
             const uint32_t zero[8] = {};
             tmem_st_32x32b_x8_async(ch.t_p, zero);
