@@ -497,7 +497,8 @@ ENC_API enc_status enc_reserve_scored(enc_t h, int batch, int seq);
  *   (natural logarithm), or NULL.  seq <= 65536.  qkv and ctx 16-byte aligned.
  * Accumulation, softmax and lse in FP32; FP16 mode rounds the unnormalised
  * probabilities to FP16 before the product with V, as enc_op_attention does, and
- * its tanh is an approximation that moves a capped score by up to cap 2^-21.
+ * its tanh is an approximation: up to a cap of 64 it moves a score by up to
+ * cap 2^-21, with larger caps by up to 2^-20 of the capped score.
  * Asynchronous. */
 ENC_API enc_status enc_op_scored_attention(enc_t h, const enc_scores* scores, const void* qkv,
                                            const int32_t* valid_len, void* ctx, float* lse, int batch, int seq,

@@ -86,3 +86,22 @@ def test_ragged_tiles_keep_small_scores(s, valid, cap, mode):
     np.add.at(bound, SO.bucket_matrix(c.spec, pos, pos), np.moveaxis((2 * rel * size).sum(0), 0, -1))
     err = np.abs(dtable.cpu().numpy() - ref)
     assert (err <= bound + 2.0 ** -23 * np.abs(ref)).all(), (err / (bound + 1e-30)).max()
+
+
+@pytest.mark.parametrize("mode", ["fp16", "fp16-simt", "fp32"])
+@pytest.mark.parametrize("cap", [2000.0, 1e4])
+@pytest.mark.parametrize("s,valid", [(100, [100, 97, 70]), (128, [128, 64, 128]), (300, [300, 257, 290])], ids=str)
+def test_small_scores_beside_a_large_one(s, valid, cap, mode):
+    """One key far past the cap does not change how the others' scores are formed."""
+    c = equal_scores(mode, s, cap, 0.4 * 2.0 ** -23 * cap, valid, outlier=True)
+    ctx, lse = c.forward()
+    ref, ref_lse, _ = SO.forward(c.spec, c.qkv, c.valid)
+    got = lse.cpu().numpy().astype(np.float64)
+    seen = np.isfinite(ref_lse)
+    # lse is near log n: the sum is off by n 2^-24, and t, its maximum and the logarithm by a few 2^-24 of 8.
+    assert np.abs(got[seen] - ref_lse[seen]).max() <= (s + 64) * 2.0 ** -24
+    # The same for the gradient's P: dv sums n of them, each rounded once in FP16 mode, and is rounded once.
+    dqkv, _ = c.backward(ctx, lse)
+    want = SO.backward(c.spec, c.qkv, c.valid, c.shaped(ctx), got, c.dctx)[0]
+    rel = (s + 64) * 2.0 ** -23 + (2.0 ** -10 if mode.startswith("fp16") else 2.0 ** -23)
+    assert (np.abs(dqkv[2].cpu().numpy() - want[2]) <= rel * np.abs(want[2]) + 2.0 ** -24).all()

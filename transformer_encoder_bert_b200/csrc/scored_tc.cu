@@ -137,7 +137,7 @@ struct SoftmaxBlock {
   bool mine;                // the row is a valid query
 };
 
-// CAP 0: none; 1: small scores; 2: by polynomial; 3: of any size.  x: the row, two scores to a register pair.
+// CAP 0: none; 1: small scores; 2: by polynomial; 3: of any size; 4: that, with a large cap.  x: the row, two scores to a register pair.
 template <int D, int CAP, int BIAS, bool MASK>
 __device__ __forceinline__ bool softmax_row(const ScoreArgs& s, const SoftmaxBlock& sb, uint64_t (&x)[BN / 2], float& m_ref,
                                             uint64_t& sum2) {
@@ -160,6 +160,9 @@ __device__ __forceinline__ bool softmax_row(const ScoreArgs& s, const SoftmaxBlo
       f2_unpack(x[k], a, c);
       x[k] = f2_pack(tanh_of(a, in2), tanh_of(c, in2));
     }
+  } else if constexpr (CAP == 4) {
+#pragma unroll
+    for (int k = 0; k < BN / 2; ++k) x[k] = tanh_careful2(x[k], sb.cap_in);
   }
   const uint64_t mul = CAP ? sb.cap2 : sb.scale2;
 #pragma unroll
@@ -231,7 +234,7 @@ __device__ __forceinline__ bool softmax_row(const ScoreArgs& s, const SoftmaxBlo
   return true;
 }
 
-template <int D, bool CAP, int BIAS, bool MASK>
+template <int D, int CAP, int BIAS, bool MASK>
 __device__ __forceinline__ bool softmax_block(const ScoreArgs& s, const SoftmaxBlock& sb, int lane, float& m_ref, uint64_t& sum2) {
   uint64_t x[BN / 2];
   {
@@ -247,7 +250,7 @@ __device__ __forceinline__ bool softmax_block(const ScoreArgs& s, const SoftmaxB
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(sb.s_free);
-  if constexpr (!CAP) {
+  if constexpr (CAP == kNoCap) {
     return softmax_row<D, 0, BIAS, MASK>(s, sb, x, m_ref, sum2);
   } else {
     float top = 0.f;                                       // (of valid rows and keys, so that no other decides)
@@ -271,7 +274,7 @@ __device__ __forceinline__ bool softmax_block(const ScoreArgs& s, const SoftmaxB
     if (!any_warp(sb.mine && top > s.cap_small_top)) return softmax_row<D, 1, BIAS, MASK>(s, sb, x, m_ref, sum2);
     if (!any_warp(sb.mine && top * fabsf(sb.cap_in) > kCapPoly))
       return softmax_row<D, 2, BIAS, MASK>(s, sb, x, m_ref, sum2);
-    return softmax_row<D, 3, BIAS, MASK>(s, sb, x, m_ref, sum2);
+    return softmax_row<D, CAP == kLargeCap ? 4 : 3, BIAS, MASK>(s, sb, x, m_ref, sum2);
   }
 }
 
@@ -287,8 +290,8 @@ __device__ __forceinline__ bool hidden_block(const SoftmaxBlock& sb, int lane) {
   return true;
 }
 
-// CAP: scores are capped.  BIAS 0: none; 1: a table; 2: slopes, with or without a table.
-template <int D, int TILES, bool CAP, int BIAS>
+// BIAS 0: none; 1: a table; 2: slopes, with or without a table.
+template <int D, int TILES, int CAP, int BIAS>
 __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasPerSm)
     scored_tc_kernel(const __grid_constant__ ScoreArgs s, const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_ctx,
@@ -641,7 +644,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasP
   }
 }
 
-template <int D, int TILES, bool CAP, int BIAS>
+template <int D, int TILES, int CAP, int BIAS>
 cudaError_t launch_v(const ScoreArgs& s, const __half* qkv, const int32_t* vl, __half* ctx, float* lse,
                      const ScoredShape& sh, int* status, cudaStream_t stream) {
   using C = Cfg<D, TILES>;
@@ -662,28 +665,28 @@ cudaError_t launch_v(const ScoreArgs& s, const __half* qkv, const int32_t* vl, _
 template <int D, int TILES>
 cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, __half* ctx, float* lse,
                      const ScoredShape& sh, int* status, cudaStream_t stream) {
-  if (s.cap > 0.f)
-    return s.slopes  ? launch_v<D, TILES, true, 2>(s, qkv, vl, ctx, lse, sh, status, stream)
-           : s.table ? launch_v<D, TILES, true, 1>(s, qkv, vl, ctx, lse, sh, status, stream)
-                     : launch_v<D, TILES, true, 0>(s, qkv, vl, ctx, lse, sh, status, stream);
-  return s.slopes  ? launch_v<D, TILES, false, 2>(s, qkv, vl, ctx, lse, sh, status, stream)
-         : s.table ? launch_v<D, TILES, false, 1>(s, qkv, vl, ctx, lse, sh, status, stream)
-                   : launch_v<D, TILES, false, 0>(s, qkv, vl, ctx, lse, sh, status, stream);
+  auto run = [&](auto cap) {
+    constexpr int CAP = decltype(cap)::value;
+    return s.slopes  ? launch_v<D, TILES, CAP, 2>(s, qkv, vl, ctx, lse, sh, status, stream)
+           : s.table ? launch_v<D, TILES, CAP, 1>(s, qkv, vl, ctx, lse, sh, status, stream)
+                     : launch_v<D, TILES, CAP, 0>(s, qkv, vl, ctx, lse, sh, status, stream);
+  };
+  return with_cap(s, run);
 }
 
 }  // namespace
 }  // namespace scored_tc
 
-// Coefficients of tanh(x) / x on |x| <= kCapSmall in powers of x^2, with x = in q.k: multiplied by in^(2k + 1) cap2.
+// TanhSmall's coefficients with x = in q.k: multiplied by in^(2k + 1) cap2.
 // Beyond the factors here a coefficient could leave FP32's range, and no score takes this form.
 void fold_cap(ScoreArgs* s) {
-  constexpr double c[5] = {1.0, -0.33333075046539307, 0.13324907422065735, -0.0529942512512207, 0.017151331529021263};
+  constexpr TanhSmall fit;
   const double in = (double)s->scale / s->cap;
   s->cap_small_top = -1.f;
   if (!(s->cap > 0.f) || !(fabs(in) >= 1e-4 && fabs(in) <= 1e4)) return;
   double f = in * s->cap * 1.4426950408889634;
-  for (int k = 0; k < 5; ++k, f *= in * in) s->cap_small[k] = (float)(c[k] * f);
-  s->cap_small_top = (float)(scored_tc::kCapSmall / fabs(in));
+  for (int k = 0; k < 5; ++k, f *= in * in) s->cap_small[k] = (float)(fit.c[k] * f);
+  s->cap_small_top = (float)(kTanhSmall / fabs(in));
 }
 
 cudaError_t launch_scored_tc(const ScoreArgs& s, const __half* qkv, const int32_t* valid_len, __half* ctx, float* lse,

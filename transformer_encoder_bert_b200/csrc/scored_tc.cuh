@@ -2,6 +2,8 @@
 // maps, descriptors, and the arithmetic of a row of scores.
 #pragma once
 
+#include <type_traits>
+
 #include "scored.cuh"
 #include "sm100.cuh"
 
@@ -145,18 +147,17 @@ __device__ __forceinline__ Bias make_bias(const ScoreArgs& s, float* column, flo
   return b;
 }
 
-// The cap, t2 = cap2 tanh(x) with x = s * in = u / cap.  The exact form,
-// tanh(x) = 1 - 2 / (1 + 2^(2 x log2 e)), costs two special-function operations
-// a score (a quarter of the FMA rate each, besides the softmax's own).  Where
-// every |x| of a warp's block is at most kCapPoly, a polynomial x P(x^2) of degree 8
-// in x^2 does it on the FMA pipe, and where every one is at most kCapSmall, one of
-// degree 4 with in and cap2 taken into its coefficients (s.cap_small), 6 operations
-// a score where the other costs 12.  Both are least-maximum fits of the relative
-// error, found by reweighted least squares: 7.7e-9 and 1.3e-8, with FP32 rounding
-// 1.1e-7 and 1e-7 (fits of the absolute error take a term less, but are off by 2e-6 of
-// a small score, which the table's gradient shows).  The exact form is off by about
-// 2^-22 of the cap.
-constexpr float kCapPoly = 1.25f, kCapSmall = 0.5f;
+// The cap, t2 = cap2 tanh(x) with x = s * in = u / cap.  1 - 2 / (1 + 2^(2 x log2 e)) costs two special-function
+// operations a score (a quarter of the FMA rate each, besides the softmax's own).  Where every |x| of a warp's block is
+// at most kCapPoly, a polynomial x P(x^2) of degree 8 in x^2 does it on the FMA pipe, and where every one is at most
+// kTanhSmall, one of degree 4 with in and cap2 taken into its coefficients (s.cap_small), 6 operations a score where the
+// other costs 12.  Both are least-maximum fits of the relative error, found by reweighted least squares: 1.9e-8 and
+// 2.9e-8, with FP32 rounding 1.1e-7 and 1e-7 (fits of the absolute error take a term less, but are off by 2e-6 of a
+// small score, which the table's gradient shows).  In the other blocks a score is off by about 2^-22 of the cap however
+// small it is.  Up to a cap of 64 that is a thirtieth of what rounding P to FP16 does to it; larger caps have kernels of
+// their own, in which scores up to kTanhSmall take the short polynomial there too (8 heads of 128, 8 sequences of 2048, a
+// cap of 8, where most blocks hold a larger score: 412 us, and 534 with that).
+constexpr float kCapPoly = 1.25f, kCapCoarse = 64.f;
 struct Cap {
   float in, cap2;
   float neg_inv2;           // -1 / cap2^2: 1 - tanh^2 of a capped score
@@ -194,10 +195,34 @@ __device__ __forceinline__ uint64_t small_cap2(const ScoreArgs& s, uint64_t x) {
   for (int k = 3; k >= 0; --k) p = f2_fma(p, z, f2_pack(s.cap_small[k], s.cap_small[k]));
   return f2_mul(x, p);
 }
+// What a kernel does about the cap (its template argument).
+constexpr int kNoCap = 0, kCap = 1, kLargeCap = 2;
+inline int cap_kind(const ScoreArgs& s) { return s.cap > kCapCoarse ? kLargeCap : s.cap > 0.f ? kCap : kNoCap; }
+template <typename F>
+cudaError_t with_cap(const ScoreArgs& s, F f) {            // f(integral constant)
+  switch (cap_kind(s)) {
+    case kNoCap: return f(std::integral_constant<int, kNoCap>());
+    case kCap: return f(std::integral_constant<int, kCap>());
+  }
+  return f(std::integral_constant<int, kLargeCap>());
+}
 // The forms of the cap; any: also when there is none.
-constexpr int kAny = 0, kPoly = 1, kSmall = 2;
+constexpr int kAny = 0, kPoly = 1, kSmall = 2, kCareful = 3;
 // tanh(s in) of any size; in2 = 2 in log2 e.
 __device__ __forceinline__ float tanh_of(float s, float in2) { return fmaf(-2.f, rcp(1.f + ex2(s * in2)), 1.f); }
+// The same of two scores, with the polynomial for those up to kTanhSmall.
+__device__ __forceinline__ uint64_t tanh_careful2(uint64_t s, float in) {
+  constexpr TanhSmall fit;
+  const uint64_t x = f2_mul(s, f2_pack(in, in)), z = f2_mul(x, x);
+  uint64_t p = f2_pack(fit.c[4], fit.c[4]);
+#pragma unroll
+  for (int k = 3; k >= 0; --k) p = f2_fma(p, z, f2_pack(fit.c[k], fit.c[k]));
+  float x0, x1, p0, p1;
+  f2_unpack(x, x0, x1);
+  f2_unpack(f2_mul(x, p), p0, p1);
+  return f2_pack(fabsf(x0) <= kTanhSmall ? p0 : tanh_of(x0, 2.f * kLog2e),
+                 fabsf(x1) <= kTanhSmall ? p1 : tanh_of(x1, 2.f * kLog2e));
+}
 
 // (Two predicated additions; a choice of addends costs two more instructions a score.)
 __device__ __forceinline__ void add_either(bool first, float v, float& a, float& b) {

@@ -124,6 +124,8 @@ __device__ __forceinline__ void row_chunk(const ScoreArgs& s, const RowBlock& rb
         } else if (FORM == kPoly) {
           const uint64_t y = f2_mul(x, f2_pack(cap.in, cap.in));
           x = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
+        } else if (FORM == kCareful) {
+          x = tanh_careful2(x, cap.in);
         } else {
           const float in2 = 2.f * kLog2e * cap.in;
           x = f2_pack(tanh_of(__uint_as_float(sv[at]), in2), tanh_of(__uint_as_float(sv[at + 1]), in2));
@@ -188,9 +190,10 @@ __device__ __forceinline__ void row_chunk(const ScoreArgs& s, const RowBlock& rb
 
 // Columns [first, last).  sums: NEAR 2: the lane's diagonals, k: columns less rows lane + 32 (k - 1), from the first
 // column and the warp's first row; else sums[1] += dT.
-template <int MODE, int CH, bool CAP, int NEAR, bool MASK>
+template <int MODE, int CH, int CAP, int NEAR, bool MASK>
 __device__ __forceinline__ void row_block(const ScoreArgs& s, const RowBlock& rb, int first, int last, const Cap& cap, float scale2,
                                           int lane, float (&sums)[3]) {
+  constexpr bool kOn = CAP != kNoCap;
   float pos = 0.f, neg = 0.f;
 #pragma unroll 1
   for (int c = first; c < last; c += CH) {
@@ -205,7 +208,7 @@ __device__ __forceinline__ void row_block(const ScoreArgs& s, const RowBlock& rb
     tmem_wait_ld(sv);
     tmem_wait_ld(dp);
     int form = kAny;
-    if constexpr (CAP) {
+    if constexpr (kOn) {
       float top = 0.f;                                     // (of valid rows and columns, so that no other decides)
       if (MASK && c + CH > rb.valid) {
 #pragma unroll
@@ -218,12 +221,12 @@ __device__ __forceinline__ void row_block(const ScoreArgs& s, const RowBlock& rb
       form = !any_warp(rb.mine && top > s.cap_small_top) ? kSmall
              : !any_warp(rb.mine && top * fabsf(cap.in) > kCapPoly) ? kPoly : kAny;
     }
-    if (CAP && form == kSmall)
-      row_chunk<MODE, CH, CAP, NEAR, MASK, CAP ? kSmall : kAny>(s, rb, cap, scale2, lane, c, sv, dp, pos, neg);
-    else if (CAP && form == kPoly)
-      row_chunk<MODE, CH, CAP, NEAR, MASK, CAP ? kPoly : kAny>(s, rb, cap, scale2, lane, c, sv, dp, pos, neg);
+    if (kOn && form == kSmall)
+      row_chunk<MODE, CH, kOn, NEAR, MASK, kOn ? kSmall : kAny>(s, rb, cap, scale2, lane, c, sv, dp, pos, neg);
+    else if (kOn && form == kPoly)
+      row_chunk<MODE, CH, kOn, NEAR, MASK, kOn ? kPoly : kAny>(s, rb, cap, scale2, lane, c, sv, dp, pos, neg);
     else
-      row_chunk<MODE, CH, CAP, NEAR, MASK, kAny>(s, rb, cap, scale2, lane, c, sv, dp, pos, neg);
+      row_chunk<MODE, CH, kOn, NEAR, MASK, CAP == kLargeCap ? kCareful : kAny>(s, rb, cap, scale2, lane, c, sv, dp, pos, neg);
     if (NEAR == 2 && c + CH == first + 32) {
       sums[0] = neg;
       neg = pos;                                           // the first 32 columns' lane is the next ones' lane - 32
@@ -250,7 +253,7 @@ __device__ __forceinline__ void hidden_rows(const RowBlock& rb, int first, int l
   }
 }
 
-template <int MODE, int CH, bool CAP, int NEAR>
+template <int MODE, int CH, int CAP, int NEAR>
 __device__ __forceinline__ void row_block_m(const ScoreArgs& s, bool mask, const RowBlock& rb, int first, int last, const Cap& cap,
                                             float scale2, int lane, float (&sums)[3]) {
   if (mask)
@@ -259,7 +262,8 @@ __device__ __forceinline__ void row_block_m(const ScoreArgs& s, bool mask, const
     row_block<MODE, CH, CAP, NEAR, false>(s, rb, first, last, cap, scale2, lane, sums);
 }
 
-template <int D, int MODE>
+// LARGE: for caps above kCapCoarse.
+template <int D, int MODE, bool LARGE>
 __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
     scored_tc_bwd_kernel(const __grid_constant__ ScoreArgs s, const __grid_constant__ CUtensorMap tm_a0,
                          const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b0,
@@ -268,6 +272,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
                          float* partial, __half* dqkv, int B, int S, int NH, int* status) {
   // (Pointers without __restrict__: no load may go through the read-only path, or move above the acquire.)
   using C = BCfg<D, MODE>;
+  constexpr int kCapped = LARGE ? kLargeCap : kCap;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -577,24 +582,24 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
         hidden_rows<MODE>(rb, first, last);
       } else if (near) {
         if (MODE == kDQ && partial) {
-          if (cap.on)
-            row_block_m<MODE, C::kChunk, true, MODE == kDQ ? 2 : 1>(s, mask, rb, first, last, cap, scale2, lane, sum);
+          if (LARGE || cap.on)
+            row_block_m<MODE, C::kChunk, kCapped, MODE == kDQ ? 2 : 1>(s, mask, rb, first, last, cap, scale2, lane, sum);
           else
-            row_block_m<MODE, C::kChunk, false, MODE == kDQ ? 2 : 1>(s, mask, rb, first, last, cap, scale2, lane, sum);
-        } else if (cap.on) {
-          row_block_m<MODE, C::kChunk, true, 1>(s, mask, rb, first, last, cap, scale2, lane, sum);
+            row_block_m<MODE, C::kChunk, kNoCap, MODE == kDQ ? 2 : 1>(s, mask, rb, first, last, cap, scale2, lane, sum);
+        } else if (LARGE || cap.on) {
+          row_block_m<MODE, C::kChunk, kCapped, 1>(s, mask, rb, first, last, cap, scale2, lane, sum);
         } else {
-          row_block_m<MODE, C::kChunk, false, 1>(s, mask, rb, first, last, cap, scale2, lane, sum);
+          row_block_m<MODE, C::kChunk, kNoCap, 1>(s, mask, rb, first, last, cap, scale2, lane, sum);
         }
       } else if (s.slopes) {
-        if (cap.on)
-          row_block_m<MODE, C::kChunk, true, 3>(s, mask, rb, first, last, cap, scale2, lane, sum);
+        if (LARGE || cap.on)
+          row_block_m<MODE, C::kChunk, kCapped, 3>(s, mask, rb, first, last, cap, scale2, lane, sum);
         else
-          row_block_m<MODE, C::kChunk, false, 3>(s, mask, rb, first, last, cap, scale2, lane, sum);
-      } else if (cap.on) {
-        row_block_m<MODE, C::kChunk, true, 0>(s, mask, rb, first, last, cap, scale2, lane, sum);
+          row_block_m<MODE, C::kChunk, kNoCap, 3>(s, mask, rb, first, last, cap, scale2, lane, sum);
+      } else if (LARGE || cap.on) {
+        row_block_m<MODE, C::kChunk, kCapped, 0>(s, mask, rb, first, last, cap, scale2, lane, sum);
       } else {
-        row_block_m<MODE, C::kChunk, false, 0>(s, mask, rb, first, last, cap, scale2, lane, sum);
+        row_block_m<MODE, C::kChunk, kNoCap, 0>(s, mask, rb, first, last, cap, scale2, lane, sum);
       }
       // Rows of the columns' operands in [n, n rounded up to 16) are read by the products: zeros.
       const int lim = n - c0, lim16 = (min(kBN, lim) + 15) & ~15;
@@ -775,19 +780,18 @@ __global__ void __launch_bounds__(kStatThreads)
   }
 }
 
-template <int D, int MODE>
+template <int D, int MODE, bool LARGE>
 cudaError_t launch_mode(const ScoreArgs& s, const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0,
                         const CUtensorMap& b1, const CUtensorMap& out, const int32_t* vl, const float* rows2, int Sp,
                         const float* norms, unsigned* counter, float* partial, __half* dqkv, const ScoredShape& sh,
                         int* status, cudaStream_t stream) {
   using C = BCfg<D, MODE>;
-  static const cudaError_t attr = cudaFuncSetAttribute(scored_tc_bwd_kernel<D, MODE>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  auto kern = scored_tc_bwd_kernel<D, MODE, LARGE>;
+  static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (attr != cudaSuccess) return attr;
   const dim3 grid((sh.seq + 127) / 128, sh.head_num, sh.batch);
-  return launch_kernel(scored_tc_bwd_kernel<D, MODE>, grid, dim3(C::kThreads), C::smem(s, sh.seq, partial != nullptr),
-                       stream, nullptr, 0, s, a0, a1, b0, b1, out, vl, rows2, Sp, norms, counter, partial, dqkv, sh.batch,
-                       sh.seq, sh.head_num, status);
+  return launch_kernel(kern, grid, dim3(C::kThreads), C::smem(s, sh.seq, partial != nullptr), stream, nullptr, 0, s, a0, a1,
+                       b0, b1, out, vl, rows2, Sp, norms, counter, partial, dqkv, sh.batch, sh.seq, sh.head_num, status);
 }
 
 template <int D>
@@ -810,11 +814,15 @@ cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, c
       !encode_operand_map(&dcols, dctx, H, sh.seq, sh.batch, 64, kBN) ||
       !encode_operand_map(&out, dqkv, D, sh.seq, 3 * planes, D < 64 ? D : 64, 32))
     return cudaErrorInvalidValue;
-  e = launch_mode<D, kDQ>(s, rows, drows, cols, cols, out, vl, rows2, Sp, norms, counter, partial, dqkv, sh, status,
-                           stream);
-  if (e != cudaSuccess) return e;
-  return launch_mode<D, kDKV>(s, rows, rows, cols, dcols, out, vl, rows2, Sp, norms, counter, nullptr, dqkv, sh, status,
-                             stream);
+  auto both = [&](auto large) {
+    constexpr bool LARGE = decltype(large)::value;
+    const cudaError_t first = launch_mode<D, kDQ, LARGE>(s, rows, drows, cols, cols, out, vl, rows2, Sp, norms, counter,
+                                                         partial, dqkv, sh, status, stream);
+    if (first != cudaSuccess) return first;
+    return launch_mode<D, kDKV, LARGE>(s, rows, rows, cols, dcols, out, vl, rows2, Sp, norms, counter, nullptr, dqkv, sh,
+                                       status, stream);
+  };
+  return cap_kind(s) == kLargeCap ? both(std::true_type()) : both(std::false_type());
 }
 
 }  // namespace

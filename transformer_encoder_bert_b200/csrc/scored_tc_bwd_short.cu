@@ -109,6 +109,8 @@ __device__ __forceinline__ void bwd_scores(const ScoreArgs& s, const BwdChunk& c
         } else if (FORM == kPoly) {
           const uint64_t y = f2_mul(x, f2_pack(cap.in, cap.in));
           x = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
+        } else if (FORM == kCareful) {
+          x = tanh_careful2(x, cap.in);
         } else {
           const float in2 = 2.f * kLog2e * cap.in;
           x = f2_pack(tanh_of(__uint_as_float(sv[at]), in2), tanh_of(__uint_as_float(sv[at + 1]), in2));
@@ -154,31 +156,32 @@ __device__ __forceinline__ void bwd_scores(const ScoreArgs& s, const BwdChunk& c
   *reinterpret_cast<uint4*>(ch.du + 16 * ((ch.unit + 1) ^ ch.swizzle)) = make_uint4(pu[4], pu[5], pu[6], pu[7]);
 }
 
-template <bool CAP, bool BIAS, bool DIAG, bool MASK>
+template <int CAP, bool BIAS, bool DIAG, bool MASK>
 __device__ __forceinline__ void bwd_chunk(const ScoreArgs& s, const BwdChunk& ch, const Cap& cap, float scale2, int lane,
                                           int k0, float& pos, float& neg) {
+  constexpr bool kOn = CAP != kNoCap;
   uint32_t sv[16], dp[16];
   tmem_ld_32x32b_x16_async(ch.t_s, sv);
   tmem_ld_32x32b_x16_async(ch.t_dp, dp);
   tmem_wait_ld(sv);
   tmem_wait_ld(dp);
   int form = kAny;
-  if constexpr (CAP) {
+  if constexpr (kOn) {
     float top = 0.f;                                       // (of valid rows and queries, so that no other decides)
 #pragma unroll
     for (int k = 0; k < 16; ++k) top = fmaxf(top, !MASK || k < ch.valid ? fabsf(__uint_as_float(sv[k])) : 0.f);
     form = !any_warp(ch.mine && top > s.cap_small_top) ? kSmall
            : !any_warp(ch.mine && top * fabsf(cap.in) > kCapPoly) ? kPoly : kAny;
   }
-  if (CAP && form == kSmall)
-    bwd_scores<CAP, BIAS, DIAG, MASK, CAP ? kSmall : kAny>(s, ch, cap, scale2, lane, k0, sv, dp, pos, neg);
-  else if (CAP && form == kPoly)
-    bwd_scores<CAP, BIAS, DIAG, MASK, CAP ? kPoly : kAny>(s, ch, cap, scale2, lane, k0, sv, dp, pos, neg);
+  if (kOn && form == kSmall)
+    bwd_scores<kOn, BIAS, DIAG, MASK, kOn ? kSmall : kAny>(s, ch, cap, scale2, lane, k0, sv, dp, pos, neg);
+  else if (kOn && form == kPoly)
+    bwd_scores<kOn, BIAS, DIAG, MASK, kOn ? kPoly : kAny>(s, ch, cap, scale2, lane, k0, sv, dp, pos, neg);
   else
-    bwd_scores<CAP, BIAS, DIAG, MASK, kAny>(s, ch, cap, scale2, lane, k0, sv, dp, pos, neg);
+    bwd_scores<kOn, BIAS, DIAG, MASK, CAP == kLargeCap ? kCareful : kAny>(s, ch, cap, scale2, lane, k0, sv, dp, pos, neg);
 }
 
-template <int D, bool CAP, bool BIAS, bool DIAG>
+template <int D, int CAP, bool BIAS, bool DIAG>
 __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
     scored_tc_bwd_short_kernel(const __grid_constant__ ScoreArgs s, const __grid_constant__ CUtensorMap tm_qkv,
                                const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_out,
@@ -542,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
   }
 }
 
-template <int D, bool CAP, bool BIAS, bool DIAG>
+template <int D, int CAP, bool BIAS, bool DIAG>
 cudaError_t launch_v(const ScoreArgs& s, const __half* qkv, const int32_t* vl, const __half* ctx, const float* lse,
                      const __half* dctx, __half* dqkv, float* partial, const ScoredShape& sh, int* status, int num_sms,
                      cudaStream_t stream) {
@@ -561,7 +564,7 @@ cudaError_t launch_v(const ScoreArgs& s, const __half* qkv, const int32_t* vl, c
                        status);
 }
 
-template <int D, bool CAP>
+template <int D, int CAP>
 cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, const __half* ctx, const float* lse,
                      const __half* dctx, __half* dqkv, float* partial, const ScoredShape& sh, int* status, int num_sms,
                      cudaStream_t stream) {
@@ -588,7 +591,7 @@ cudaError_t launch_scored_backward_tc_short(const ScoreArgs& s, const __half* qk
     return launch_d<decltype(d)::value, decltype(cap)::value>(s, qkv, valid_len, ctx, lse, dctx, dqkv, partial, sh, status,
                                                               num_sms, stream);
   };
-  auto capped = [&](auto d) { return s.cap > 0.f ? run(d, std::true_type()) : run(d, std::false_type()); };
+  auto capped = [&](auto d) { return with_cap(s, [&](auto cap) { return run(d, cap); }); };
   switch (sh.size_per_head) {
     case 32: return capped(std::integral_constant<int, 32>());
     case 64: return capped(std::integral_constant<int, 64>());

@@ -62,15 +62,15 @@ struct ShortChunk {
   int keys;                 // valid keys of the chunk (any number)
   bool mine;                // the row is a valid query
 };
-template <bool CAP, bool BIAS, bool MASK>
+template <int CAP, bool BIAS, bool MASK>
 __device__ __forceinline__ float first_pass(const ScoreArgs& s, const ShortChunk& ch, float mx) {
   uint32_t sv[32];
   tmem_ld_32x32b_x32(ch.t_s, sv);
   uint64_t x[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) x[k] = f2_pack(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1]));
-  uint64_t mul = CAP ? ch.cap2 : ch.scale2;
-  if constexpr (CAP) {
+  uint64_t mul = CAP != kNoCap ? ch.cap2 : ch.scale2;
+  if constexpr (CAP != kNoCap) {
     float top = 0.f;                                       // (of valid rows and keys, so that no other decides)
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
@@ -93,6 +93,9 @@ __device__ __forceinline__ float first_pass(const ScoreArgs& s, const ShortChunk
         const uint64_t y = f2_mul(x[k], in);
         x[k] = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
       }
+    } else if constexpr (CAP == kLargeCap) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = tanh_careful2(x[k], ch.cap_in);
     } else {
       const float in2 = 2.f * kLog2e * ch.cap_in;
 #pragma unroll
@@ -121,7 +124,7 @@ __device__ __forceinline__ float first_pass(const ScoreArgs& s, const ShortChunk
   return fmaxf(m2[0], m2[1]);
 }
 
-template <int D, bool CAP, bool BIAS>
+template <int D, int CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, SCfg<D>::kCtasPerSm)
     scored_tc_short_kernel(const __grid_constant__ ScoreArgs s, const __grid_constant__ CUtensorMap tm_qkv,
                            const __grid_constant__ CUtensorMap tm_ctx, const int32_t* __restrict__ valid_len,
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, SCfg<D>::kCtasPerSm)
   }
 }
 
-template <int D, bool CAP, bool BIAS>
+template <int D, int CAP, bool BIAS>
 cudaError_t launch_v(const ScoreArgs& s, const __half* qkv, const int32_t* vl, __half* ctx, float* lse,
                      const ScoredShape& sh, int* status, int num_sms, cudaStream_t stream) {
   using C = SCfg<D>;
@@ -410,11 +413,12 @@ template <int D>
 cudaError_t launch_d(const ScoreArgs& s, const __half* qkv, const int32_t* vl, __half* ctx, float* lse,
                      const ScoredShape& sh, int* status, int num_sms, cudaStream_t stream) {
   const bool bias = s.table || s.slopes;
-  if (s.cap > 0.f)
-    return bias ? launch_v<D, true, true>(s, qkv, vl, ctx, lse, sh, status, num_sms, stream)
-                : launch_v<D, true, false>(s, qkv, vl, ctx, lse, sh, status, num_sms, stream);
-  return bias ? launch_v<D, false, true>(s, qkv, vl, ctx, lse, sh, status, num_sms, stream)
-              : launch_v<D, false, false>(s, qkv, vl, ctx, lse, sh, status, num_sms, stream);
+  auto run = [&](auto cap) {
+    constexpr int CAP = decltype(cap)::value;
+    return bias ? launch_v<D, CAP, true>(s, qkv, vl, ctx, lse, sh, status, num_sms, stream)
+                : launch_v<D, CAP, false>(s, qkv, vl, ctx, lse, sh, status, num_sms, stream);
+  };
+  return with_cap(s, run);
 }
 
 }  // namespace
