@@ -532,7 +532,9 @@ ENC_API enc_status enc_op_scored_attention_backward(enc_t h, const enc_scores* s
  * attends to positions 0..p (whatever causal and prefix_len say); doc_ids is
  * [batch, capacity] and holds p's document too.  len is not changed.  A sequence
  * with len[b] outside [0, capacity) gets ctx = 0 and an unchanged cache.  Every
- * other part of the cache stays as it is.  Asynchronous. */
+ * other part of the cache stays as it is.  All sums and weights are FP32; FP16
+ * mode rounds ctx once, and its tanh moves a score by up to 2^-20 of the capped
+ * score.  Asynchronous. */
 ENC_API enc_status enc_op_scored_attention_step(enc_t h, const enc_scores* scores, const void* qkv, void* cache,
                                                 const int32_t* len, void* ctx, int batch, int capacity,
                                                 enc_stream_t stream);

@@ -11,6 +11,7 @@ import encoder_inputs as EI
 from oracle import scored_oracle as SO
 from parity_utils import encoder_from_inputs, to_dev
 from test_gpu_scored import Case, encoder
+from transformer_encoder_bert_b200 import Scores
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +106,29 @@ def test_small_scores_beside_a_large_one(s, valid, cap, mode):
     want = SO.backward(c.spec, c.qkv, c.valid, c.shaped(ctx), got, c.dctx)[0]
     rel = (s + 64) * 2.0 ** -23 + (2.0 ** -10 if mode.startswith("fp16") else 2.0 ** -23)
     assert (np.abs(dqkv[2].cpu().numpy() - want[2]) <= rel * np.abs(want[2]) + 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "fp32"])
+@pytest.mark.parametrize("cap", [30.0, 1e3, 1e4])
+@pytest.mark.parametrize("capacity", [100, 600])
+def test_step_keeps_small_scores(capacity, cap, dtype):
+    """Half of the keys score u, half -u, with values 1 and -1: ctx = tanh(u), which a tanh good to a step (2^-23) of
+    the cap rounds to nothing."""
+    nh, d, b = 2, 64, 2
+    enc = encoder(nh, d, dtype)
+    np_dt = np.float16 if dtype == "fp16" else np.float32
+    a = np_dt(np.sqrt(0.45 * 2.0 ** -23 * cap / 0.125))
+    new, cache = np.zeros((3, b, nh, 1, d), np_dt), np.zeros((2, b, nh, capacity, d), np_dt)
+    sign = np.where(np.arange(capacity) % 2, -1.0, 1.0)
+    new[0, ..., 0] = a
+    cache[0, ..., 0] = (sign * a)[None, None]
+    cache[1] = sign[None, None, :, None]
+    length = np.array([capacity - 1, 59], np.int32)           # the new token, of the odd positions, is the last -u
+    new[1, ..., 0], new[2] = -a, -1
+    ctx = torch.empty((b, nh * d), dtype=to_dev(new).dtype, device="cuda")
+    enc.op_scored_attention_step(Scores(scale=0.125, cap=cap), to_dev(new), to_dev(cache), to_dev(length), ctx, b, capacity)
+    u = cap * np.tanh(float(a) * float(a) * 0.125 / cap)
+    # A weight is 1 -+ 2u with an error of 2^-22 (its exponential), the two sums' of (capacity / 4) 2^-24 or less; then
+    # 2^-20 of u and the rounding of the result.
+    tol = 2.0 ** -21 + capacity * 2.0 ** -24 / 4 + (2.0 ** -20 + (2.0 ** -11 if dtype == "fp16" else 2.0 ** -23)) * u + 2.0 ** -25
+    assert np.abs(ctx.cpu().numpy().astype(np.float64) - np.tanh(u)).max() <= tol
