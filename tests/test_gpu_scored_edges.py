@@ -132,3 +132,40 @@ def test_step_keeps_small_scores(capacity, cap, dtype):
     # 2^-20 of u and the rounding of the result.
     tol = 2.0 ** -21 + capacity * 2.0 ** -24 / 4 + (2.0 ** -20 + (2.0 ** -11 if dtype == "fp16" else 2.0 ** -23)) * u + 2.0 ** -25
     assert np.abs(ctx.cpu().numpy().astype(np.float64) - np.tanh(u)).max() <= tol
+
+
+@pytest.mark.parametrize("mode", ["fp16", "fp16-simt", "fp32"])
+@pytest.mark.parametrize("cap", [1.0, 100.0])
+@pytest.mark.parametrize("s", [90, 300])
+def test_gradients_through_saturated_scores(s, cap, mode):
+    """Every score 5 to 8 caps out, where 1 - tanh^2 is 2e-4 to 5e-7 and tanh itself has no digits left for it."""
+    nh, d, b = 2, 64, 2
+    c = Case("plain", mode, b, nh, s, d, seed=31, valid=[s, s - 7])
+    c.spec.scale, c.spec.cap = 0.125, cap
+    r = np.random.default_rng(32)
+    c.qkv[:2] = 0
+    c.qkv[0, ..., 0] = r.uniform(7, 8, (b, nh, s))            # scale q k = q k / 8 in +-[5, 8] caps
+    c.qkv[1, ..., 0] = r.uniform(5.75, 8, (b, nh, s)) * r.choice([-1.0, 1.0], (b, nh, s)) * cap
+    if cap == 100.0:                                          # (the keys below the cap would get no weight)
+        c.qkv[1] = np.abs(c.qkv[1])
+    c.dctx = (c.dctx * 30).astype(c.dctx.dtype)
+    ctx, lse = c.forward()
+    dqkv, _ = c.backward(ctx, lse)
+    ref, _, (p, size, du) = SO.backward(c.spec, c.qkv, c.valid, c.shaped(ctx), lse.cpu().numpy().astype(np.float64), c.dctx)
+    q, k = (np.abs(SO._clean(c.qkv[i], c.valid, 2)) for i in range(2))
+    x = 0.125 * (q @ np.swapaxes(k, -1, -2)) / cap
+    slope = np.where(p > 0, 1 / np.cosh(np.minimum(x, 300)) ** 2, 0)
+    # x is off by 3 roundings and 2^-24 of its exponent's rounding: 2^-21 of 8, twice that for the slope, whose own
+    # operations add 2^-20; P by t (4 roundings of 1.5 cap, tanh 2^-22 of the cap) and 2^-19; sums of s terms by s 2^-24.
+    rel = 2.0 ** -17 + cap * 2.0 ** -20 + 2.0 ** -19 + (s + d) * 2.0 ** -24
+    half = 2.0 ** -11 if mode.startswith("fp16") else 0.0
+    # FP16: dU is scaled so that the largest |dctx_i| |v_j| is at 2^13 or more, and below 2^-14 its halves are off by 2^-25.
+    do, v = (SO._clean(a, c.valid, i) for a, i in ((c.dctx, 1), (c.qkv[2], 2)))
+    norm = np.sqrt((do ** 2).sum(-1)).max() * np.sqrt((v ** 2).sum(-1)).max()
+    step = (2.0 ** -25 * 2.0 ** -13 * 2 * norm if mode == "fp16" else 0.0) * (p > 0)
+    err = half * np.abs(du) + 2 * rel * size * slope + step
+    out = 2.0 ** -11 if half else 2.0 ** -24
+    for i, want in ((0, 0.125 * (err @ k)), (1, 0.125 * (np.swapaxes(err, -1, -2) @ q))):
+        bound = want + out * np.abs(ref[i]) + (2.0 ** -25 if half else 0.0)
+        got = np.abs(dqkv[i].cpu().numpy() - ref[i])
+        assert (got <= bound + 1e-30).all(), (i, (got / (bound + 1e-30)).max())

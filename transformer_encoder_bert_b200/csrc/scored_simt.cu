@@ -172,8 +172,12 @@ __device__ __forceinline__ float capped2(const ScoreArgs& s, float inv_cap, floa
   const float u = dot * s.scale;
   slope = 1.f;
   if (s.cap <= 0.f) return u * kLog2e;
-  const float th = tanhf(u * inv_cap);
+  const float x = u * inv_cap, th = tanhf(x);
   slope = fmaf(-th, th, 1.f);
+  if (fabsf(th) > 0.75f) {               // near 1 that difference loses its digits: from E = e^(-2 |x|)
+    const float e = exp2f(fabsf(x) * (-2.f * kLog2e)), r = 1.f / (1.f + e);
+    slope = 4.f * e * r * r;
+  }
   return s.cap * th * kLog2e;
 }
 

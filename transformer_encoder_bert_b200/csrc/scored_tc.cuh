@@ -224,6 +224,35 @@ __device__ __forceinline__ uint64_t tanh_careful2(uint64_t s, float in) {
                  fabsf(x1) <= kTanhSmall ? p1 : tanh_of(x1, 2.f * kLog2e));
 }
 
+// The gradient's: tanh and 1 - tanh^2 of two scores times in, of any size.  From E = 2^(-2 |x| log2 e), r = 1 / (1 + E):
+// tanh |x| = 1 - 2 E r and 1 - tanh^2 = 4 E r^2, which keeps its precision where tanh is near 1 (1 - tanh^2 from tanh
+// itself is off by 2^-23, a hundredth of it at x = 6).
+template <bool CAREFUL>
+__device__ __forceinline__ uint64_t tanh_slope2(uint64_t s, float in, uint64_t& slope) {
+  const uint64_t x = f2_mul(s, f2_pack(in, in));
+  float x0, x1;
+  f2_unpack(x, x0, x1);
+  const float e0 = ex2(fabsf(x0) * (-2.f * kLog2e)), e1 = ex2(fabsf(x1) * (-2.f * kLog2e));
+  const uint64_t r = f2_pack(rcp(1.f + e0), rcp(1.f + e1)), er = f2_mul(f2_pack(e0, e1), r);
+  slope = f2_mul(er, f2_mul(r, f2_pack(4.f, 4.f)));
+  float t0, t1;
+  f2_unpack(f2_fma(er, f2_pack(-2.f, -2.f), f2_pack(1.f, 1.f)), t0, t1);
+  t0 = copysignf(t0, x0);
+  t1 = copysignf(t1, x1);
+  if (CAREFUL) {
+    constexpr TanhSmall fit;
+    const uint64_t z = f2_mul(x, x);
+    uint64_t p = f2_pack(fit.c[4], fit.c[4]);
+#pragma unroll
+    for (int k = 3; k >= 0; --k) p = f2_fma(p, z, f2_pack(fit.c[k], fit.c[k]));
+    float p0, p1;
+    f2_unpack(f2_mul(x, p), p0, p1);
+    t0 = fabsf(x0) <= kTanhSmall ? p0 : t0;
+    t1 = fabsf(x1) <= kTanhSmall ? p1 : t1;
+  }
+  return f2_pack(t0, t1);
+}
+
 // (Two predicated additions; a choice of addends costs two more instructions a score.)
 __device__ __forceinline__ void add_either(bool first, float v, float& a, float& b) {
   asm("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t@p add.f32 %0, %0, %3;\n\t@!p add.f32 %1, %1, %3;\n\t}"

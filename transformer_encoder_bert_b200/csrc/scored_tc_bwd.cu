@@ -118,17 +118,15 @@ __device__ __forceinline__ void row_chunk(const ScoreArgs& s, const RowBlock& rb
     for (int q = 0; q < 4; q += 2) {
       const int at = k + q;
       uint64_t x = f2_pack(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1]));
+      uint64_t slope2 = 0;                                 // 1 - tanh^2
       if constexpr (CAP) {
         if (FORM == kSmall) {
           x = small_cap2(s, x);
         } else if (FORM == kPoly) {
           const uint64_t y = f2_mul(x, f2_pack(cap.in, cap.in));
           x = f2_mul(y, tanh_over_x2(f2_mul(y, y)));
-        } else if (FORM == kCareful) {
-          x = tanh_careful2(x, cap.in);
         } else {
-          const float in2 = 2.f * kLog2e * cap.in;
-          x = f2_pack(tanh_of(__uint_as_float(sv[at]), in2), tanh_of(__uint_as_float(sv[at + 1]), in2));
+          x = tanh_slope2<FORM == kCareful>(x, cap.in, slope2);
         }
       }
       uint64_t add = base2;
@@ -147,7 +145,8 @@ __device__ __forceinline__ void row_chunk(const ScoreArgs& s, const RowBlock& rb
       uint64_t u2 = dt2;
       if constexpr (CAP) {                                 // dU = dT (1 - tanh^2)
         const float f = FORM == kSmall ? cap.neg_inv2 : -1.f;
-        u2 = f2_mul(dt2, f2_fma(f2_mul(x, f2_pack(f, f)), x, one2));
+        if (FORM == kSmall || FORM == kPoly) slope2 = f2_fma(f2_mul(x, f2_pack(f, f)), x, one2);
+        u2 = f2_mul(dt2, slope2);
       }
       float u0, u1, a0, a1;
       f2_unpack(u2, u0, u1);
