@@ -169,3 +169,22 @@ def test_gradients_through_saturated_scores(s, cap, mode):
         bound = want + out * np.abs(ref[i]) + (2.0 ** -25 if half else 0.0)
         got = np.abs(dqkv[i].cpu().numpy() - ref[i])
         assert (got <= bound + 1e-30).all(), (i, (got / (bound + 1e-30)).max())
+
+
+# ---------------------------------------------------------------- scratch
+def test_scratch_grows_by_what_is_needed_when_memory_is_short():
+    """Scratch grows by doubling, but a device without room for twice the old size still serves a little more than it."""
+    enc = fresh_encoder(4, 32, "fp32")
+    filler = None
+    try:
+        free = torch.cuda.mem_get_info()[0]
+        enc.reserve_scored(4096, 4096)
+        torch.cuda.empty_cache()
+        held = free - torch.cuda.mem_get_info()[0]            # 1.1 GB
+        assert held > 2 ** 30
+        filler = torch.empty(torch.cuda.mem_get_info()[0] - held - held // 2, dtype=torch.uint8, device="cuda")
+        enc.reserve_scored(4300, 4096)
+    finally:
+        filler = None
+        enc.close()
+        torch.cuda.empty_cache()

@@ -588,8 +588,14 @@ enc_status ensure_scored_ws(enc_handle* h, int batch, int seq, bool have_stream,
                   "enc_reserve_scored first", need);
   }
   void* p = nullptr;
-  const size_t bytes = std::max(need, 2 * h->scored_ws_bytes);   // doubling bounds what the retired ones hold
-  if (cudaMalloc(&p, bytes) != cudaSuccess) {
+  size_t bytes = std::max(need, 2 * h->scored_ws_bytes);   // doubling bounds what the retired ones hold
+  cudaError_t e = cudaMalloc(&p, bytes);
+  if (e != cudaSuccess && bytes > need) {
+    cudaGetLastError();
+    bytes = need;
+    e = cudaMalloc(&p, bytes);
+  }
+  if (e != cudaSuccess) {
     cudaGetLastError();
     return fail(ENC_ERR_OOM, "scratch allocation of %zu bytes failed", bytes);
   }
