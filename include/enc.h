@@ -485,8 +485,10 @@ ENC_API enc_status enc_set_scores(enc_t h, const enc_scores* scores);
 
 /* enc_reserve_scored - grow the scratch of the three calls below now
  * (synchronous) to hold any of them at batch x seq (seq = capacity for the
- * step).  Without it a call grows the scratch itself (cudaMalloc), except while
- * `stream` is being captured: then ENC_ERR_INVALID_ARG.  Scratch that was ever
+ * step).  Without it a call that needs more grows the scratch itself
+ * (cudaMalloc), except while `stream` is being captured: then
+ * ENC_ERR_INVALID_ARG.  The forward, the step, and in FP16 mode the backward of
+ * seq <= 128 without dtable need none.  Scratch that was ever
  * handed to a call stays allocated until enc_destroy, so that a graph captured
  * by the caller keeps valid addresses when the scratch grows later. */
 ENC_API enc_status enc_reserve_scored(enc_t h, int batch, int seq);

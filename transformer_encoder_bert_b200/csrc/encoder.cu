@@ -310,15 +310,23 @@ bool use_tc_attention(const enc_handle* h, int seq) {
   return enc::attention_tc_supported(h->d, seq) && h->tc_attn;
 }
 
+// The kernels of a scored attention call.
+enum class ScoredPath { kShort, kTc, kSimt };
+ScoredPath scored_path(const enc_handle* h, int seq) {
+  if (h->dtype != ENC_FP16 || !h->tc_attn) return ScoredPath::kSimt;
+  return seq <= enc::kScoredShort ? ScoredPath::kShort : ScoredPath::kTc;
+}
+
 // Attention with modified scores (scored.cuh).
 enc_status step_scored(enc_handle* h, const enc::ScoreArgs& s, const void* qkv, const int32_t* vl, void* ctx,
                        float* lse, int batch, int seq, cudaStream_t st) {
   const enc::ScoredShape sh{batch, seq, h->nh, h->d};
+  const ScoredPath path = scored_path(h, seq);
   cudaError_t e;
-  if (h->dtype == ENC_FP16 && h->tc_attn && seq <= enc::kScoredShort)
+  if (path == ScoredPath::kShort)
     e = enc::launch_scored_tc_short(s, static_cast<const __half*>(qkv), vl, static_cast<__half*>(ctx), lse, sh,
                                     h->status, h->num_sms, st);
-  else if (h->dtype == ENC_FP16 && h->tc_attn)
+  else if (path == ScoredPath::kTc)
     e = enc::launch_scored_tc(s, static_cast<const __half*>(qkv), vl, static_cast<__half*>(ctx), lse, sh, h->status, st);
   else
     e = enc::launch_scored_simt(s, qkv, vl, ctx, lse, sh, h->dtype == ENC_FP16, st);
@@ -560,21 +568,39 @@ enc_status make_scores(enc_handle* h, const enc_scores* p, enc::ScoreArgs& s) {
   return ENC_OK;
 }
 
-// Scratch of the backward pass: the row statistics and the counter (of either kernels), then
-// each query block's sums of the table's gradient (for the smallest block and
-// the largest table, or the sums by distance).
-size_t scored_rows_bytes(const enc_handle* h, int batch, int seq) {
-  return align_up(std::max(((size_t)batch * seq * h->nh + 1) * 4,
-                           enc::scored_backward_tc_scratch(enc::ScoredShape{batch, seq, h->nh, h->d})), 256);
+// Scratch of a backward call: the row statistics and the counter (the short kernel has none), then, where the table's
+// gradient is asked for (buckets > 0), the sums of each query block, or the short kernel's sums by distance.
+struct ScoredScratch {
+  size_t rows, total;       // bytes of the former, and of both
+};
+ScoredScratch scored_scratch(ScoredPath path, const enc::ScoredShape& sh, int buckets) {
+  const size_t items = (size_t)sh.batch * sh.head_num;
+  auto sums = [&](int rows) { return items * (((size_t)sh.seq + rows - 1) / rows) * buckets * 4; };
+  size_t rows = 0, partial = 0;
+  switch (path) {
+    case ScoredPath::kShort: partial = buckets ? items * 256 * 4 : 0; break;
+    case ScoredPath::kTc:
+      rows = enc::scored_backward_tc_scratch(sh);
+      partial = sums(enc::kScoredTcRows);
+      break;
+    case ScoredPath::kSimt:
+      rows = (items * sh.seq + 1) * 4;
+      partial = sums(enc::kScoredSimtRows);
+      break;
+  }
+  rows = align_up(rows, 256);
+  return {rows, rows + partial};
 }
-size_t scored_ws_bytes(const enc_handle* h, int batch, int seq) {
-  const size_t blocks = ((size_t)seq + enc::kScoredSimtRows - 1) / enc::kScoredSimtRows;
-  return scored_rows_bytes(h, batch, seq) +
-         (size_t)batch * h->nh * std::max<size_t>(256, blocks * enc::kMaxScoreBuckets) * 4;
+// For any call at that shape, whatever the options.
+size_t scored_reserve_bytes(const enc::ScoredShape& sh) {
+  size_t most = 0;
+  for (ScoredPath path : {ScoredPath::kShort, ScoredPath::kTc, ScoredPath::kSimt})
+    if (path != ScoredPath::kShort || sh.seq <= enc::kScoredShort)
+      most = std::max(most, scored_scratch(path, sh, enc::kMaxScoreBuckets).total);
+  return most;
 }
 
-enc_status ensure_scored_ws(enc_handle* h, int batch, int seq, bool have_stream, cudaStream_t st) {
-  const size_t need = scored_ws_bytes(h, batch, seq);
+enc_status ensure_scored_ws(enc_handle* h, size_t need, bool have_stream, cudaStream_t st) {
   if (need <= h->scored_ws_bytes) return ENC_OK;
   if (have_stream) {
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
@@ -1578,7 +1604,7 @@ enc_status enc_reserve_scored(enc_t h, int batch, int seq) {
   if (s != ENC_OK) return s;
   if ((s = check_tokens(batch, seq)) != ENC_OK) return s;
   if (seq > enc::kMaxScoreSeq) return fail(ENC_ERR_UNSUPPORTED, "seq %d exceeds %d", seq, enc::kMaxScoreSeq);
-  if ((s = ensure_scored_ws(h, batch, seq, false, nullptr)) != ENC_OK) return s;
+  if ((s = ensure_scored_ws(h, scored_reserve_bytes({batch, seq, h->nh, h->d}), false, nullptr)) != ENC_OK) return s;
   return ok();
 }
 
@@ -1612,20 +1638,21 @@ enc_status enc_op_scored_attention_backward(enc_t h, const enc_scores* scores, c
   if (overlap(dqkv, 3 * act, qkv, 3 * act) || overlap(dqkv, 3 * act, ctx, act) || overlap(dqkv, 3 * act, dctx, act))
     return fail(ENC_ERR_INVALID_ARG, "dqkv overlaps an input");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if ((s = ensure_scored_ws(h, batch, seq, true, st)) != ENC_OK) return s;
-  float* partial =
-      dtable ? reinterpret_cast<float*>(static_cast<char*>(h->scored_ws) + scored_rows_bytes(h, batch, seq)) : nullptr;
   const enc::ScoredShape sh{batch, seq, h->nh, h->d};
+  const ScoredPath path = scored_path(h, seq);
+  const ScoredScratch scratch = scored_scratch(path, sh, dtable ? a.buckets : 0);
+  if ((s = ensure_scored_ws(h, scratch.total, true, st)) != ENC_OK) return s;
+  float* partial = dtable ? reinterpret_cast<float*>(static_cast<char*>(h->scored_ws) + scratch.rows) : nullptr;
   cudaError_t e;
   int rows, short_ctas = 0;                                // of a query block of `partial`
-  if (h->dtype == ENC_FP16 && h->tc_attn && seq <= enc::kScoredShort) {
+  if (path == ScoredPath::kShort) {
     rows = enc::kScoredShort;
     short_ctas = enc::scored_short_ctas(sh, h->num_sms);
     e = enc::launch_scored_backward_tc_short(a, static_cast<const __half*>(qkv), valid_len,
                                              static_cast<const __half*>(ctx), lse, static_cast<const __half*>(dctx),
                                              static_cast<__half*>(dqkv), partial, sh, h->status, h->num_sms, st);
     if (e == cudaSuccess) h->launches += 1;
-  } else if (h->dtype == ENC_FP16 && h->tc_attn) {
+  } else if (path == ScoredPath::kTc) {
     rows = enc::kScoredTcRows;
     e = enc::launch_scored_backward_tc(a, static_cast<const __half*>(qkv), valid_len, static_cast<const __half*>(ctx),
                                        lse, static_cast<const __half*>(dctx), static_cast<__half*>(dqkv), partial,
