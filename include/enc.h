@@ -444,6 +444,8 @@ ENC_API enc_status enc_op_ffn2_ln(enc_t h, int layer, const void* u, const void*
  *   j < prefix_len[b]), and doc_ids[b][i] == doc_ids[b][j];
  *   ctx_i = sum over the visible keys of softmax_j(t) v_j,
  *   lse_i = log(sum over the visible keys of exp(t)).
+ * Whatever a call of this section writes may not overlap anything else that it
+ * is given (ENC_ERR_INVALID_ARG).
  * A row that sees no key, and every row i >= n, has ctx = 0 and lse = -infinity.
  * (enc_op_attention without enc_set_scores computes rows i >= n like the others.)
  * What q, k, v and dctx hold in rows i >= n is never used.  Rows below n hold
@@ -518,8 +520,7 @@ ENC_API enc_status enc_op_scored_attention(enc_t h, const enc_scores* scores, co
  * The same result on every run (no atomic additions).  FP16 mode accumulates in
  * FP32 and rounds P and dU to FP16 for the products; dU is scaled by a power of
  * two per (sequence, head) first, taken from the norms of dctx and v, so that
- * neither small nor large gradients leave FP16's range.  dqkv may not overlap
- * qkv, ctx or dctx.  Asynchronous. */
+ * neither small nor large gradients leave FP16's range.  Asynchronous. */
 ENC_API enc_status enc_op_scored_attention_backward(enc_t h, const enc_scores* scores, const void* qkv,
                                                     const int32_t* valid_len, const void* ctx, const float* lse,
                                                     const void* dctx, void* dqkv, float* dtable, int batch, int seq,

@@ -242,3 +242,56 @@ def test_reserved_scratch_serves_every_call_of_its_shape(s, mode):
         assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
         assert held_outside_torch() == held
     enc.close()
+
+
+# ---------------------------------------------------------------- buffers that overlap
+@pytest.mark.parametrize("mode", ["fp16", "fp32"])
+def test_overlaps_are_refused(mode):
+    """Whatever a call writes may not lie over what it reads, or over what else it writes."""
+    b, nh, s, d = 2, 4, 16, 32
+    enc = encoder(nh, d, mode)
+    lib, st = enc.lib, torch.cuda.current_stream().cuda_stream
+    size = 2 if mode == "fp16" else 4
+    act, stat = b * s * nh * d * size, b * s * nh * 4
+    names = dict(qkv=3 * act, ctx=act, dctx=act, dqkv=3 * act, lse=stat, valid=4 * b, slopes=4 * nh, table=16 * nh * 4,
+                 dtable=16 * nh * 4, prefix=4 * b, docs=4 * b * s, cache=2 * act // s * 3, new=3 * act // s)
+    step = dict(names, ctx=act // s, docs=4 * b * 3)
+    block = torch.zeros(sum(-(-n // 256) * 256 for n in names.values()), dtype=torch.uint8, device="cuda")
+    at, place = block.data_ptr(), {}
+    for name, n in names.items():
+        place[name] = at
+        at += -(-n // 256) * 256
+
+    def call(op, **moved):
+        p = dict(place, **moved)
+        sc = Scores(causal=True)
+        c = sc.c
+        c.slopes, c.bias_table, c.num_buckets, c.max_distance = p["slopes"], p["table"], 16, 128
+        c.prefix_len, c.doc_ids = p["prefix"], p["docs"]
+        if op == "forward":
+            return lib.enc_op_scored_attention(enc.handle, sc.pointer, p["qkv"], p["valid"], p["ctx"], p["lse"], b, s, st)
+        if op == "backward":
+            return lib.enc_op_scored_attention_backward(enc.handle, sc.pointer, p["qkv"], p["valid"], p["ctx"], p["lse"],
+                                                        p["dctx"], p["dqkv"], p["dtable"], b, s, st)
+        return lib.enc_op_scored_attention_step(enc.handle, sc.pointer, p["new"], p["cache"], p["valid"], p["ctx"], b, 3, st)
+
+    scores = ["slopes", "table", "prefix", "docs"]
+    uses = dict(forward=(["ctx", "lse"], ["qkv", "valid"] + scores),
+                backward=(["dqkv", "dtable"], ["qkv", "ctx", "dctx", "lse", "valid"] + scores),
+                step=(["cache", "ctx"], ["new", "valid"] + scores))
+    before = enc.launch_count()
+    for op, (written, read) in uses.items():
+        sizes = step if op == "step" else names
+        for i, w in enumerate(written):
+            for o in read + written[:i]:
+                start = place[o] + (sizes[o] - 1) // 16 * 16  # over the last bytes of o
+                assert call(op, **{w: start}) == 1, (op, w, o)
+                assert "overlaps" in lib.enc_last_error().decode()
+                if w in ("ctx", "lse", "dtable"):             # and o over the last bytes of w
+                    start = place[w] + (sizes[w] - 1) // 16 * 16
+                    assert call(op, **{o: start}) == 1, (op, o, w)
+    assert enc.launch_count() == before
+    for op in uses:
+        assert call(op) == 0
+    torch.cuda.synchronize()
+    assert enc.device_status() == 0

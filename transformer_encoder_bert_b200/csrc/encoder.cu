@@ -513,9 +513,34 @@ enc_status check_scored_forward(const enc_handle* h, int seq) {
   return ENC_OK;
 }
 
-bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
-  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
-  return x < y + b_bytes && y < x + a_bytes;
+// Buffers of a call (nullptr: not given).
+struct Buffer {
+  const char* name;
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Buffer& a, const Buffer& b) {
+  const char *x = static_cast<const char*>(a.p), *y = static_cast<const char*>(b.p);
+  return x && y && x < y + b.bytes && y < x + a.bytes;
+}
+// What a scored call writes lies apart from all else that it names, the arrays of its scores (doc_ids [batch, seq])
+// included.
+enc_status check_apart(const enc_handle* h, const enc::ScoreArgs& s, int batch, int seq,
+                       std::initializer_list<Buffer> written, std::initializer_list<Buffer> read) {
+  const size_t nh = h->nh, b = batch;
+  const Buffer arrays[] = {{"slopes", s.slopes, nh * 4},
+                           {"bias_table", s.table, (size_t)s.buckets * nh * 4},
+                           {"prefix_len", s.prefix, b * 4},
+                           {"doc_ids", s.docs, b * seq * 4}};
+  for (auto w = written.begin(); w != written.end(); ++w) {
+    auto meets = [&](const Buffer& o) { return overlap(*w, o) ? fail(ENC_ERR_INVALID_ARG, "%s overlaps %s", w->name, o.name) : ENC_OK; };
+    enc_status st = ENC_OK;
+    for (auto o = written.begin(); o != w && st == ENC_OK; ++o) st = meets(*o);
+    for (auto o = read.begin(); o != read.end() && st == ENC_OK; ++o) st = meets(*o);
+    for (auto o = std::begin(arrays); o != std::end(arrays) && st == ENC_OK; ++o) st = meets(*o);
+    if (st != ENC_OK) return st;
+  }
+  return ENC_OK;
 }
 
 // Checks an enc_scores and lays it out for the kernels.
@@ -1617,7 +1642,10 @@ enc_status enc_op_scored_attention(enc_t h, const enc_scores* scores, const void
   if ((s = check_ptrs({qkv, ctx})) != ENC_OK) return s;
   if (!valid_len) return fail(ENC_ERR_INVALID_ARG, "valid_len is null");
   const size_t act = (size_t)batch * seq * h->H * h->esize;
-  if (overlap(ctx, act, qkv, 3 * act)) return fail(ENC_ERR_INVALID_ARG, "ctx overlaps qkv");
+  const size_t stat = (size_t)batch * seq * h->nh * 4;
+  if ((s = check_apart(h, a, batch, seq, {{"ctx", ctx, act}, {"lse", lse, stat}},
+                       {{"qkv", qkv, 3 * act}, {"valid_len", valid_len, (size_t)batch * 4}})) != ENC_OK)
+    return s;
   if ((s = step_scored(h, a, qkv, valid_len, ctx, lse, batch, seq, reinterpret_cast<cudaStream_t>(stream))) != ENC_OK)
     return s;
   return ok();
@@ -1635,8 +1663,11 @@ enc_status enc_op_scored_attention_backward(enc_t h, const enc_scores* scores, c
   if (!valid_len || !lse) return fail(ENC_ERR_INVALID_ARG, "valid_len or lse is null");
   if (dtable && !a.table) return fail(ENC_ERR_INVALID_ARG, "dtable without a bias_table");
   const size_t act = (size_t)batch * seq * h->H * h->esize;
-  if (overlap(dqkv, 3 * act, qkv, 3 * act) || overlap(dqkv, 3 * act, ctx, act) || overlap(dqkv, 3 * act, dctx, act))
-    return fail(ENC_ERR_INVALID_ARG, "dqkv overlaps an input");
+  const size_t stat = (size_t)batch * seq * h->nh * 4;
+  if ((s = check_apart(h, a, batch, seq, {{"dqkv", dqkv, 3 * act}, {"dtable", dtable, (size_t)a.buckets * h->nh * 4}},
+                       {{"qkv", qkv, 3 * act}, {"ctx", ctx, act}, {"dctx", dctx, act}, {"lse", lse, stat},
+                        {"valid_len", valid_len, (size_t)batch * 4}})) != ENC_OK)
+    return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const enc::ScoredShape sh{batch, seq, h->nh, h->d};
   const ScoredPath path = scored_path(h, seq);
@@ -1687,9 +1718,9 @@ enc_status enc_op_scored_attention_step(enc_t h, const enc_scores* scores, const
   if ((s = check_ptrs({qkv, cache, ctx})) != ENC_OK) return s;
   if (!len) return fail(ENC_ERR_INVALID_ARG, "len is null");
   const size_t act = (size_t)batch * h->H * h->esize;
-  if (overlap(ctx, act, qkv, 3 * act) || overlap(cache, 2 * act * capacity, qkv, 3 * act) ||
-      overlap(cache, 2 * act * capacity, ctx, act))
-    return fail(ENC_ERR_INVALID_ARG, "qkv, cache and ctx overlap");
+  if ((s = check_apart(h, a, batch, capacity, {{"cache", cache, 2 * act * capacity}, {"ctx", ctx, act}},
+                       {{"qkv", qkv, 3 * act}, {"len", len, (size_t)batch * 4}})) != ENC_OK)
+    return s;
   const enc::ScoredShape sh{batch, capacity, h->nh, h->d};
   cudaError_t e = enc::launch_scored_step(a, qkv, cache, len, ctx, sh, h->dtype == ENC_FP16, h->num_sms,
                                           reinterpret_cast<cudaStream_t>(stream));
