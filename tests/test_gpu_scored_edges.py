@@ -295,3 +295,43 @@ def test_overlaps_are_refused(mode):
         assert call(op) == 0
     torch.cuda.synchronize()
     assert enc.device_status() == 0
+
+
+# ---------------------------------------------------------------- tensors that a caller lets go of
+@pytest.mark.parametrize("how", ["forward", "host_async"])
+@pytest.mark.parametrize("as_handle", [False, True], ids=["stream", "handle"])
+def test_scores_outlive_forwards_in_flight(as_handle, how):
+    """Replacing the scores while a forward on another stream still waits does not give their memory to the next tensor."""
+    nh, d, b, s = 4, 32, 2, 40
+    inp = EI.make_inputs(EI.Workload("stack", EI.EncoderShape(nh, d, 64, 2), b, s, "fp16", s, s, seed=1))
+    enc = encoder_from_inputs(inp)
+    x, vl = to_dev(inp.x), to_dev(np.asarray(inp.valid_len, np.int32))
+    want = enc.forward(x, vl)
+    out, side = torch.empty_like(x), torch.cuda.Stream()
+    host = [t.cpu().pin_memory() for t in (x, vl, out)]
+    table = torch.zeros((32, nh), device="cuda")              # (zeros: the scores stay the plain ones)
+    docs = torch.zeros((b, s), dtype=torch.int32, device="cuda")
+    places = {table.data_ptr(), docs.data_ptr()}
+    sc = Scores(table=table, doc_ids=docs)
+    enc.set_scores(sc)
+    enc.forward(x, vl)                                        # (everything is loaded and allocated)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)                        # about 0.2 s
+    st = side.cuda_stream if as_handle else side
+    if how == "forward":
+        enc.forward(x, vl, out=out, stream=st)
+    else:
+        enc.forward_host_async_ptr(*(t.data_ptr() for t in host), b, s, stream=st)
+        enc.host_join(st)
+    enc.set_scores(None)
+    busy = not side.query()
+    del sc, table, docs
+    fresh = [torch.empty((32, nh), device="cuda") for _ in range(8)] + [torch.empty((b, s), device="cuda") for _ in range(8)]
+    assert busy and not side.query()
+    assert places.isdisjoint(t.data_ptr() for t in fresh)
+    torch.cuda.synchronize()
+    got = (host[2] if how == "host_async" else out).float().cpu().numpy()
+    assert np.abs(got - want.float().cpu().numpy()).max() < 0.05
+    assert enc.device_status() == 0
+    enc.close()

@@ -92,7 +92,10 @@ class Scores:
     1/sqrt(size_per_head)), a tanh cap (0 = none), slopes [head_num] of a linear distance
     bias, a table [num_buckets, head_num] of relative position biases, a causal mask with
     prefix_len [batch], doc_ids [batch, seq].  slopes and table are CUDA float32 tensors,
-    prefix_len and doc_ids CUDA int32 tensors; they are kept alive by this object."""
+    prefix_len and doc_ids CUDA int32 tensors; they are kept alive by this object, and their
+    memory is not handed out again before the forwards that Encoder.set_scores runs with them
+    have ended, on whatever stream (a graph that the caller captures itself reads them at
+    every replay: keep the object as long)."""
 
     def __init__(self, scale: Optional[float] = None, cap: float = 0.0, slopes=None, table=None,
                  max_distance: int = 128, bidirectional: bool = True, causal: bool = False, prefix_len=None,
@@ -100,6 +103,7 @@ class Scores:
         self.slopes, self.table, self.prefix_len, self.doc_ids = slopes, table, prefix_len, doc_ids
         self.devices = {t.get_device() for t in (slopes, table, prefix_len, doc_ids) if t is not None
                         and hasattr(t, "get_device")}
+        self._streams: set = set()
         self.c = EncScores(scale=0.0 if scale is None else scale, cap=cap, slopes=_typed_ptr(slopes, "float32", 1),
                            bias_table=_typed_ptr(table, "float32", 2),
                            num_buckets=0 if table is None else table.shape[0],
@@ -121,6 +125,17 @@ class Scores:
             raise ValueError(f"prefix_len has shape {tuple(self.prefix_len.shape)}, expected {(batch,)}")
         if self.doc_ids is not None and tuple(self.doc_ids.shape) != (batch, seq):
             raise ValueError(f"doc_ids has shape {tuple(self.doc_ids.shape)}, expected {(batch, seq)}")
+
+    def used_on(self, stream: Optional[int]):
+        """Tell PyTorch's allocator that work on this stream (a handle; None or 0: the default one) reads the tensors."""
+        if stream in self._streams:
+            return
+        import torch
+        st = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        for t in (self.slopes, self.table, self.prefix_len, self.doc_ids):
+            if t is not None:
+                t.record_stream(st)
+        self._streams.add(stream)
 
     @property
     def pointer(self) -> int:
@@ -300,7 +315,7 @@ class Encoder:
         """x: CUDA [B, S, H] tensor in the storage dtype; valid_len: CUDA int32 [B]."""
         import torch
         B, S, H = x.shape
-        self._check_scores(B, S)
+        self._check_scores(B, S, stream)
         if out is None:
             out = torch.empty_like(x)
         _check(self.lib.enc_forward(self.handle, _dptr(x), _dptr(valid_len), _dptr(out), B, S,
@@ -311,7 +326,7 @@ class Encoder:
         """enc_forward_noalloc: the forward with its scratch in the library's fixed
         device array (no device allocation); out must be given."""
         B, S, H = x.shape
-        self._check_scores(B, S)
+        self._check_scores(B, S, stream)
         _check(self.lib.enc_forward_noalloc(self.handle, _dptr(x), _dptr(valid_len), _dptr(out), B, S,
                                             _current_stream(stream)))
         return out
@@ -324,20 +339,20 @@ class Encoder:
         if out is None:
             out = np.empty_like(x)
         B, S, _ = x.shape
-        self._check_scores(B, S)
+        self._check_scores(B, S, stream)
         _check(self.lib.enc_forward_host(self.handle, x.ctypes.data, vl.ctypes.data, out.ctypes.data,
                                          B, S, _current_stream(stream)))
         return out
 
     def forward_host_ptr(self, x_ptr: int, vl_ptr: int, out_ptr: int, batch: int, seq: int, stream=None):
         """enc_forward_host on raw host pointers (e.g. pinned torch tensors)."""
-        self._check_scores(batch, seq)
+        self._check_scores(batch, seq, stream)
         _check(self.lib.enc_forward_host(self.handle, x_ptr, vl_ptr, out_ptr, batch, seq,
                                          _current_stream(stream)))
 
     def forward_host_async_ptr(self, x_ptr: int, vl_ptr: int, out_ptr: int, batch: int, seq: int, stream=None):
         """enc_forward_host_async on raw (pinned) host pointers; see host_join."""
-        self._check_scores(batch, seq)
+        self._check_scores(batch, seq, stream)
         _check(self.lib.enc_forward_host_async(self.handle, x_ptr, vl_ptr, out_ptr, batch, seq,
                                                _current_stream(stream)))
 
@@ -348,7 +363,7 @@ class Encoder:
     def record(self, x, valid_len, out) -> "RecordedForward":
         """Record one forward on these CUDA tensors as a CUDA graph (see enc_graph_create)."""
         B, S, _ = x.shape
-        self._check_scores(B, S)
+        self._check_scores(B, S, record=True)
         g = ctypes.c_void_p()
         _check(self.lib.enc_graph_create(self.handle, _dptr(x), _dptr(valid_len), _dptr(out), B, S,
                                          ctypes.byref(g)))
@@ -392,7 +407,7 @@ class Encoder:
         _check(self.lib.enc_op_qkv(self.handle, layer, _dptr(x), _dptr(qkv), batch, seq, _current_stream(stream)))
 
     def op_attention(self, qkv, valid_len, ctx, batch: int, seq: int, stream=None):
-        self._check_scores(batch, seq)
+        self._check_scores(batch, seq, stream)
         _check(self.lib.enc_op_attention(self.handle, _dptr(qkv), _dptr(valid_len), _dptr(ctx), batch, seq,
                                          _current_stream(stream)))
 
@@ -413,10 +428,12 @@ class Encoder:
     def _act(self) -> str:
         return "float16" if self.dtype == "fp16" else "float32"
 
-    def _check_scores(self, batch: int, seq: int):
-        """The tensors of set_scores against the batch and seq of a forward."""
+    def _check_scores(self, batch: int, seq: int, stream=None, record: bool = False):
+        """The tensors of set_scores against the batch and seq of a forward on that stream."""
         if self._scores_keep is not None:
             self._scores_keep.check(self.head_num, self._device(), batch, seq)
+            if not record:
+                self._scores_keep.used_on(_current_stream(stream))
 
     def _device(self) -> int:
         """The current device, which must be the handle's (the library checks that)."""
