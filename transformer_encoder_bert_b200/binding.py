@@ -103,6 +103,9 @@ class Scores:
         self.slopes, self.table, self.prefix_len, self.doc_ids = slopes, table, prefix_len, doc_ids
         self.devices = {t.get_device() for t in (slopes, table, prefix_len, doc_ids) if t is not None
                         and hasattr(t, "get_device")}
+        for name, value, meant in (("scale", scale, "None is 1/sqrt(size_per_head)"), ("cap", cap or None, "0 is none")):
+            if value is not None and ctypes.c_float(value).value == 0:       # (what the struct's 0 stands for)
+                raise ValueError(f"{name} {value} is zero as a float32; {meant}")
         self._streams: set = set()
         self.c = EncScores(scale=0.0 if scale is None else scale, cap=cap, slopes=_typed_ptr(slopes, "float32", 1),
                            bias_table=_typed_ptr(table, "float32", 2),
