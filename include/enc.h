@@ -518,9 +518,9 @@ ENC_API enc_status enc_op_scored_attention(enc_t h, const enc_scores* scores, co
  *   dtable FP32 [num_buckets, head_num], or NULL: the sum of dT over the batch
  *     and every (i, j) of the bucket (overwritten, not added to).
  * The same result on every run (no atomic additions).  FP16 mode accumulates in
- * FP32 and rounds P and dU to FP16 for the products; dU is scaled by a power of
- * two per (sequence, head) first, taken from the norms of dctx and v, so that
- * neither small nor large gradients leave FP16's range.  Asynchronous. */
+ * FP32 and rounds P and dU to FP16 for the products; P is scaled by 2^13 first,
+ * dU by a power of two per (sequence, head) taken from the norms of dctx and v, so
+ * that neither small nor large weights and gradients leave FP16's range.  Asynchronous. */
 ENC_API enc_status enc_op_scored_attention_backward(enc_t h, const enc_scores* scores, const void* qkv,
                                                     const int32_t* valid_len, const void* ctx, const float* lse,
                                                     const void* dctx, void* dqkv, float* dtable, int batch, int seq,

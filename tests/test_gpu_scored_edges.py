@@ -335,3 +335,37 @@ def test_scores_outlive_forwards_in_flight(as_handle, how):
     assert np.abs(got - want.float().cpu().numpy()).max() < 0.05
     assert enc.device_status() == 0
     enc.close()
+
+
+# ---------------------------------------------------------------- small weights
+def seldom_attended(mode, d, s, bits, v=1.0, do=1.0):
+    """Key 0 takes nearly all of every row, the others about 2^-bits each."""
+    b, nh = 2, 2
+    c = Case("plain", mode, b, nh, s, d, seed=35, valid=[s, s - 9])
+    c.spec.scale = 1.0
+    c.qkv[:2] *= 0.01
+    c.qkv[:2, ..., 0] = 0
+    c.qkv[0, ..., 0] = 1
+    c.qkv[1, :, :, 0, 0] = bits * np.log(2)
+    c.qkv[2] = (np.abs(c.qkv[2]) + 1).astype(c.qkv.dtype) * c.qkv.dtype.type(v)
+    c.qkv[2, :, :, 0] = 0
+    c.dctx = (np.abs(c.dctx) + 1).astype(c.dctx.dtype) * c.dctx.dtype.type(do)
+    return c
+
+
+@pytest.mark.parametrize("mode", ["fp16", "fp16-simt", "fp32"])
+@pytest.mark.parametrize("bits", [16, 22, 26])
+@pytest.mark.parametrize("d,s", [(64, 100), (64, 300), (32, 300), (128, 128), (128, 300)], ids=str)
+def test_gradient_of_seldom_attended_keys(d, s, bits, mode):
+    """dv of keys whose weights are far below FP16's smallest numbers."""
+    c = seldom_attended(mode, d, s, bits, do=500.0)
+    ctx, lse = c.forward()
+    dqkv, _ = c.backward(ctx, lse)
+    ref, _, (p, _, _) = SO.backward(c.spec, c.qkv, c.valid, c.shaped(ctx), lse.cpu().numpy().astype(np.float64), c.dctx)
+    # t is below 20 and off by (d + 8) 2^-23 of that or less, 2^-21 more for its log2 form and the exponential; a weight
+    # is rounded once (2^-11) in FP16 mode, as 2^13 of itself, which is 2^-13 or more here; all terms have one sign.
+    half = mode.startswith("fp16")
+    rel = 20 * (d + 8) * 2.0 ** -23 + 20 * 2.0 ** -22 + s * 2.0 ** -23 + (2.0 ** -10 if half else 2.0 ** -23)
+    got, want = dqkv[2, :, :, 1:].cpu().numpy(), ref[2][:, :, 1:]       # (key 0's own sum may pass 65504)
+    err = np.abs(got - want)
+    assert (err <= rel * np.abs(want) + (2.0 ** -25 if half else 0)).all(), (err / (np.abs(want) + 1e-30)).max()

@@ -195,6 +195,13 @@ __device__ __forceinline__ uint64_t small_cap2(const ScoreArgs& s, uint64_t x) {
   for (int k = 3; k >= 0; --k) p = f2_fma(p, z, f2_pack(s.cap_small[k], s.cap_small[k]));
   return f2_mul(x, p);
 }
+// The backward's P, at most 1, is rounded to FP16 for dV = P^T dO as P 2^13: otherwise a weight below 2^-14 would lose
+// digits, and one below 2^-25 would be nothing, which is all that a key gets that is seldom attended to.  The statistics
+// hold 13 - lse2, dU's scale takes the factor back, and dV's output does; the three bits left allow for a P above 1 by
+// the rounding of large scores.
+constexpr int kPBits = 13;
+constexpr float kPScale = 1 << kPBits, kPInverse = 1.f / kPScale;
+
 // What a kernel does about the cap (its template argument).
 constexpr int kNoCap = 0, kCap = 1, kLargeCap = 2;
 inline int cap_kind(const ScoreArgs& s) { return s.cap > kCapCoarse ? kLargeCap : s.cap > 0.f ? kCap : kNoCap; }

@@ -20,7 +20,7 @@
 // the columns to a thread shorten it.  Heads of 128 fill the TMEM with one CTA:
 // its warpgroups take the blocks in turn, each with S and dP columns of its own.
 //
-// P and dU are rounded to FP16 for the products.  P is at most 1.  dU is scaled
+// P and dU are rounded to FP16 for the products, P as P 2^13 (kPBits).  dU is scaled
 // by a power of two e per (sequence, head): |dT| <= 2 max|dO_i| max|v_j|, and e
 // puts that product of norms between 2^13 and 2^14, so that no dU leaves FP16's
 // range and small gradients keep their bits.  e is exact and is taken out of
@@ -60,7 +60,7 @@ struct BCfg {
   static constexpr int kStages = 3;
   static constexpr int kStage = 2 * kBBytes;
   static constexpr int kB = 2 * kABytes;
-  static constexpr int kCol = kB + kStages * kStage;       // dKV: -lse2 and D of a block's queries, per stage
+  static constexpr int kCol = kB + kStages * kStage;       // dKV: kPBits - lse2 and D of a block's queries, per stage
   static constexpr int kColBytes = 2 * kBN * 4;
   static constexpr int kBars = kCol + (MODE == kDKV ? kStages * kColBytes : 0);
   // a_full, drain, b_full, b_empty (kStages each), s_full, p_full, done (NB each)
@@ -81,11 +81,11 @@ struct BCfg {
 // One row's block of 64 columns, 32 at a time: from S and dP to P and dU.
 struct RowBlock {
   uint32_t t_s, t_dp;       // TMEM addresses of the row warp's S and dP columns
-  float base, step;         // bias (less lse2 in dQ mode): base, base + step * column, or base + lut
+  float base, step;         // bias (plus kPBits - lse2 in dQ mode): base, base + step * column, or base + lut
   const float* lut;         // at column 0
   uint32_t see[2];          // bits: visible columns
-  float e, de;              // dU's scale, and D e (dQ mode)
-  const float* col;         // dKV mode: -lse2 [64], D [64] of the columns (shared memory)
+  float e, de;              // what dT's dP - D is scaled by (dU's scale over P's), and D times that (dQ mode)
+  const float* col;         // dKV mode: kPBits - lse2 [64], D [64] of the columns (shared memory)
   int valid;                // columns that are valid positions (any number)
   bool mine;                // the row is one
   int p_at;                 // P and dU of column c go to column p_at + c / 2 (of S, of dP)
@@ -109,7 +109,7 @@ __device__ __forceinline__ void row_chunk(const ScoreArgs& s, const RowBlock& rb
   uint64_t far2 = 0;                                       // two partial sums of dT (0.0f, 0.0f)
 #pragma unroll
   for (int k = 0; k < CH; k += 4) {
-    ulonglong2 nl = make_ulonglong2(0, 0), dc = make_ulonglong2(0, 0);       // -lse2 and D of four columns
+    ulonglong2 nl = make_ulonglong2(0, 0), dc = make_ulonglong2(0, 0);       // kPBits - lse2 and D of four columns
     if (MODE == kDKV) {
       nl = *reinterpret_cast<const ulonglong2*>(rb.col + c + k);
       dc = *reinterpret_cast<const ulonglong2*>(rb.col + kBN + c + k);
@@ -517,8 +517,8 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
     RowBlock rb;
     const int doc = docs && mine ? docs[pos] : 0;
     rb.mine = mine;
-    rb.e = e;
-    rb.de = dsum * e;
+    rb.e = e * kPInverse;
+    rb.de = dsum * rb.e;
     const int buf = C::NB == 2 ? w : 0, first = C::kShare == 2 ? 32 * w : 0, last = C::kShare == 2 ? first + 32 : kBN;
     rb.t_s = t_lane + C::kS + buf * kBN;
     rb.t_dp = t_lane + C::kDP + buf * kBN;
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
 #pragma unroll 1
       for (int part = w; part < kParts; part += 2) {
         const int acc = part / C::kSub, u = part % C::kSub;                  // acc 0: dQ or dK; 1: dV
-        const float f = !mine ? 0.f : acc == 0 ? s.scale * inv_e : 1.f;
+        const float f = !mine ? 0.f : acc == 0 ? s.scale * inv_e : kPInverse;
         uint8_t* tile = smem + part * 16384 + quad * 32 * kRowBytes;
 #pragma unroll 1
         for (int c = 0; c < kCols; c += 32) {
@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(BCfg<D, MODE>::kThreads, D > 64 ? 1 : 2)
   if (MODE == kDKV) pdl_wait();
 }
 
-// Per row i: -lse in units of log2 (-inf where the row sees nothing or is past
+// Per row i: kPBits - lse in units of log2 (-inf where the row sees nothing or is past
 // n, which makes P zero) and D_i, in rows padded to Sp; per 128 rows, the
 // largest |dO_i|^2 and |v_j|^2.  D / 8 lanes read a row with 16-byte loads.
 constexpr int kStatThreads = 256;
@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(kStatThreads)
     mv = fmaxf(mv, vv);
     if (gl == 0) {
       const float l = i < n ? lse[bh * S + i] * kLog2e : -INFINITY;
-      rows2[bh * Sp + i] = l == -INFINITY ? -INFINITY : -l;
+      rows2[bh * Sp + i] = l == -INFINITY ? -INFINITY : kPBits - l;
       rows2[(planes + bh) * Sp + i] = dot;
     }
   }

@@ -56,7 +56,7 @@ struct SBCfg {
   // full, s_full, p_full, acc_full, free, group, drain
   static constexpr int kSlot = kBars + 64;
   static constexpr int kMax = kSlot + 16;                  // per row warp: norms of dO and V
-  static constexpr int kCol = kMax + 2 * kRowWarps * 4;    // -lse2 [128], D [128]
+  static constexpr int kCol = kMax + 2 * kRowWarps * 4;    // kPBits - lse2 [128], D [128]
   static constexpr int kDocs = kCol + 256 * 4;
   static constexpr int kColumn = kDocs + 128 * 4;          // the head's column of the bias table
   static constexpr int kLut = kColumn + kMaxScoreBuckets * 4;   // bias of distance k - 127
@@ -73,11 +73,11 @@ struct SBCfg {
 struct BwdChunk {
   uint32_t t_s, t_dp, t_p;  // TMEM addresses
   const float* lut;         // the row's bias at the chunk's first query; falls with the query
-  const float* col;         // -lse2 [128] and D [128] at the first query
+  const float* col;         // kPBits - lse2 [128] and D [128] at the first query
   int lo, hi;               // visible queries, as far as length and causality go
   const int* docs;          // documents of the queries, or nullptr
   int doc;
-  float e;                  // dU's scale
+  float e;                  // dU's scale over P's
   uint8_t* du;              // the row of dU^T (64 queries), and the swizzle and 16-byte unit of the chunk
   int swizzle, unit;
   int valid;                // queries that are valid positions (any number)
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
         dot += __shfl_xor_sync(0xffffffffu, dot, 1);
         float mo = oo + __shfl_xor_sync(0xffffffffu, oo, 1), mv = vv + __shfl_xor_sync(0xffffffffu, vv, 1);
         if (shalf == 0) {
-          col[srow] = l == -INFINITY ? -INFINITY : -l;
+          col[srow] = l == -INFINITY ? -INFINITY : kPBits - l;
           col[128 + srow] = dot;
         }
 #pragma unroll
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
       const int ilow_all = max(score_ilow(s, w1, prefix), ilow_first);
       BwdChunk ch;
       ch.doc = s.docs ? pos_docs[r] : 0;
-      ch.e = e;
+      ch.e = e * kPInverse;
       ch.swizzle = r & 7;
       if (!(ok = warp_wait(s_full, ph))) break;
       tc_fence_after();
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, SBCfg<D>::kCtasPerSm)
 #pragma unroll 1
       for (int piece = w; piece < kPieces; piece += 2) {
         const int part = piece / (D / 32), c = piece % (D / 32) * 32;        // 0: dQ, 1: dK, 2: dV
-        const float f = !mine ? 0.f : part == 2 ? 1.f : s.scale * inv_e;
+        const float f = !mine ? 0.f : part == 2 ? kPInverse : s.scale * inv_e;
         uint32_t oa[32];
         tmem_ld_32x32b_x32(t_row + (part == 0 ? C::kDQ : part == 1 ? C::kDK : C::kDV) + c, oa);
         uint8_t* tile = smem + C::kDU + warp * 4096 + ((piece >> 1) & 1) * 2048;
