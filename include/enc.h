@@ -500,7 +500,8 @@ ENC_API enc_status enc_reserve_scored(enc_t h, int batch, int seq);
  *   int32 [batch]; ctx [batch * seq, H]; lse device FP32 [batch, head_num, seq]
  *   (natural logarithm), or NULL.  seq <= 65536.  qkv and ctx 16-byte aligned.
  * Accumulation, softmax and lse in FP32; FP16 mode rounds the unnormalised
- * probabilities to FP16 before the product with V, as enc_op_attention does, and
+ * probabilities to FP16 before the product with V, as enc_op_attention does
+ * (scaled, so that those down to 2^-32 of the row's largest count), and
  * its tanh is an approximation: up to a cap of 64 it moves a score by up to
  * cap 2^-21, with larger caps by up to 2^-20 of the capped score.
  * Asynchronous. */

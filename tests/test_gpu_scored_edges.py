@@ -369,3 +369,35 @@ def test_gradient_of_seldom_attended_keys(d, s, bits, mode):
     got, want = dqkv[2, :, :, 1:].cpu().numpy(), ref[2][:, :, 1:]       # (key 0's own sum may pass 65504)
     err = np.abs(got - want)
     assert (err <= rel * np.abs(want) + (2.0 ** -25 if half else 0)).all(), (err / (np.abs(want) + 1e-30)).max()
+
+
+@pytest.mark.parametrize("mode", ["fp16", "fp32"])
+@pytest.mark.parametrize("d,s,bits", [(64, 128, 20), (64, 16384, 25.7), (128, 16384, 25.7), (32, 9000, 25.7)], ids=str)
+def test_many_small_weights_add_up(d, s, bits, mode):
+    """Weights that FP16 would round to nothing beside the row's largest, which has a v of 0."""
+    b, nh = 1, 2
+    enc = encoder(nh, d, mode)
+    dt = torch.float16 if mode == "fp16" else torch.float32
+    qkv = torch.zeros((3, b, nh, s, d), dtype=dt, device="cuda")
+    qkv[0, ..., 0] = 1
+    qkv[1, :, :, 0, 0] = bits * np.log(2)
+    qkv[2] = torch.linspace(1, 2, d, device="cuda").to(dt)
+    qkv[2, :, :, 0] = 0
+    ctx, lse = torch.empty((b * s, nh * d), dtype=dt, device="cuda"), torch.empty((b, nh, s), device="cuda")
+    enc.op_scored_attention(Scores(scale=1.0), qkv, torch.tensor([s], dtype=torch.int32, device="cuda"), ctx, b, s, lse=lse)
+    assert enc.device_status() == 0
+    w = np.exp(-float(qkv[1, 0, 0, 0, 0]))
+    v = qkv[2, 0, 0, 1].double().cpu().numpy()
+    ref = (s - 1) * w / (1 + (s - 1) * w) * v
+    got = ctx.double().cpu().numpy().reshape(s, nh, d)
+    # FP16: a weight of 2^-25.7 is 2^-18.7 as it is rounded, to a multiple of 2^-24: off by 2^-25, a 75th of it (of 2^-20,
+    # 2^-5, by 2^-11); and the result is rounded once (2^-25 below 2^-14).  t: one product of a value below 18, 2^-22
+    # for its log2 form and 2^-22 for the exponential; sums of s equal terms: s 2^-24.
+    if mode == "fp16":
+        rel = (2.0 ** -25 / 2.0 ** -18.8 if bits > 25 else 2.0 ** -11) + 2.0 ** -11 + 2.0 ** -17 + s * 2.0 ** -24
+        tol = rel * ref + 2.0 ** -25
+    else:
+        tol = (2.0 ** -17 + s * 2.0 ** -24) * ref
+    assert (np.abs(got - ref) <= tol).all(), (np.abs(got - ref) / tol).max()
+    want = float(qkv[1, 0, 0, 0, 0]) + np.log1p((s - 1) * w)
+    assert np.abs(lse.double().cpu().numpy() - want).max() <= 2.0 ** -20 * 18 + s * 2.0 ** -24

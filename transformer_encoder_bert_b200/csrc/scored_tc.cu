@@ -11,9 +11,11 @@
 // A softmax thread reads its whole row of S into registers and releases S, so
 // that the next block's S is computed during this block's exponentials; it
 // turns the row into t (scale, cap, bias, masks), takes the maximum, writes
-// P = 2^(t2 - m) as FP16 to TMEM and adds up l in FP32.  m is a reference
+// P = 2^(t2 - m + 7) as FP16 to TMEM and adds up l in FP32.  m is a reference
 // maximum: it moves only when a block exceeds it by 2^8, and then the thread
-// scales its row of O first.  O / l does not depend on m.
+// scales its row of O first.  O / l does not depend on m.  The 7 uses up FP16's
+// range above 2^8: a weight below 2^-25 - 7 of the row's largest counts for
+// nothing in O, where 65,536 of them at 2^-25 would be a five-hundredth of the row.
 //
 // What bounds a block is the softmax, not the products: 8 cycles of the
 // special-function unit a score and warp, and a chain of waits and dependent
@@ -75,7 +77,8 @@ bool encode_operand_map(CUtensorMap* map, const void* base, uint64_t cols, uint6
 
 namespace {
 
-constexpr float kRescaleLog2 = 8.f;                // P < 2^8 between moves of the reference maximum
+constexpr float kRescaleLog2 = 8.f;                // 2^(t2 - m) stays below 2^8 between moves of the reference maximum
+constexpr float kRaiseLog2 = 7.f;                  // and P below 2^15
 
 constexpr int BN = 64;                             // keys of a block
 
@@ -217,7 +220,8 @@ __device__ __forceinline__ bool softmax_row(const ScoreArgs& s, const SoftmaxBlo
     sum2 = f2_mul(sum2, f2_pack(alpha, alpha));
   }
   const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-  const uint64_t neg_m2 = f2_pack(-mu, -mu);
+  const float neg_m = kRaiseLog2 - mu;
+  const uint64_t neg_m2 = f2_pack(neg_m, neg_m);
 #pragma unroll
   for (int c = 0; c < BN; c += 32) {
     uint32_t pk[16];
@@ -629,7 +633,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasP
           tma_store_3d(&tm_ctx, smem_u32(out) + u * 16384 + (warp & 3) * 32 * kRowBytes, h * D + 64 * u, row0, b);
         bulk_commit_group();
       }
-      if (lse && i < S) lse[((size_t)b * NH + h) * S + i] = seen ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+      if (lse && i < S) lse[((size_t)b * NH + h) * S + i] = seen ? (log2f(l) - (kRaiseLog2 - m_ref)) * kLn2 : -INFINITY;
       if (lane == 0) bulk_wait_group_read<0>();            // shared memory has been read
     }
   }

@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kSoftmax = 4;                                // warps
 constexpr int kThreads = 32 * (kSoftmax + 1);
+constexpr float kRaiseLog2 = 15.f;                         // P = 2^(t2 - maximum + 15), in the upper half of FP16's range
 
 template <int D>
 struct SCfg {
@@ -306,7 +307,8 @@ __global__ void __launch_bounds__(kThreads, SCfg<D>::kCtasPerSm)
         mx = 32 * c + 32 <= jall ? first_pass<CAP, BIAS, false>(s, ch, mx) : first_pass<CAP, BIAS, true>(s, ch, mx);
       }
       const float mu = mx == -INFINITY ? 0.f : mx;
-      const uint64_t neg_m2 = f2_pack(-mu, -mu);
+      const float neg_m = kRaiseLog2 - mu;
+      const uint64_t neg_m2 = f2_pack(neg_m, neg_m);
       uint64_t sum2 = 0;                                   // two partial row sums (0.0f, 0.0f)
 #pragma unroll 1
       for (int c = 0; c < stored; ++c) {
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, SCfg<D>::kCtasPerSm)
       const float l = s0 + s1;
       const bool seen = r < n && l > 0.f;
       const float inv = seen ? 1.f / l : 0.f;
-      if (lse && r < S) lse[((size_t)b * NH + h) * S + r] = seen ? (mx + log2f(l)) * kLn2 : -INFINITY;
+      if (lse && r < S) lse[((size_t)b * NH + h) * S + r] = seen ? (log2f(l) - neg_m) * kLn2 : -INFINITY;
       if (!(ok = warp_wait(o_full, ph))) break;
       tc_fence_after();
       // The row of O as FP16 into the V tile (P V has read it), in the store's swizzle.
