@@ -401,3 +401,28 @@ def test_many_small_weights_add_up(d, s, bits, mode):
     assert (np.abs(got - ref) <= tol).all(), (np.abs(got - ref) / tol).max()
     want = float(qkv[1, 0, 0, 0, 0]) + np.log1p((s - 1) * w)
     assert np.abs(lse.double().cpu().numpy() - want).max() <= 2.0 ** -20 * 18 + s * 2.0 ** -24
+
+
+# ---------------------------------------------------------------- padded rows
+@pytest.mark.parametrize("mode", ["fp16", "fp16-simt", "fp32"])
+@pytest.mark.parametrize("kind", ["cap", "table", "docs", "cap-table-shuffled", "cap-slopes-table-prefix-docs"])
+@pytest.mark.parametrize("nh,d,s,valid", [(3, 64, 70, [37, 69, 5, 16]), (2, 128, 128, [127, 65, 33, 1]), (4, 32, 100, [90, 40, 64, 0]),
+                                          (3, 64, 300, [153, 299, 5, 257]), (2, 128, 300, [130, 201, 64, 290]),
+                                          (4, 32, 200, [199, 129, 17, 0])], ids=str)
+def test_padded_rows_may_hold_anything_in_every_form(nh, d, s, valid, kind, mode):
+    """NaN and infinities in rows at or past n, and any document ids there, change no bit of any output."""
+    c = Case(kind, mode, len(valid), nh, s, d, seed=36, valid=valid)
+    ctx, lse = c.forward()
+    grads = c.backward(ctx, lse)
+    r = np.random.default_rng(37)
+    for b, n in enumerate(valid):
+        c.qkv[:, b, :, n:] = np.where(np.arange(d) % 2, np.nan, np.where(np.arange(d) % 4, np.inf, -np.inf))
+        c.dctx[b, n:] = np.where(np.arange(d) % 2, np.inf, np.nan)
+        if c.spec.doc_ids is not None:
+            c.spec.doc_ids[b, n:] = r.integers(-(2 ** 31), 2 ** 31, s - n)
+    dirty_ctx, dirty_lse = c.forward()
+    assert torch.equal(ctx, dirty_ctx) and torch.equal(lse, dirty_lse)
+    dirty = c.backward(ctx, lse)
+    assert torch.equal(grads[0], dirty[0])
+    if grads[1] is not None:
+        assert torch.isfinite(dirty[1]).all() and torch.equal(grads[1], dirty[1])
