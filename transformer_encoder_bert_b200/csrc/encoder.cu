@@ -20,6 +20,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -637,6 +638,11 @@ enc_status ensure_scored_ws(enc_handle* h, size_t need, bool have_stream, cudaSt
     if (cap != cudaStreamCaptureStatusNone)
       return fail(ENC_ERR_INVALID_ARG, "%zu bytes of scratch needed while the stream is captured: call "
                   "enc_reserve_scored first", need);
+  }
+  try {
+    h->scored_retired.reserve(h->scored_retired.size() + 1);   // before the old scratch has to go there
+  } catch (const std::bad_alloc&) {
+    return fail(ENC_ERR_OOM, "out of host memory");
   }
   void* p = nullptr;
   size_t bytes = std::max(need, 2 * h->scored_ws_bytes);   // doubling bounds what the retired ones hold
