@@ -451,6 +451,8 @@ ENC_API enc_status enc_op_ffn2_ln(enc_t h, int layer, const void* u, const void*
  * What q, k, v and dctx hold in rows i >= n is never used.  Rows below n hold
  * finite values: a key that a mask hides from a query has the weight zero there,
  * and zero times an infinity or a NaN is not zero.
+ * A bias may be -infinity, or below -2e38 (t is held as t log2 e): its keys get no
+ * weight, and a row that has no other keys counts as one that sees none.
  *
  * bucket(r) of a relative position r = j - i, with num_buckets and max_distance:
  *   bidirectional: m = num_buckets / 2, a = |r|, and m is added for r > 0;
@@ -492,7 +494,8 @@ ENC_API enc_status enc_set_scores(enc_t h, const enc_scores* scores);
  * ENC_ERR_INVALID_ARG.  The forward, the step, and in FP16 mode the backward of
  * seq <= 128 without dtable need none.  Scratch that was ever
  * handed to a call stays allocated until enc_destroy, so that a graph captured
- * by the caller keeps valid addresses when the scratch grows later. */
+ * by the caller keeps valid addresses when the scratch grows later.  Graphs of one
+ * handle share it, as calls do: replay them on one stream, or one after the other. */
 ENC_API enc_status enc_reserve_scored(enc_t h, int batch, int seq);
 
 /* enc_op_scored_attention - one attention step with these scores:

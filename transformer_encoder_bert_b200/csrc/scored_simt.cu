@@ -17,12 +17,12 @@
 //
 // Bound by shared memory: a step of 64 FMAs reads 8 float4 (and the second
 // products as many), and short sequences by the latency of a block's few tiles.
-// Measured, FP32, 12 heads of 64, 8 sequences of 512: forward 162 us, 23 TF/s of
-// the visible pairs' products (table 191 us), backward 441 us, 21 TF/s (table 582
+// Measured, FP32, 12 heads of 64, 8 sequences of 256 to 512: forward 165 us, 23 TF/s
+// of the visible pairs' products (table 194 us), backward 444 us, 21 TF/s (table 583
 // us).  Tiles are copied under the arithmetic of the ones before (forward 186,
 // backward 549 us without), a last tile of at most 16 columns forms those alone (4
-// heads of 32, 16 sequences of 131: forward 22.6 -> 19.9 us), and the dK/dV grid
-// runs beside the dQ grid (the same sequences' backward 63.5 -> 43.1 us).
+// heads of 32, 16 sequences of up to 131, a table: forward 22.6 -> 20.3 us), and the
+// dK/dV grid runs beside the dQ grid (the same sequences' backward 63.5 -> 44.0 us).
 #include "scored.cuh"
 
 namespace enc {

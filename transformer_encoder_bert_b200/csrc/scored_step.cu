@@ -16,8 +16,10 @@
 // thread reads back only what it asked for itself, so the ring needs no barrier
 // and the next stage's loads stay in flight under the arithmetic, with three CTAs
 // of 256 threads (32 KB a stage) to an SM.  Measured at 16 heads of 64, 32
-// sequences, capacity 4096, caches half to wholly full: 85 us, 4.7 TB/s of the
-// measured 6.56 (93 us with a cap and a table); two CTAs with three stages 100 us.
+// sequences, capacity 4096, caches half to wholly full, with a cap and a table: 87
+// us, 92 with a cold L2, 4.4 TB/s of the measured 6.56; the same total in caches of
+// one length 79 us, so a third of the gap is the longest caches' clusters, which end
+// last.  Two CTAs with three stages took 100 us where this took 85.
 // The kU dot products are added up over the group by halving: each exchange
 // passes half of the rows on, so that a lane ends with the score of one row and
 // bias, cap and exponential are worked out once per row.  The group keeps a

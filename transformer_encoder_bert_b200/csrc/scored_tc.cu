@@ -32,11 +32,14 @@
 // thread has before S arrives; a warp whose rows see none of the block writes
 // P = 0 and leaves it.
 //
-// Measured, full lengths: 8 heads of 128, 37 sequences of 2048: 736 us, 864 TF/s
-// (slopes 887, table 812, cap 972 us); 16 heads of 64, 37 of 1024: 300 us, 529
-// TF/s (slopes 383, table 415, cap 442 us), where a block of 64 keys takes the three
-// tiles of an SM 2,570 cycles against 1,536 of exponentials alone: the rest is
-// loads from and stores to TMEM, the arithmetic of t and P, and waits.
+// Measured, full lengths: 8 heads of 128, 37 sequences of 2048: 731 us, 870 TF/s
+// (slopes 887, table 811, cap 967 us); 16 heads of 64, 37 of 1024: 303 us, 525
+// TF/s (slopes 386, table 404, cap 453 us), where a block of 64 keys takes the three
+// tiles of an SM some 2,600 cycles against 1,536 of exponentials alone: the rest is
+// loads from and stores to TMEM, the arithmetic of t and P, and waits.  The document
+// mask costs about as much as the blocks that it hides: 16 heads of 64, 32 sequences
+// of 256 to 512, four documents each: 82 us against 76 without, 126 against 115 with
+// a cap of 30.
 #include <cmath>
 #include <mutex>
 
@@ -125,8 +128,8 @@ struct Cfg {
 // and the row's sum.  BIAS 0: none; 1: base; 2: base + step * column; 3: from the
 // table in shared memory.  Every variant is a body of its own from the load to the store:
 // with the row in registers, each place where two ways of preparing it join costs
-// moves of the whole row (measured with heads of 64 and 1024 keys, no bias: 456 us
-// with branches inside one body, 265 us without them).
+// moves of the whole row (when the bodies were split, heads of 64 and 1024 keys, no bias:
+// 456 us with branches inside one body, 286 us with a body each).
 struct SoftmaxBlock {
   uint32_t t_s, t_p, t_o;   // TMEM addresses of the row's S, P and O
   uint32_t s_free, o_done;  // barriers: S has been read; P V is done

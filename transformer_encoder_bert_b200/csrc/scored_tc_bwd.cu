@@ -33,11 +33,12 @@
 // a block whose distances all share a bucket only adds its values up.
 //
 // Measured, full lengths, counted as five products: 8 heads of 128, 37 sequences
-// of 2048: 2.66 ms, 598 TF/s (837 as the seven that run; table 2.83, cap 2.98
-// ms); 16 heads of 64, 37 of 1024: 1.13 ms, 353 TF/s (table 1.29, cap 1.37 ms).
+// of 2048: 2.69 ms, 592 TF/s (829 as the seven that run; table 2.79, cap 3.02
+// ms); 16 heads of 64, 37 of 1024: 1.13 ms, 351 TF/s (table 1.27, cap 1.40 ms).
 // What bounds a block is the chain S and dP -> a row's arithmetic -> the products
-// -> the next S and dP in the same columns; TMEM holds no third pair of buffers
-// beside the accumulators.
+// -> the next S and dP in the same columns.  In dKV mode TMEM holds no third pair of
+// buffers beside the accumulators; in dQ mode a quarter of it and more is free, but dU
+// lies over dP there too, so the next scores wait for the product.
 #include "scored_tc.cuh"
 
 namespace enc {

@@ -33,7 +33,7 @@
 // 2,400 without the sums).
 //
 // Measured, 12 heads of 64: 64 sequences of 64 to 128 with a table 50 us against
-// 13 us of bytes; 148 full sequences of 128 58 us, 319 TF/s (table 78, cap 63 us).
+// 13 us of bytes; 148 full sequences of 128 59 us, 318 TF/s (table 80, cap 67 us).
 // Bound by an item's chain of latencies: with two items to an SM, 5,000 cycles
 // each with the table's sums, of which 630 are loads and stores at full bandwidth.
 #include "scored_tc.cuh"

@@ -20,8 +20,9 @@
 // [128, 256).  Chunks of 32 keys that no row of a warp sees cost nothing but a
 // store of zeros, and warps whose rows are all padding do no work.
 //
-// Measured: 12 heads of 64, 256 sequences of 64 to 128, a table: 42.7 us, 0.59 of
-// the measured bandwidth on its 165 MB; 148 full sequences of 128: 28 us with a
+// Measured: 12 heads of 64, 256 sequences of 64 to 128, a table: 41 us, 44 with a
+// cold L2, 0.57 of the measured bandwidth on the 165 MB of its valid rows (the boxes
+// hold 128 rows whatever n is: 201 MB move); 148 full sequences of 128: 28 us with a
 // table, 32 with a cap.  The encoder's plain attention kernel takes 40 us on the
 // data of the first.
 #include "scored_tc.cuh"
