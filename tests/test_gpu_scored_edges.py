@@ -177,9 +177,9 @@ def test_scratch_grows_by_what_is_needed_when_memory_is_short():
     enc = fresh_encoder(4, 32, "fp32")
     filler = None
     try:
+        torch.cuda.empty_cache()                              # (what other tests left in PyTorch's cache)
         free = torch.cuda.mem_get_info()[0]
         enc.reserve_scored(4096, 4096)
-        torch.cuda.empty_cache()
         held = free - torch.cuda.mem_get_info()[0]            # 0.8 GB
         assert held > 2 ** 29
         filler = torch.empty(torch.cuda.mem_get_info()[0] - held - held // 2, dtype=torch.uint8, device="cuda")
