@@ -426,3 +426,25 @@ def test_padded_rows_may_hold_anything_in_every_form(nh, d, s, valid, kind, mode
     assert torch.equal(grads[0], dirty[0])
     if grads[1] is not None:
         assert torch.isfinite(dirty[1]).all() and torch.equal(grads[1], dirty[1])
+
+
+@pytest.mark.parametrize("mode", ["fp16", "fp16-simt", "fp32"])
+@pytest.mark.parametrize("sign", [1, -1], ids=["rising", "falling"])
+@pytest.mark.parametrize("size", [5e7, 1.4e8, 1e9], ids=str)
+@pytest.mark.parametrize("d,s", [(64, 100), (64, 300), (32, 300), (128, 128), (128, 700)], ids=str)
+def test_scores_of_any_finite_size(d, s, size, sign, mode):
+    """Scores up to 10^9, further apart than their rounding: each row is its largest key's.  (Where floats are 8 or 16
+    apart, a 7 or 15 added to one becomes a factor of 2 or 256.)"""
+    c = Case("plain", mode, 2, 2, s, d, seed=38, valid=[s, s - 3])
+    c.spec.scale = float(np.float32(size / (16384 * 16 * (s // 2))))
+    c.qkv[:2] = 0
+    c.qkv[0, ..., 0] = 16384
+    c.qkv[1, ..., 0] = (sign * 16 * np.arange(-(s // 2), s - s // 2))[None, None]
+    ctx, lse = c.forward()
+    got, out = c.shaped(ctx), lse.cpu().numpy()
+    for b, n in enumerate(c.valid):
+        best = n - 1 if sign > 0 else 0
+        want = np.broadcast_to(c.qkv[2, b, :, best].astype(np.float64), (n, 2, d))
+        assert np.array_equal(got[b, :n], want)
+        top = c.spec.scale * 16384 * float(c.qkv[1, b, 0, best, 0])
+        assert (np.abs(out[b, :, :n] - top) <= 2.0 ** -22 * abs(top) + 1e-6).all()

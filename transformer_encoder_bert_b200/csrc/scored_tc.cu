@@ -14,8 +14,9 @@
 // P = 2^(t2 - m + 7) as FP16 to TMEM and adds up l in FP32.  m is a reference
 // maximum: it moves only when a block exceeds it by 2^8, and then the thread
 // scales its row of O first.  O / l does not depend on m.  The 7 uses up FP16's
-// range above 2^8: a weight below 2^-25 - 7 of the row's largest counts for
-// nothing in O, where 65,536 of them at 2^-25 would be a five-hundredth of the row.
+// range above 2^8: a weight counts for nothing in O below 2^-32 of the row's
+// largest, not already below 2^-25, where 65,536 of them would be a five-hundredth
+// of the row.
 //
 // What bounds a block is the softmax, not the products: 8 cycles of the
 // special-function unit a score and warp, and a chain of waits and dependent
@@ -207,7 +208,7 @@ __device__ __forceinline__ bool softmax_row(const ScoreArgs& s, const SoftmaxBlo
   // Until a key has been seen m_ref is -inf, and O and l are zeros.
   const bool moved = bmax > m_ref + kRescaleLog2;
   if (any_warp(moved)) {
-    const float alpha = moved ? ex2(m_ref - bmax) : 1.f;
+    const float alpha = moved ? ex2(raised(kRaiseLog2, bmax) - raised(kRaiseLog2, m_ref)) : 1.f;
     if (moved) m_ref = bmax;
     if (sb.it > 0) {
       tc_fence_after();
@@ -223,7 +224,7 @@ __device__ __forceinline__ bool softmax_row(const ScoreArgs& s, const SoftmaxBlo
     sum2 = f2_mul(sum2, f2_pack(alpha, alpha));
   }
   const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-  const float neg_m = kRaiseLog2 - mu;
+  const float neg_m = raised(kRaiseLog2, mu);
   const uint64_t neg_m2 = f2_pack(neg_m, neg_m);
 #pragma unroll
   for (int c = 0; c < BN; c += 32) {
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kCtasP
           tma_store_3d(&tm_ctx, smem_u32(out) + u * 16384 + (warp & 3) * 32 * kRowBytes, h * D + 64 * u, row0, b);
         bulk_commit_group();
       }
-      if (lse && i < S) lse[((size_t)b * NH + h) * S + i] = seen ? (log2f(l) - (kRaiseLog2 - m_ref)) * kLn2 : -INFINITY;
+      if (lse && i < S) lse[((size_t)b * NH + h) * S + i] = seen ? (log2f(l) - raised(kRaiseLog2, m_ref)) * kLn2 : -INFINITY;
       if (lane == 0) bulk_wait_group_read<0>();            // shared memory has been read
     }
   }

@@ -202,6 +202,12 @@ __device__ __forceinline__ uint64_t small_cap2(const ScoreArgs& s, uint64_t x) {
 constexpr int kPBits = 13;
 constexpr float kPScale = 1 << kPBits, kPInverse = 1.f / kPScale;
 
+// What the forward adds to t2 before the exponential: `raise` less the row's reference.  References past 2^17 do not
+// take the raise, which their rounding could multiply beyond FP16's range.
+__device__ __forceinline__ float raised(float raise, float reference) {
+  return fabsf(reference) < 131072.f ? raise - reference : -reference;
+}
+
 // What a kernel does about the cap (its template argument).
 constexpr int kNoCap = 0, kCap = 1, kLargeCap = 2;
 inline int cap_kind(const ScoreArgs& s) { return s.cap > kCapCoarse ? kLargeCap : s.cap > 0.f ? kCap : kNoCap; }

@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, SCfg<D>::kCtasPerSm)
         mx = 32 * c + 32 <= jall ? first_pass<CAP, BIAS, false>(s, ch, mx) : first_pass<CAP, BIAS, true>(s, ch, mx);
       }
       const float mu = mx == -INFINITY ? 0.f : mx;
-      const float neg_m = kRaiseLog2 - mu;
+      const float neg_m = raised(kRaiseLog2, mu);
       const uint64_t neg_m2 = f2_pack(neg_m, neg_m);
       uint64_t sum2 = 0;                                   // two partial row sums (0.0f, 0.0f)
 #pragma unroll 1
