@@ -10,7 +10,7 @@ import torch
 import encoder_inputs as EI
 from oracle import scored_oracle as SO
 from parity_utils import encoder_from_inputs, to_dev
-from test_gpu_scored import Case, encoder
+from test_gpu_scored import Case, check_backward, check_forward, encoder
 from transformer_encoder_bert_b200 import Scores
 
 pytestmark = pytest.mark.gpu
@@ -448,3 +448,16 @@ def test_scores_of_any_finite_size(d, s, size, sign, mode):
         assert np.array_equal(got[b, :n], want)
         top = c.spec.scale * 16384 * float(c.qkv[1, b, 0, best, 0])
         assert (np.abs(out[b, :, :n] - top) <= 2.0 ** -22 * abs(top) + 1e-6).all()
+
+
+@pytest.mark.parametrize("cap,std", [(100.0, 6.0), (1e4, 40.0)])
+@pytest.mark.parametrize("kind", ["cap", "cap-slopes", "cap-docs", "cap-table-one-way-causal", "cap-slopes-table-prefix-docs"])
+@pytest.mark.parametrize("nh,d,s", [(3, 64, 90), (3, 64, 300), (2, 128, 128), (2, 128, 260), (4, 32, 70), (4, 32, 200)], ids=str)
+def test_large_caps_in_every_form(nh, d, s, kind, cap, std):
+    """The kernels of caps above 64: scores from near nothing to past the cap."""
+    c = Case(kind, "fp16", 2, nh, s, d, seed=39, std=std)
+    c.spec.cap = cap
+    c.qkv[2] = (c.qkv[2] / std).astype(np.float16)
+    ctx, lse = c.forward()
+    check_forward(c, ctx, lse)
+    check_backward(c, ctx, lse, *c.backward(ctx, lse))
