@@ -33,9 +33,9 @@
 // thread has before S arrives; a warp whose rows see none of the block writes
 // P = 0 and leaves it.
 //
-// Measured, full lengths: 8 heads of 128, 37 sequences of 2048: 731 us, 870 TF/s
-// (slopes 887, table 811, cap 967 us); 16 heads of 64, 37 of 1024: 303 us, 525
-// TF/s (slopes 386, table 404, cap 453 us), where a block of 64 keys takes the three
+// Measured, full lengths: 8 heads of 128, 37 sequences of 2048: 731 to 755 us
+// between runs, 840 to 870 TF/s (slopes 890, table 805, cap 965 us); 16 heads of 64,
+// 37 of 1024: 300 us, 530 TF/s (slopes 385, table 401, cap 450 us), where a block of 64 keys takes the three
 // tiles of an SM some 2,600 cycles against 1,536 of exponentials alone: the rest is
 // loads from and stores to TMEM, the arithmetic of t and P, and waits.  The document
 // mask costs about as much as the blocks that it hides: 16 heads of 64, 32 sequences
